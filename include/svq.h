@@ -348,6 +348,105 @@ int svq_w8a16_gemm(const void *x, const int8_t *w, const void *scales, void *out
 /* Name of the kernel svq_w8a16_gemm would launch (static text), or NULL. */
 const char *svq_w8a16_kernel_name(int64_t M, int64_t N, int64_t K, int32_t group_size);
 
+/* ---- per-request operators of a verify chunk ------------------------------------ */
+
+/* Largest rank of svq_adapter_add. */
+#define SVQ_MAX_ADAPTER_RANK 256
+
+/* Workspace bytes needed by svq_adapter_add (never 0); (size_t)-1 if the
+ * arguments are invalid. */
+size_t svq_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t slots);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that they
+ * share: y = base is the output of any of the GEMMs above for the same x, and
+ * every row adds its own adapter's product,
+ *     out[m] = base[m] + scales[s] * B_s (A_s x[m]),   s = rows[m].
+ * A row whose index is outside [0, slots) has no adapter: out[m] = base[m].
+ * Products and sums are fp32 (the rank-R intermediate enters the second product
+ * with 16 significant bits), out is rounded to bf16 (nearest even) once. Rows
+ * are independent: no row's result depends on another row or on an adapter that
+ * is not its own.
+ *   base     bf16 [M][ld_base], the first N columns of each row; 16-byte aligned
+ *   x        bf16 [M][K], 16-byte aligned
+ *   a        bf16 [slots][R][K], 16-byte aligned, finite (any size: 64-bit offsets)
+ *   b        bf16 [slots][N][R], 16-byte aligned, finite
+ *   rows     int32 [M], the adapter of each row
+ *   scales   fp32 [slots]
+ *   out      bf16 [M][ld_out], 16-byte aligned; its first N columns are written,
+ *            the rest of each row is left as it was. May be base itself (same
+ *            pointer, ld_out == ld_base); otherwise the two must not overlap.
+ *   ld_base, ld_out >= N, multiples of 8: the columns of one projection inside a
+ *            fused output are addressed by their first column and the fused width
+ * Requires N % 16 == 0, K % 128 == 0, R % 8 == 0, R <= SVQ_MAX_ADAPTER_RANK.
+ * An adapter of a smaller rank is padded with zero rows of A and zero columns of B.
+ *   workspace  at least svq_adapter_workspace_bytes(...) bytes, 256-byte aligned;
+ *              it need not be cleared, and a workspace of the GEMMs may be passed
+ *              (its arrival counters are left alone). Calls that share a workspace
+ *              must be stream-ordered.
+ */
+int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void *a, const void *b,
+                    const int32_t *rows, const float *scales, void *out, int64_t ld_out, int64_t M, int64_t N,
+                    int64_t K, int32_t R, int32_t slots, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes needed by svq_sample; 0 if none, (size_t)-1 if invalid. */
+size_t svq_sample_workspace_bytes(int64_t M, int64_t V);
+
+/*
+ * One token per row of logits, as a vocabulary head writes them, from given
+ * random numbers. A row's tokens stand in order of descending logit, equal ones
+ * by ascending index (-0 equals +0). With w(i) = exp((l_i - max) / T) and W(n)
+ * the sum of the first n:
+ *     n1 = top_k tokens (all if top_k <= 0)
+ *     n2 = the fewest tokens with W(n2) >= top_p W(n1)   (no limit if top_p >= 1)
+ *     n3 = the tokens with w >= min_p                    (no limit if min_p <= 0)
+ *     n  = the least of these, at least 1
+ *     token = the first whose W, itself included, exceeds u W(n)
+ *     logprob = ln of the probability of that token among the n
+ * Weights and sums are fp64. temperature <= 0 (or NaN) takes the first token,
+ * with logprob 0, whatever the other parameters. Logits that are NaN or -inf are
+ * never drawn; among +inf ones the draw is uniform. A row with nothing to draw
+ * gives token -1 and logprob -inf. u is clamped to [0, 1), NaN to 0.
+ *   logits       bf16 [M][ld], the first V of each row; 2-byte aligned (rows of
+ *                any alignment; 16-byte aligned rows are not faster)
+ *   u            fp32 [M]
+ *   temperature  fp32 [M], or NULL for 1
+ *   top_k        int32 [M], or NULL for no limit
+ *   top_p, min_p fp32 [M], or NULL for no limit
+ *   tokens       int32 [M]
+ *   logprobs     fp32 [M], or NULL
+ * Requires ld >= V; the logits may pass 2 GiB. Outputs must not overlap each
+ * other, the inputs or the workspace (svq_sample_workspace_bytes(...) bytes,
+ * 256-byte aligned, as for svq_adapter_add; NULL/0 when 0 bytes are needed).
+ */
+int svq_sample(const void *logits, int64_t ld, const float *u, const float *temperature, const int32_t *top_k,
+               const float *top_p, const float *min_p, int32_t *tokens, float *logprobs, int64_t M, int64_t V,
+               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Acceptance of drafted tokens (Eole recipe, opening paragraph: the main model
+ * verifies a chunk of drafted tokens). Sequence s owns rows starts[s] ..
+ * starts[s+1] - 1 of the chunk: the first row's input is its last committed
+ * token, the others' inputs are its drafts. tokens are what the main model
+ * sampled at each row (svq_sample). A draft is accepted if it and all drafts
+ * before it equal the token sampled one row earlier:
+ *     n    = number of leading rows i with tokens[i] == inputs[i + 1]
+ *     next = tokens[starts[s] + n], the token that follows the accepted drafts
+ * For drafts that are given tokens this is speculative sampling: drawing t from
+ * p and accepting a draft d when t == d accepts with probability p(d), and
+ * otherwise t is distributed as p without d.
+ *   tokens, inputs  int32 [M]; a negative token (nothing to draw) accepts nothing
+ *   starts          int32 [S + 1], ascending, in [0, M] (values outside are clamped
+ *                   to it); a sequence may be empty
+ *   accepted, next  int32 [S]; an empty sequence gets 0 and -1
+ *   committed       int32 [M]: the accepted drafts and then next at the first
+ *                   n + 1 rows of each sequence, -1 at its other rows and at rows
+ *                   outside every sequence
+ * Outputs must not overlap the inputs or each other.
+ */
+int svq_accept_drafts(const int32_t *tokens, const int32_t *inputs, const int32_t *starts, int32_t *accepted,
+                      int32_t *next, int32_t *committed, int64_t M, int64_t S, void *stream);
+
 /* ---- format-generic queries ---------------------------------------------------- */
 
 /* Workspace bytes the GEMM of `op` (an svq_op) needs with its automatic kernel

@@ -24,7 +24,8 @@ __all__ = [
     "EXPORTED_SYMBOLS", "rtn_quantize", "w8a16_gemm", "w8a16_workspace_bytes", "w8a16_kernel_name",
     "fuse_projections", "fuse_or_keep", "ct_to_gptq", "MAX_FUSED_PARTS", "mxfp8_quantize",
     "OP_W4A16", "OP_MXFP8", "OP_W8A16", "workspace_bytes", "kernel_name",
-    "launch_geometry", "stream_probe",
+    "launch_geometry", "stream_probe", "adapter_add", "adapter_workspace_bytes", "sample",
+    "sample_workspace_bytes", "accept_drafts", "MAX_ADAPTER_RANK",
 ]
 
 KERNEL_AUTO, KERNEL_DOT2, KERNEL_MFMA_SKINNY, KERNEL_MFMA_WIDE = 0, 1, 2, 3
@@ -40,12 +41,14 @@ EXPORTED_SYMBOLS = (
     "svq_w8a16_workspace_bytes", "svq_w8a16_gemm", "svq_w8a16_kernel_name",
     "svq_fuse_projections", "svq_ct_to_gptq", "svq_mxfp8_quantize", "svq_workspace_bytes",
     "svq_kernel_name", "svq_launch_geometry", "svq_stream_probe", "svq_mfma_probe", "svq_mxfp8_repack",
-    "svq_w4a16_gemm_noalloc",
+    "svq_w4a16_gemm_noalloc", "svq_adapter_workspace_bytes", "svq_adapter_add",
+    "svq_sample_workspace_bytes", "svq_sample", "svq_accept_drafts",
 )
 
 OP_W4A16, OP_MXFP8, OP_W8A16 = 1, 2, 3
 
 MAX_FUSED_PARTS = 16
+MAX_ADAPTER_RANK = 256
 
 _i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 _lib = None
@@ -124,6 +127,16 @@ def lib():
         L.svq_mfma_probe.argtypes = [ctypes.c_uint32, ctypes.c_uint32, ctypes.c_uint32, _i32, _p, _p]
         L.svq_w4a16_gemm_noalloc.restype = ctypes.c_int
         L.svq_w4a16_gemm_noalloc.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p]
+        L.svq_adapter_workspace_bytes.restype = _sz
+        L.svq_adapter_workspace_bytes.argtypes = [_i64, _i64, _i64, _i32, _i32]
+        L.svq_adapter_add.restype = ctypes.c_int
+        L.svq_adapter_add.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32, _i32, _p, _sz, _p]
+        L.svq_sample_workspace_bytes.restype = _sz
+        L.svq_sample_workspace_bytes.argtypes = [_i64, _i64]
+        L.svq_sample.restype = ctypes.c_int
+        L.svq_sample.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _p, _sz, _p]
+        L.svq_accept_drafts.restype = ctypes.c_int
+        L.svq_accept_drafts.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _p]
         _lib = L
         return L
 
@@ -515,3 +528,165 @@ def ct_to_gptq(weight_packed, weight_scale, group_size=128, qweight=None, scales
                                 _dev_ptr(qweight, "qweight"), _dev_ptr(scales, "scales"), N, K, group_size,
                                 _stream_ptr(weight_packed)), "svq_ct_to_gptq")
     return qweight, scales
+
+
+# ---- per-request operators of a verify chunk ----------------------------------------
+
+def _typed(t, name, kinds, shape, device):
+    """Device pointer of a contiguous tensor of one of the dtypes `kinds`, of the
+    given shape, on `device`."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in kinds:
+        raise TypeError(f"{name} must be {' or '.join(str(k) for k in kinds)}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return _dev_ptr(t, name)
+
+
+def _row_matrix(t, name, kinds):
+    """(pointer, row stride) of a matrix whose rows are contiguous and apart."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    if t.dtype not in kinds:
+        raise TypeError(f"{name} must be {' or '.join(str(k) for k in kinds)}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _bf16_kinds():
+    torch = _torch()
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _scratch(nbytes, workspace, device):
+    """(pointer, bytes) of the caller's workspace, or of one from PyTorch's allocator
+    on the current stream: it need not be cleared, no other call shares it, and a
+    call that is captured gets its own from the graph's pool. Also returns the
+    tensor, which the caller keeps until the launch is enqueued."""
+    torch = _torch()
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def adapter_workspace_bytes(M, N, K, R, slots) -> int:
+    v = lib().svq_adapter_workspace_bytes(M, N, K, R, slots)
+    if v == ctypes.c_size_t(-1).value:
+        raise SvqError(10, "svq_adapter_workspace_bytes")
+    return v
+
+
+def adapter_add(base, x, a, b, rows, scales, out=None, workspace=None):
+    """base [M, N] + scales[s] * B_s (A_s x[m]) for the adapter s = rows[m] of each row.
+
+    base is a projection's output for x [M, K]; a [slots, R, K] and b [slots, N, R]
+    hold the adapters, all bf16; rows int32 [M] (an index outside [0, slots): no
+    adapter), scales float32 [slots]. base and out may be column slices of wider
+    matrices, and out may be base itself.
+    """
+    torch = _torch()
+    kinds = _bf16_kinds()
+    base_ptr, ld_base = _row_matrix(base, "base", kinds)
+    dev = base.device
+    M, N = base.shape
+    if x.dim() != 2 or a.dim() != 3:
+        raise ValueError("x must be [M, K] and a [slots, R, K]")
+    K = x.shape[1]
+    slots, R = a.shape[0], a.shape[1]
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out_ptr, ld_out = _row_matrix(out, "out", kinds)
+        if tuple(out.shape) != (M, N) or out.device != dev:
+            raise ValueError(f"out must have shape {(M, N)} on {dev}")
+        nbytes = adapter_workspace_bytes(M, N, K, R, slots)
+        ws_ptr, ws_bytes, keep = _scratch(nbytes, workspace, dev)
+        _check(lib().svq_adapter_add(base_ptr, ld_base, _typed(x, "x", kinds, (M, K), dev),
+                                     _typed(a, "a", kinds, (slots, R, K), dev),
+                                     _typed(b, "b", kinds, (slots, N, R), dev),
+                                     _typed(rows, "rows", (torch.int32,), (M,), dev),
+                                     _typed(scales, "scales", (torch.float32,), (slots,), dev), out_ptr, ld_out,
+                                     M, N, K, R, slots, ws_ptr, ws_bytes, _stream_ptr(base)), "svq_adapter_add")
+    return out
+
+
+def sample_workspace_bytes(M, V) -> int:
+    v = lib().svq_sample_workspace_bytes(M, V)
+    if v == ctypes.c_size_t(-1).value:
+        raise SvqError(2, "svq_sample_workspace_bytes")
+    return v
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, workspace=None):
+    """One token per row of bf16 logits [M, V] from random numbers u float32 [M] in [0, 1).
+
+    temperature, top_p, min_p float32 [M] and top_k int32 [M], each row its own, or
+    None. Returns (tokens int32 [M], logprobs float32 [M]): temperature first, then
+    top-k, top-p (of what top-k leaves) and min-p (against the likeliest token);
+    temperature <= 0 is greedy. A row with nothing to draw gives -1 and -inf. logits
+    may be a column slice of a wider matrix.
+    """
+    torch = _torch()
+    ptr, ld = _row_matrix(logits, "logits", _bf16_kinds())
+    dev = logits.device
+    M, V = logits.shape
+    f32, i32 = (torch.float32,), (torch.int32,)
+
+    def per_row(t, name, kinds):
+        return None if t is None else _typed(t, name, kinds, (M,), dev)
+
+    with torch.cuda.device(dev):
+        nbytes = sample_workspace_bytes(M, V)
+        tokens = torch.empty(M, dtype=torch.int32, device=dev)
+        logprobs = torch.empty(M, dtype=torch.float32, device=dev)
+        ws_ptr, ws_bytes, keep = _scratch(nbytes, workspace, dev)
+        _check(lib().svq_sample(ptr, ld, _typed(u, "u", f32, (M,), dev), per_row(temperature, "temperature", f32),
+                                per_row(top_k, "top_k", i32), per_row(top_p, "top_p", f32),
+                                per_row(min_p, "min_p", f32), _dev_ptr(tokens, "tokens"),
+                                _dev_ptr(logprobs, "logprobs"), M, V, ws_ptr, ws_bytes, _stream_ptr(logits)),
+               "svq_sample")
+    return tokens, logprobs
+
+
+def accept_drafts(tokens, inputs, starts):
+    """Accepts drafted tokens against the main model's samples.
+
+    tokens, inputs int32 [M]: the sample and the input of each row of a verify chunk;
+    starts int32 [S + 1]: sequence s owns rows starts[s] .. starts[s + 1] - 1, the
+    inputs after its first row are its drafts. Returns (accepted [S], next [S],
+    committed [M]), int32: the number of accepted drafts, the token that follows
+    them, and both in place, -1 elsewhere.
+    """
+    torch = _torch()
+    i32 = (torch.int32,)
+    if tokens.dim() != 1 or starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("tokens must be [M] and starts [S + 1] with S >= 1")
+    dev, M, S = tokens.device, tokens.shape[0], starts.shape[0] - 1
+    tp = _typed(tokens, "tokens", i32, (M,), dev)
+    ip, sp = _typed(inputs, "inputs", i32, (M,), dev), _typed(starts, "starts", i32, (S + 1,), dev)
+    with torch.cuda.device(dev):
+        accepted = torch.empty(S, dtype=torch.int32, device=dev)
+        following = torch.empty(S, dtype=torch.int32, device=dev)
+        committed = torch.empty(M, dtype=torch.int32, device=dev)
+        _check(lib().svq_accept_drafts(tp, ip, sp, _dev_ptr(accepted, "accepted"), _dev_ptr(following, "next"),
+                                       _dev_ptr(committed, "committed"), M, S, _stream_ptr(tokens)),
+               "svq_accept_drafts")
+    return accepted, following, committed

@@ -1,0 +1,258 @@
+// Low-rank adapters of many requests beside a shared projection (svq_adapter_add):
+//
+//   t[m]   = A_s x[m]                      s = rows[m], fp32
+//   out[m] = bf16(base[m] + scale[s] * B_s t[m])
+//
+// and out[m] = base[m] where rows[m] names no adapter. Two launches:
+//
+// 1. down: t, split over K. A workgroup takes 16 rows, up to 64 ranks, one range
+//    of K and one of the adapters that occur among its rows; its 8 waves take the
+//    range's 128-element tiles round-robin (x and A are both K-major, so MFMA
+//    operands are loaded straight from memory, 64 contiguous bytes a row per
+//    instruction) and meet in LDS. Rows of other adapters in the tile ride along
+//    and are not stored: an output element depends on its own row of x and on its
+//    own adapter only, so one request's infinities or NaN never reach another.
+// 2. up: a wave takes 64 columns of those 16 rows; B is the MFMA's A operand, so
+//    a lane ends up with 16 consecutive columns of one row and reads base and
+//    writes out in 16-byte pieces. The K ranges of t are summed in a fixed order.
+//
+// t stays fp32 up to the second product, whose bf16 operand is scale * t split in
+// two (high and low halves, 16 significant bits): rounding it to one bf16 would put
+// an error of the size of the output's own rounding on the sum. MFMA time is idle
+// here: the bound is the bytes of A, B, base and out (or, for a few rows, latency).
+#include <algorithm>
+
+#include "svq_launch.h"
+
+namespace svq {
+
+namespace {
+
+constexpr int kDownWaves = 8;
+constexpr int kUpWaves = 4;
+
+// The adapter of lane l's row (row l % 16 of the tile): -1 for none, -2 past the end.
+__device__ __forceinline__ int tile_slot(const int32_t *rows, int64_t row0, int64_t M, int slots, int lane) {
+    const int64_t m = row0 + (lane & 15);
+    if (m >= M) return -2;
+    const int s = rows[m];
+    return (uint32_t)s < (uint32_t)slots ? s : -1;
+}
+
+// Lanes (of the first 16) whose row is the tile's first one with its adapter.
+__device__ __forceinline__ uint32_t tile_leaders(int slot, int lane, bool with_bare) {
+    bool first = lane < 16 && (slot >= 0 || (with_bare && slot == -1));
+#pragma unroll
+    for (int j = 0; j < 15; ++j)
+        if (__builtin_amdgcn_readlane(slot, j) == slot && j < lane) first = false;
+    return (uint32_t)__ballot(first);
+}
+
+// RT rank tiles of 16 per workgroup.
+template <int RT>
+__global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
+    const uint16_t *__restrict__ x, const uint16_t *__restrict__ a, const int32_t *__restrict__ rows,
+    float *__restrict__ part, int64_t M, int K, int R, int slots, int ways, int rank_chunks, int splits, int T) {
+    __shared__ f32x4 red[kDownWaves][RT][64];
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r = lane & 15, g = lane >> 4;
+    int b = blockIdx.x;
+    const int ks = b % splits;
+    b /= splits;
+    const int rc = b % rank_chunks;
+    b /= rank_chunks;
+    const int way = b % ways;
+    const int64_t row0 = (int64_t)(b / ways) * 16;
+    const int slot = tile_slot(rows, row0, M, slots, lane);
+    uint32_t leaders = tile_leaders(slot, lane, false);
+    const int KT = K >> 7, kend = min(KT, (ks + 1) * T);
+    const int64_t xrow = min(row0 + r, M - 1);
+    const uint16_t *xp = x + xrow * K + 8 * g;
+    const int rank0 = rc * 16 * RT;
+
+    for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
+        if (ord % ways != way) continue;
+        const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
+        const uint16_t *ap[RT];
+        bool in[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int rank = rank0 + 16 * i + r;
+            in[i] = rank < R;  // ranks past R: no load, a zero operand
+            ap[i] = a + ((int64_t)s * R + min(rank, R - 1)) * K + 8 * g;
+        }
+        f32x4 acc[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int kt = ks * T + wave; kt < kend; kt += kDownWaves) {
+            uint4 xv[4], av[RT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xv[j] = *(const uint4 *)(xp + kt * 128 + 32 * j);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    av[i][j] = in[i] ? *(const uint4 *)(ap[i] + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i] = mfma16x16x32(xv[j], av[i][j], acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
+        __syncthreads();
+        // rank tile `wave` (for RT > 8 there would be more tiles than waves)
+        static_assert(RT <= kDownWaves, "one wave sums one rank tile");
+        if (wave < RT) {
+            f32x4 sum = red[0][wave][lane];
+#pragma unroll
+            for (int w = 1; w < kDownWaves; ++w) sum += red[w][wave][lane];
+            const int rank = rank0 + 16 * wave + r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rs = __shfl(slot, 4 * g + i);
+                if (rs == s && rank < R) part[((int64_t)ks * M + row0 + 4 * g + i) * R + rank] = sum[i];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// NS: 32-rank steps.
+template <int NS>
+__global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
+    const uint16_t *base, const float *__restrict__ part, const uint16_t *__restrict__ b,
+    const int32_t *__restrict__ rows, const float *__restrict__ scales, uint16_t *out, int64_t M, int N, int R,
+    int slots, int64_t ld_base, int64_t ld_out, int ways, int col_groups, int splits) {
+    constexpr int kPitch = 32 * NS + 8;  // bf16 elements: rows 16 bytes apart in banks
+    __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r = lane & 15, g = lane >> 4;
+    int blk = blockIdx.x;
+    const int cg = blk % col_groups;
+    blk /= col_groups;
+    const int way = blk % ways;
+    const int64_t row0 = (int64_t)(blk / ways) * 16;
+    const int slot = tile_slot(rows, row0, M, slots, lane);
+    uint32_t leaders = tile_leaders(slot, lane, true);
+    const int col0 = (cg * kUpWaves + wave) * 64;
+    const int col = col0 + 16 * g;       // this lane's 16 output columns
+    const int64_t m = row0 + r;          // and its row
+
+    for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
+        if (ord % ways != way) continue;
+        const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
+        const bool mine = slot == s && col < N;
+        uint4 y[2];
+        if (s < 0) {  // rows without an adapter
+            if (mine && (const uint16_t *)out != base) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *(uint4 *)(out + m * ld_out + col + 8 * h) = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+            }
+            continue;
+        }
+        // scale * t of this adapter's rows, rounded in two halves
+        const float scale = scales[s];
+        for (int i = threadIdx.x; i < 16 * 32 * NS; i += 64 * kUpWaves) {
+            const int row = i / (32 * NS), rank = i % (32 * NS);
+            float t = 0.f;
+            if (rank < R && row0 + row < M && rows[row0 + row] == s) {
+                const float *p = part + (row0 + row) * R + rank;
+                for (int ks = 0; ks < splits; ++ks) t += p[(int64_t)ks * M * R];
+                t *= scale;
+            }
+            const uint16_t hi = f32_to_bf16_rne(t);
+            const float rest = t - bits_f32((uint32_t)hi << 16);
+            thi[row][rank] = hi;
+            tlo[row][rank] = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(rest);
+        }
+        f32x4 acc[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (mine) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            const uint4 hi = *(const uint4 *)&thi[r][32 * st + 8 * g], lo = *(const uint4 *)&tlo[r][32 * st + 8 * g];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                // MFMA row 4 g' + i of product q is column 16 g' + 4 q + i
+                const int n = col0 + 16 * (r >> 2) + 4 * q + (r & 3), rank = 32 * st + 8 * g;
+                uint4 bv = make_uint4(0, 0, 0, 0);
+                if (n < N && rank < R) bv = *(const uint4 *)(b + ((int64_t)s * N + n) * R + rank);
+                acc[q] = mfma16x16x32(bv, hi, acc[q]);
+                acc[q] = mfma16x16x32(bv, lo, acc[q]);
+            }
+        }
+        if (mine) {
+            uint32_t o[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const uint32_t v = (&y[w >> 2].x)[w & 3];
+                const float lo = bits_f32(v << 16) + acc[w >> 1][2 * (w & 1)];
+                const float hi = bits_f32(v & 0xFFFF0000u) + acc[w >> 1][2 * (w & 1) + 1];
+                o[w] = (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
+            }
+            *(uint4 *)(out + m * ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(uint4 *)(out + m * ld_out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+AdapterPlan plan_adapter(int64_t M, int64_t K, int64_t R, int64_t slots) {
+    AdapterPlan p{};
+    p.row_tiles = (M + 15) / 16;
+    // adapters of one tile side by side while tiles alone do not fill the chip
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(M, 16), slots);
+    p.ways = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / p.row_tiles));
+    p.rank_tiles = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
+    p.rank_chunks = (int)((R + 16 * p.rank_tiles - 1) / (16 * p.rank_tiles));
+    const int64_t KT = K / 128, most_splits = (KT + kDownWaves - 1) / kDownWaves;
+    const int64_t groups = p.row_tiles * p.rank_chunks;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most_splits, (512 + groups - 1) / groups));
+    p.tiles_per_split = (int)((KT + want - 1) / want);
+    p.splits = (int)((KT + p.tiles_per_split - 1) / p.tiles_per_split);
+    p.workspace_bytes = kCounterBytes + (size_t)p.splits * M * R * 4;
+    return p;
+}
+
+hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld_base, const void *x, const void *a,
+                              const void *b, const int32_t *rows, const float *scales, void *out, int64_t ld_out,
+                              int64_t M, int64_t N, int64_t K, int R, int slots, void *workspace,
+                              hipStream_t stream) {
+    float *part = (float *)ws_partials(workspace);
+    const dim3 down((uint32_t)(p.row_tiles * p.ways * p.rank_chunks * p.splits));
+#define SVQ_DOWN(RT)                                                                                                 \
+    hipLaunchKernelGGL((adapter_down_kernel<RT>), down, dim3(64 * kDownWaves), 0, stream, (const uint16_t *)x,       \
+                       (const uint16_t *)a, rows, part, M, (int)K, R, slots, p.ways, p.rank_chunks, p.splits,        \
+                       p.tiles_per_split)
+    if (p.rank_tiles == 1) SVQ_DOWN(1);
+    else if (p.rank_tiles == 2) SVQ_DOWN(2);
+    else SVQ_DOWN(4);
+#undef SVQ_DOWN
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int col_groups = (int)((N + 64 * kUpWaves - 1) / (64 * kUpWaves));
+    // one way more than adapters: rows without one are a group of their own
+    const int ways = (int)std::min<int64_t>(p.ways == 1 ? 1 : p.ways + 1, 16);
+    const dim3 up((uint32_t)(p.row_tiles * ways * col_groups));
+#define SVQ_UP(NS)                                                                                                  \
+    hipLaunchKernelGGL((adapter_up_kernel<NS>), up, dim3(64 * kUpWaves), 0, stream, (const uint16_t *)base, part,   \
+                       (const uint16_t *)b, rows, scales, (uint16_t *)out, M, (int)N, R, slots, ld_base, ld_out,    \
+                       ways, col_groups, p.splits)
+    if (R <= 32) SVQ_UP(1);
+    else if (R <= 64) SVQ_UP(2);
+    else if (R <= 128) SVQ_UP(4);
+    else SVQ_UP(8);
+#undef SVQ_UP
+    return hipGetLastError();
+}
+
+}  // namespace svq
