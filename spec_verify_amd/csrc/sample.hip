@@ -12,15 +12,17 @@
 // A token is a whole number, so W must not depend on rounding: fp64 sums. What
 // makes that cheap is that bf16 logits take few different values. The kernel never
 // sorts: it counts values (a histogram in LDS, exact and independent of the order
-// of its atomics), which orders them, and takes one fp64 exponential per occurring
-// value instead of one per token. The position then names a value and an ordinal
-// among its equals, and a scan of the row finds that occurrence.
+// of its atomics), which orders them, and takes fp64 exponentials per occurring
+// value instead of per token. The position then names a value and an ordinal among
+// its equals, and a scan of the row finds that occurrence.
 //
 // Values are binned by their bf16 pattern: magnitudes in [2^-16, 2^16) of either
-// sign are 8192 bins; zero has one; smaller magnitudes (a logit in 10^4) go to a
-// list that is ordered by comparison. A row with more than kSideMax of those, or
-// with a larger magnitude, is counted the long way: four windows of 16384 patterns
-// each, one scan of the row per window and step.
+// sign are 8192 bins, 8 consecutive ones per thread. Eight consecutive patterns lie
+// in one binade, so their weights are a geometric series: two exponentials a thread
+// (the first occurring value's and the ratio) give all eight. Zero, up to kSideMax
+// smaller magnitudes (a logit or two in a vocabulary) and one pattern below -2^16
+// (a mask value) are items of their own. Any other row is counted the long way:
+// eight windows of 8192 patterns, one scan of the row per window and step.
 #include <algorithm>
 
 #include "svq_launch.h"
@@ -31,12 +33,14 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr uint32_t kBinsHalf = 4096;        // 32 exponents x 128 mantissas
-constexpr uint32_t kBins = 2 * kBinsHalf;   // positive descending, then negative descending
-constexpr uint32_t kMagLo = 111u << 7;      // pattern of 2^-16
-constexpr uint32_t kSideMax = kThreads - 1; // and one entry for zero
-constexpr uint32_t kWindow = 16384;         // patterns per window of the long way
-constexpr int kWindows = 4;
+constexpr uint32_t kBinsHalf = 4096;         // 32 exponents x 128 mantissas of one sign
+constexpr uint32_t kBins = 2 * kBinsHalf;    // of raw index sign << 12 | (magnitude - kMagLo)
+constexpr int kOwn = kBins / kThreads;       // bins of a thread
+constexpr uint32_t kMagLo = 111u << 7;       // pattern of 2^-16
+constexpr uint32_t kSideMax = 64;            // smaller magnitudes; zero and the low pattern are two more items
+constexpr int kItems = kSideMax + 2;
+constexpr int kWindows = 65536 / kBins;
+constexpr int kLastPositive = kThreads / 2 - 1;  // its bins are followed by the side items
 
 // ---- a row of logits -------------------------------------------------------------
 
@@ -59,30 +63,36 @@ __device__ __forceinline__ Row make_row(const uint16_t *p, int V) {
 
 __device__ __forceinline__ uint4 row_vec(const Row &r, int v) { return *(const uint4 *)(r.p + r.head + (int64_t)v * 8); }
 
-// Calls f(bits) for every element of vectors [vb, ve), and of the head and the tail
-// where asked; any order.
-template <typename F>
-__device__ __forceinline__ void for_elements(const Row &r, int vb, int ve, bool head, bool tail, F f) {
+// Calls pair(word) for every two elements of vectors [vb, ve), and single(bits) for those
+// of the head and the tail where asked; any order.
+template <typename F, typename G>
+__device__ __forceinline__ void for_elements(const Row &r, int vb, int ve, bool head, bool tail, F pair, G single) {
     const int t = threadIdx.x;
-    auto vec = [&](uint4 q) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t u = (&q.x)[w];
-            f(u & 0xFFFFu);
-            f(u >> 16);
-        }
-    };
     int v = vb + t;
     for (; v + 3 * kThreads < ve; v += 4 * kThreads) {
         uint4 q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = row_vec(r, v + i * kThreads);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vec(q[i]);
+        for (int i = 0; i < 4; ++i) {
+            pair(q[i].x);
+            pair(q[i].y);
+            pair(q[i].z);
+            pair(q[i].w);
+        }
     }
-    for (; v < ve; v += kThreads) vec(row_vec(r, v));
-    if (head && t < r.head) f(r.p[t]);
-    if (tail && t >= 64 && t < 64 + r.tail) f(r.p[r.head + 8 * r.nvec + t - 64]);
+    for (; v < ve; v += kThreads) {
+        const uint4 q = row_vec(r, v);
+        pair(q.x);
+        pair(q.y);
+        pair(q.z);
+        pair(q.w);
+    }
+    // one wave takes both ends
+    int at = -1;
+    if (head && t < r.head) at = t;
+    if (tail && t >= 8 && t < 8 + r.tail) at = r.head + 8 * r.nvec + t - 8;
+    if (at >= 0) single(r.p[at]);
 }
 
 // ---- patterns, order and weights ---------------------------------------------------
@@ -92,25 +102,22 @@ __device__ __forceinline__ uint32_t key_of(uint32_t b) {
     if (b == 0x8000u) b = 0;
     return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
 }
-__device__ __forceinline__ uint32_t bits_of(uint32_t key) { return (key & 0x8000u) ? (key & 0x7FFFu) : (~key & 0xFFFFu); }
 // NaN and -inf are never drawn: finite values and +inf have keys in [0x80, 0xFF80].
 __device__ __forceinline__ bool key_valid(uint32_t key) { return key - 0x80u <= 0xFF00u; }
 __device__ __forceinline__ double value_of(uint32_t bits) { return (double)bits_f32(bits << 16); }
-
-__device__ __forceinline__ uint32_t bin_bits(uint32_t bin) {
-    return bin < kBinsHalf ? kMagLo + (kBinsHalf - 1 - bin) : (0x8000u | (kMagLo + (bin - kBinsHalf)));
-}
+// Raw bin index <-> place in descending order (an involution).
+__device__ __forceinline__ uint32_t bin_order(uint32_t bin) { return bin < kBinsHalf ? kBinsHalf - 1 - bin : bin; }
 
 struct Weight {
     double max, inv_t;
     __device__ __forceinline__ double exponent(uint32_t bits) const {
-        const double d = value_of(bits) - max;
-        return value_of(bits) == max ? 0.0 : d * inv_t;  // also for max = +inf
+        const double v = value_of(bits);
+        return v == max ? 0.0 : (v - max) * inv_t;
     }
     __device__ __forceinline__ double operator()(uint32_t bits) const {
-        const double d = value_of(bits) - max;
-        if (value_of(bits) == max) return 1.0;
-        return d < -1.0e300 ? 0.0 : exp(d * inv_t);  // finite below an infinite maximum: 0, whatever T
+        const double v = value_of(bits), d = v - max;
+        // below an infinite maximum: 0, whatever T
+        return v == max ? 1.0 : (d < -1.0e300 ? 0.0 : exp(d * inv_t));
     }
 };
 
@@ -130,341 +137,415 @@ __device__ __forceinline__ uint32_t limit_of(const Params &p, int64_t m) {
 
 struct Hist {
     uint32_t bin[kBins];
-    uint32_t side[kSideMax + 1];        // patterns of tiny magnitudes
-    uint32_t side_n, zeros, odd;        // odd: the row needs the long way
+    uint32_t side[kSideMax];
+    uint32_t side_n, zeros, odd;  // odd: the row needs the long way
+    uint32_t low_n, low_bits;     // tokens of the one pattern at or below -2^16
 };
 
 __device__ __forceinline__ void hist_clear(Hist &h) {
     for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) h.side_n = h.zeros = h.odd = 0;
+    if (threadIdx.x == 0) h.side_n = h.zeros = h.odd = h.low_n = h.low_bits = 0;
 }
 
-__device__ __forceinline__ void hist_add(Hist &h, uint32_t b) {
-    const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
-    if (q < kBinsHalf) {
-        atomicAdd(&h.bin[(b & 0x8000u) ? kBinsHalf + q : kBinsHalf - 1 - q], 1u);
-    } else if (mag == 0) {
-        atomicAdd(&h.zeros, 1u);
-    } else if (mag < kMagLo) {
-        const uint32_t at = atomicAdd(&h.side_n, 1u);
-        if (at < kSideMax) h.side[at] = b;
-    } else if (mag <= 0x7F80u && b != 0xFF80u) {
-        h.odd = 1;
-    }
+// A token count for one pattern at or below -2^16; a second such pattern makes the row odd.
+__device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
+    const uint32_t was = atomicCAS(&h.low_bits, 0u, bits);
+    if (was != 0 && was != bits) h.odd = 1;
+    atomicAdd(&h.low_n, n);
 }
 
-// ---- block scans ----------------------------------------------------------------------
-
-struct Scratch {
-    double wsum[kWaves][4];
-    uint32_t csum[kWaves][4];
-    uint32_t sel[8];
-    double val[4];
-    uint32_t count[kWaves + 1];
-};
-
-// Exclusive prefix over the segments in order, threads in order within a segment,
-// of local sums c[S] and w[S]; the totals go to tc, tw. Fixed order of additions.
-template <int S>
-__device__ __forceinline__ void order_scan(Scratch &sc, const uint32_t (&c)[S], const double (&w)[S],
-                                           uint32_t (&ec)[S], double (&ew)[S], uint32_t &tc, double &tw) {
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    uint32_t ic[S];
-    double iw[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        ic[s] = c[s];
-        iw[s] = w[s];
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint32_t pc = __shfl_up(ic[s], d);
-            const double pw = __shfl_up(iw[s], d);
-            if (lane >= d) {
-                ic[s] += pc;
-                iw[s] += pw;
-            }
+// Counts vectors [vb, ve) of a row. Two elements at a time: subtracting kMagLo from both
+// halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14 say that
+// the magnitude has a bin (9 vector instructions and 2 LDS additions for two elements).
+// Zeros and mask values, which can be most of a row, are counted in registers.
+__device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve, bool head, bool tail) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t zeros = 0, low_n = 0, low_bits = 0;
+    char *base = (char *)h.bin;
+    auto single = [&](uint32_t b) {
+        const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
+        if (q < kBinsHalf) {
+            atomicAdd(&h.bin[(b >> 15) * kBinsHalf + q], 1u);
+        } else if (mag == 0) {
+            ++zeros;
+        } else if (mag < kMagLo) {
+            const uint32_t at = atomicAdd(&h.side_n, 1u);
+            if (at < kSideMax) h.side[at] = b;
+        } else if (b > 0x8000u && b < 0xFF80u) {
+            if (low_n == 0) low_bits = b;
+            if (b == low_bits) ++low_n;
+            else h.odd = 1;
+        } else if (b <= 0x7F80u) {
+            h.odd = 1;
         }
-    if (lane == 63)
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            sc.csum[wave][s] = ic[s];
-            sc.wsum[wave][s] = iw[s];
+    };
+    auto pair = [&](uint32_t w) {
+        const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo};
+        const uint32_t t = __builtin_bit_cast(uint32_t, (u16x2)(__builtin_bit_cast(u16x2, w) - lo));
+        if ((t & 0x70007000u) == 0) {
+            const uint32_t a = ((t << 2) & 0x3FFC3FFCu) | ((t >> 1) & 0x40004000u);
+            atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), 1u);
+            atomicAdd((uint32_t *)(base + (a >> 16)), 1u);
+        } else {
+            single(w & 0xFFFFu);
+            single(w >> 16);
         }
-    __syncthreads();
-    tc = 0;
-    tw = 0.0;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        uint32_t bc = tc;
-        double bw = tw;
-        for (int v = 0; v < kWaves; ++v) {
-            if (v == wave) {
-                bc = tc;
-                bw = tw;
-            }
-            tc += sc.csum[v][s];
-            tw += sc.wsum[v][s];
-        }
-        const uint32_t xc = __shfl_up(ic[s], 1);
-        const double xw = __shfl_up(iw[s], 1);
-        ec[s] = bc + (lane ? xc : 0);
-        ew[s] = bw + (lane ? xw : 0.0);
-    }
-    __syncthreads();
+    };
+    for_elements(r, vb, ve, head, tail, pair, single);
+    if (zeros) atomicAdd(&h.zeros, zeros);
+    if (low_n) hist_low(h, low_bits, low_n);
 }
 
 // ---- the draw ---------------------------------------------------------------------------
 
-struct Drawn {
-    uint32_t bits, ordinal;  // the value and which of its occurrences
-    float logprob;
-    bool any, counted;       // anything to draw from; by the histogram, not the long way
+struct Found {
+    double mass, logprob;    // W, and of a draw its log-probability
+    uint32_t pos, bits, ord; // tokens counted; of a draw the value and which of its occurrences
 };
 
-// Counts(seg) makes segment `seg` of the order readable; count(seg, j) and bits(seg, j)
-// are its bins, descending, NB(seg) of them for each thread.
-template <int S, typename Bins>
-__device__ Drawn draw(Scratch &sc, Bins &bins, const Params &par, int64_t m) {
-    Drawn out{0, 0, -__builtin_inff(), false, Bins::kResident};
-    const int t = threadIdx.x;
-    Weight wt;
+struct Draw {
+    Hist h;
+    uint32_t item_bits[kItems], item_count[kItems];
+    double item_weight[kItems];
+    double wsum[kWaves], win_mass[kWindows + 1], win_first[kWindows];
+    uint32_t csum[kWaves], win_count[kWindows + 1];
+    uint32_t first, owner[8];
+    uint32_t count[kWaves];  // locate's
+    int at;
+    Found found;
+};
+
+struct Drawn {
+    uint32_t bits, ordinal;
+    float logprob;
+    bool any, counted;  // anything to draw from; by the histogram, not the long way
+};
+
+enum Seek { kMass, kTopP, kMinP, kDraw };
+
+// Draws from the whole row's histogram in sh.h. Used by whole workgroups.
+__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params &par, int64_t m) {
+    Hist &h = sh.h;
+    const int t = threadIdx.x, lane = t & 63, wave = wave_id();
+    const bool longway = h.odd || h.side_n > kSideMax;
+    const int windows = longway ? kWindows : 1;
+    Drawn out{0, 0, -__builtin_inff(), false, !longway};
     const bool greedy = is_greedy(par, m);
+    Weight wt;
+    wt.max = 0.0;
     wt.inv_t = greedy || !par.temperature ? 1.0 : 1.0 / (double)par.temperature[m];
-
-    // the largest value
-    if (t == 0) sc.sel[0] = 0;
-    __syncthreads();
-    uint32_t best = 0;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        bins.load(s);
-        for (int j = 0; j < bins.nb(s); ++j)
-            if (bins.count(s, j)) best = max(best, key_of(bins.bits(s, j)));
-        if (!Bins::kResident && __syncthreads_or(best != 0)) break;
+    if (t < 8) sh.owner[t] = 0;
+    if (t == 8) sh.first = ~0u;
+    if (t == 9) {
+        sh.win_count[0] = 0;
+        sh.win_mass[0] = 0.0;
     }
-    if (best) atomicMax(&sc.sel[0], best);
-    __syncthreads();
-    const uint32_t top = sc.sel[0];
-    if (top == 0) return out;  // nothing to draw from
-    out.any = true;
-    wt.max = value_of(bits_of(top));
 
-    uint32_t c[S], ec[S], total;
-    double w[S], ew[S], wtotal;
+    // side items in order: a value's place is the number of larger entries and its first
+    // entry stands there for all equal ones (the places of the others stay empty); zero
+    // stands between the signs. The low pattern is the last item, after every bin.
+    const uint32_t side_n = longway ? 0 : h.side_n, zeros = longway ? 0 : h.zeros, low_n = longway ? 0 : h.low_n;
+    const int sides = (int)(side_n + (zeros ? 1 : 0));
+    if (t < kItems) sh.item_count[t] = 0;
+    __syncthreads();
+    if (t < sides) {
+        const uint32_t mine = t < (int)side_n ? h.side[t] : 0, key = key_of(mine);
+        uint32_t place = 0, equal = 0;
+        bool lead = true;
+        for (uint32_t j = 0; j < side_n; ++j) {
+            const uint32_t o = key_of(h.side[j]);
+            place += o > key;
+            equal += o == key;
+            lead = lead && !(o == key && (int)j < t);
+        }
+        if (t < (int)side_n && zeros) place += 0x8000u > key;
+        if (lead) {
+            sh.item_bits[place] = mine;
+            sh.item_count[place] = t < (int)side_n ? equal : zeros;
+        }
+    } else if (t == kThreads - 1) {
+        sh.item_bits[kItems - 1] = h.low_bits;
+        sh.item_count[kItems - 1] = low_n;
+    }
+    __syncthreads();
+
+    // this thread's bins, descending: patterns bits0, bits0 + dir, ...
+    uint32_t bits0 = 0, cnt[kOwn], c = 0, ec = 0;
+    int dir = 0, f = kOwn;        // f: its first occurring bin
+    double wf = 0.0, ratio = 0.0, w = 0.0, ew = 0.0;  // that one's weight; W of the thread and before it
+    int current = -1;
+
+    // Items of thread t after its bins: [item_b, item_e).
+    const int item_b = t == kThreads - 1 ? kItems - 1 : 0;
+    const int item_e = longway ? item_b : (t == kLastPositive ? sides : (t == kThreads - 1 ? kItems : 0));
+
+    auto analyse = [&](int win) {
+        // read before the barriers below, behind which it is set
+        const bool find_max = current < 0 || sh.first == ~0u;
+        if (longway) {  // count this window's patterns
+            __syncthreads();
+            for (int i = t; i < (int)kBins / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+            auto single = [&](uint32_t b) {
+                const uint32_t key = key_of(b), place = 65535u - key - (uint32_t)win * kBins;
+                if (key_valid(key) && place < kBins) atomicAdd(&h.bin[place], 1u);
+            };
+            for_elements(
+                row, 0, row.nvec, true, true,
+                [&](uint32_t x) {
+                    single(x & 0xFFFFu);
+                    single(x >> 16);
+                },
+                single);
+            __syncthreads();
+            const uint32_t key0 = 65535u - (uint32_t)win * kBins - kOwn * t;
+            dir = key0 & 0x8000u ? -1 : 1;
+            bits0 = key0 & 0x8000u ? key0 & 0x7FFFu : ~key0 & 0xFFFFu;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        bins.load(s);
-        c[s] = 0;
-        w[s] = 0.0;
-        for (int j = 0; j < bins.nb(s); ++j) {
-            const uint32_t n = bins.count(s, j);
-            if (n) {
-                c[s] += n;
-                w[s] += n * wt(bins.bits(s, j));
+            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kOwn * t + j];
+        } else if (t <= kLastPositive) {
+            dir = -1;
+            bits0 = kMagLo + kBinsHalf - 1 - kOwn * t;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kBinsHalf - 1 - kOwn * t - j];
+        } else {
+            dir = 1;
+            bits0 = 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kOwn * t + j];
+        }
+        c = 0;
+        f = kOwn;
+#pragma unroll
+        for (int j = kOwn - 1; j >= 0; --j) {
+            c += cnt[j];
+            if (cnt[j]) f = j;
+        }
+        if (find_max) {  // the largest value, once
+            uint32_t place = ~0u;
+            if (f < kOwn) place = t * 128 + f;
+            else
+                for (int i = item_e - 1; i >= item_b; --i)
+                    if (sh.item_count[i]) place = t * 128 + kOwn + i;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) place = min(place, (uint32_t)__shfl_xor((int)place, d));
+            if (lane == 0 && place != ~0u) atomicMin(&sh.first, place);
+            __syncthreads();
+            const uint32_t first = sh.first;
+            if (first != ~0u) {
+                const uint32_t ft = first >> 7, fj = first & 127;
+                if (fj >= kOwn) wt.max = value_of(sh.item_bits[fj - kOwn]);
+                else if (longway) {
+                    const uint32_t key = 65535u - (uint32_t)win * kBins - (kOwn * ft + fj);
+                    wt.max = value_of(key & 0x8000u ? key & 0x7FFFu : ~key & 0xFFFFu);
+                } else if (ft <= kLastPositive) wt.max = value_of(kMagLo + kBinsHalf - 1 - kOwn * ft - fj);
+                else wt.max = value_of(0x8000u | (kMagLo + kOwn * (ft - kLastPositive - 1) + fj));
+                // the items' weights, one a thread
+                if (t < kItems && sh.item_count[t]) sh.item_weight[t] = wt(sh.item_bits[t]);
+            }
+            __syncthreads();
+        }
+        w = 0.0;
+        if (f < kOwn) {
+            wf = wt(bits0 + dir * f);
+            const double gap = value_of(bits0) - value_of(bits0 + dir);
+            ratio = exp(-gap * wt.inv_t);
+            double x = wf;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                if (cnt[j]) w += cnt[j] * x;
+                if (j >= f) x *= ratio;
             }
         }
-    }
-    order_scan<S>(sc, c, w, ec, ew, total, wtotal);
-
-    // W(n) for 1 <= n <= total
-    auto mass = [&](uint32_t n) -> double {
-        if (n >= total) return wtotal;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (ec[s] < n && n <= ec[s] + c[s]) sc.sel[1] = s;
-        __syncthreads();
-        const int seg = sc.sel[1];
-        bins.load(seg);
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (s == seg && ec[s] < n && n <= ec[s] + c[s]) {
-                uint32_t left = n - ec[s];
-                double sum = ew[s];
-                for (int j = 0; j < bins.nb(s) && left; ++j) {
-                    const uint32_t k = min(left, bins.count(s, j));
-                    if (k) sum += k * wt(bins.bits(s, j));
-                    left -= k;
-                }
-                sc.val[0] = sum;
+        for (int i = item_b; i < item_e; ++i)
+            if (sh.item_count[i]) {
+                c += sh.item_count[i];
+                w += sh.item_count[i] * sh.item_weight[i];
             }
-        __syncthreads();
-        return sc.val[0];
-    };
-    // The last (segment, thread) that holds tokens of the first `n` and has
-    // W before it below `target` (or equal to it, if `eq`): the one that crosses it.
-    auto crossing = [&](double target, uint32_t n, bool eq) -> uint32_t {
-        if (t == 0) sc.sel[2] = 0;
-        __syncthreads();
-        uint32_t at = 0;
+        // exclusive prefix over the threads, after the windows before this one
+        uint32_t ic = c;
+        double iw = w;
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (c[s] && ec[s] < n && (ec[s] == 0 || ew[s] < target || (eq && ew[s] == target))) at = s * kThreads + t + 1;
-        if (at) atomicMax(&sc.sel[2], at);
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t pc = __shfl_up(ic, d);
+            const double pw = __shfl_up(iw, d);
+            if (lane >= d) {
+                ic += pc;
+                iw += pw;
+            }
+        }
+        if (lane == 63) {
+            sh.csum[wave] = ic;
+            sh.wsum[wave] = iw;
+        }
+        const uint32_t xc = __shfl_up(ic, 1);
+        const double xw = __shfl_up(iw, 1);
         __syncthreads();
-        const uint32_t r = sc.sel[2] - 1;
-        bins.load(r / kThreads);
-        return r;
+        uint32_t bc = sh.win_count[win];
+        double bw = sh.win_mass[win];
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            if (v == wave) {
+                ec = bc + (lane ? xc : 0);
+                ew = bw + (lane ? xw : 0.0);
+            }
+            bc += sh.csum[v];
+            bw += sh.wsum[v];
+        }
+        if (t == 0) {
+            sh.win_count[win + 1] = bc;
+            sh.win_mass[win + 1] = bw;
+        }
+        // the weight of the window's first value, where it has any
+        if (longway && c && ec == sh.win_count[win]) sh.win_first[win] = wf;
+        __syncthreads();
+        current = win;
+    };
+
+    for (int win = 0; win < windows; ++win) analyse(win);
+    const uint32_t total = sh.win_count[windows];
+    const double wtotal = sh.win_mass[windows];
+    if (total == 0) return out;  // nothing to draw from
+    out.any = true;
+
+    // Finds the thread that crosses n tokens or mass x, and in it the item.
+    int seeks = 0;
+    auto seek = [&](Seek mode, uint32_t n, double x) {
+        if (longway) {
+            int win = 0;
+            for (int i = 0; i < kWindows; ++i) {
+                const uint32_t b = sh.win_count[i];
+                if (sh.win_count[i + 1] == b) continue;
+                const double bm = sh.win_mass[i];
+                const bool in = mode == kMass ? b < n
+                                : mode == kTopP ? b == 0 || bm < x
+                                : mode == kMinP ? b == 0 || sh.win_first[i] >= x
+                                                : b < n && (b == 0 || bm <= x);
+                if (in) win = i;
+            }
+            if (win != current) analyse(win);
+        }
+        const int slot = seeks++ & 7;
+        // holds for a leading stretch of the threads that own tokens
+        const bool in = c && (mode == kMass ? ec < n
+                              : mode == kTopP ? ec == 0 || ew < x
+                              : mode == kMinP ? (f < kOwn ? wf : sh.item_weight[item_b]) >= x || ec == 0
+                                              : ec < n && (ec == 0 || ew <= x));
+        const uint64_t mask = __ballot(in);
+        if (mask && lane == 0) atomicMax(&sh.owner[slot], (uint32_t)(wave * 64 + 64 - __builtin_clzll(mask)));
+        __syncthreads();
+        if (sh.owner[slot] == (uint32_t)t + 1) {
+            uint32_t pos = ec, bits = 0, ord = 0;
+            double before = ew, weight = wf;
+            bool done = false;
+            int j = f;
+            int i = item_b;
+            while (!done) {
+                uint32_t k, b;
+                double v;
+                if (j < kOwn) {
+                    k = longway ? h.bin[kOwn * t + j] : h.bin[t <= kLastPositive ? kBinsHalf - 1 - kOwn * t - j : kOwn * t + j];
+                    b = bits0 + dir * j;
+                    v = weight;
+                    weight *= ratio;
+                    ++j;
+                } else if (i < item_e) {
+                    k = sh.item_count[i];
+                    b = sh.item_bits[i];
+                    v = sh.item_weight[i];
+                    ++i;
+                } else break;
+                if (k == 0) continue;
+                if (mode != kTopP && mode != kMinP) {
+                    k = min(k, n - pos);  // no more than n tokens
+                    if (k == 0) break;
+                }
+                const double end = before + k * v;
+                uint32_t part = k;
+                if (mode == kMinP) {
+                    done = v < x;
+                    if (done) part = 0;
+                } else if (mode == kTopP && end >= x) {
+                    // tokens whose W before them is below x
+                    const double y = v > 0.0 ? ceil((x - before) / v) : (double)k;
+                    part = y <= 0.0 ? 0 : (y >= (double)k ? k : (uint32_t)y);
+                    while (part > 0 && before + (part - 1) * v >= x) --part;
+                    while (part < k && before + part * v < x) ++part;
+                    done = true;
+                } else if (mode == kDraw) {
+                    if (v > 0.0 || pos == 0) {  // the last with weight, should rounding leave none crossing
+                        bits = b;
+                        ord = k - 1;
+                    }
+                    if (end > x) {
+                        const double y = (x - before) / v;
+                        ord = y <= 0.0 ? 0 : (y >= (double)k ? k - 1 : (uint32_t)y);
+                        while (ord > 0 && before + ord * v > x) --ord;
+                        while (ord + 1 < k && before + (ord + 1) * v <= x) ++ord;
+                        done = true;
+                    }
+                }
+                pos += part;
+                before = end;
+            }
+            sh.found.pos = pos;
+            sh.found.mass = before;
+            sh.found.bits = bits;
+            sh.found.ord = ord;
+        }
+        __syncthreads();
     };
 
     uint32_t n = total;
+    double mass = wtotal;
     const uint32_t k = limit_of(par, m);
-    if (k && k < n) n = k;
-    if (!greedy && par.top_p) {
-        const float p = par.top_p[m];
-        if (p < 1.f) {
-            const double target = (double)p * mass(n);
-            const uint32_t own = crossing(target, n, false);
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (own == (uint32_t)(s * kThreads + t)) {
-                    // tokens whose W before them is below the target
-                    uint32_t kept = ec[s];
-                    double before = ew[s];
-                    for (int j = 0; j < bins.nb(s); ++j) {
-                        const uint32_t cnt = bins.count(s, j);
-                        if (!cnt) continue;
-                        const double v = wt(bins.bits(s, j));
-                        const double end = before + cnt * v;
-                        if (end < target) {
-                            kept += cnt;
-                            before = end;
-                            continue;
-                        }
-                        double x = v > 0.0 ? ceil((target - before) / v) : (double)cnt;
-                        uint32_t add = x <= 0.0 ? 0 : (x >= (double)cnt ? cnt : (uint32_t)x);
-                        while (add > 0 && before + (add - 1) * v >= target) --add;
-                        while (add < cnt && before + add * v < target) ++add;
-                        kept += add;
-                        break;
-                    }
-                    sc.sel[3] = kept ? kept : 1;
-                }
-            __syncthreads();
-            n = min(n, sc.sel[3]);
-        }
-    }
-    if (!greedy && par.min_p) {
-        const float q = par.min_p[m];
-        if (q > 0.f) {
-            if (t == 0) sc.sel[4] = 1;
-            __syncthreads();
-            uint32_t kept = 0;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                bins.load(s);
-                uint32_t run = ec[s];
-                for (int j = 0; j < bins.nb(s); ++j) {
-                    const uint32_t cnt = bins.count(s, j);
-                    if (!cnt) continue;
-                    if (wt(bins.bits(s, j)) < (double)q) break;
-                    run += cnt;
-                    kept = run;
-                }
-            }
-            if (kept) atomicMax(&sc.sel[4], kept);
-            __syncthreads();
-            n = min(n, sc.sel[4]);
-        }
-    }
-    const double sum = mass(n);
+    const float top_p = greedy || !par.top_p ? 1.f : par.top_p[m], min_p = greedy || !par.min_p ? 0.f : par.min_p[m];
     float u = par.u[m];
     u = u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;  // [0, 1), NaN as 0
-    const double target = (double)u * sum;
-    const uint32_t own = crossing(target, n, true);
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-        if (own == (uint32_t)(s * kThreads + t)) {
-            uint32_t pos = ec[s];
-            double before = ew[s];
-            uint32_t bits = 0, ord = 0;
-            for (int j = 0; j < bins.nb(s) && pos < n; ++j) {
-                const uint32_t cnt = min(bins.count(s, j), n - pos);
-                if (!cnt) continue;
-                const uint32_t bb = bins.bits(s, j);
-                const double v = wt(bb);
-                const double end = before + cnt * v;
-                if (v > 0.0 || pos == 0) {  // the last value with weight, should rounding leave none crossing
-                    bits = bb;
-                    ord = cnt - 1;
-                }
-                if (end > target) {
-                    const double x = (target - before) / v;
-                    ord = x <= 0.0 ? 0 : (x >= (double)cnt ? cnt - 1 : (uint32_t)x);
-                    while (ord > 0 && before + ord * v > target) --ord;
-                    while (ord + 1 < cnt && before + (ord + 1) * v <= target) ++ord;
-                    break;
-                }
-                pos += cnt;
-                before = end;
-            }
-            sc.sel[5] = bits;
-            sc.sel[6] = ord;
-            sc.val[1] = wt.exponent(bits) - log(sum);
+    // at most: W(n1), n2, n3, W(n), the draw
+#pragma unroll 1
+    for (int step = 0; step < 5; ++step) {
+        Seek mode = kMass;
+        double x = 0.0;
+        if (step == 0) {
+            if (!(k && k < n)) continue;
+            n = k;
+        } else if (step == 1) {
+            if (!(top_p < 1.f)) continue;
+            mode = kTopP;
+            x = (double)top_p * mass;
+        } else if (step == 2) {
+            if (!(min_p > 0.f)) continue;
+            mode = kMinP;
+            x = (double)min_p;
+        } else if (step == 3) {
+            if (!(top_p < 1.f) && !(min_p > 0.f)) continue;  // as step 0 left it
+        } else {
+            mode = kDraw;
+            x = (double)u * mass;
         }
-    __syncthreads();
-    out.bits = sc.sel[5];
-    out.ordinal = sc.sel[6];
-    out.logprob = (float)sc.val[1];
+        seek(mode, n, x);
+        const uint32_t pos = sh.found.pos;
+        if (mode == kMass) mass = sh.found.mass;
+        else if (mode != kDraw) n = min(n, max(pos, 1u));
+        __syncthreads();
+    }
+    out.bits = sh.found.bits;
+    out.ordinal = sh.found.ord;
+    out.logprob = (float)(wt.exponent(out.bits) - log(mass));
     return out;
 }
-
-// The order of a counted row: positive bins, tiny magnitudes and zero, negative bins.
-struct CountedBins {
-    static constexpr bool kResident = true;
-    const uint32_t *bin, *side_bits, *side_count;
-    int sides;
-    __device__ __forceinline__ void load(int) {}
-    __device__ __forceinline__ int nb(int s) const { return s == 1 ? 1 : (int)kBinsHalf / kThreads; }
-    __device__ __forceinline__ uint32_t index(int s, int j) const {
-        return (s ? kBinsHalf : 0) + threadIdx.x * (kBinsHalf / kThreads) + j;
-    }
-    __device__ __forceinline__ uint32_t count(int s, int j) const {
-        if (s == 1) return (int)threadIdx.x < sides ? side_count[threadIdx.x] : 0;
-        return bin[index(s, j)];
-    }
-    __device__ __forceinline__ uint32_t bits(int s, int j) const {
-        return s == 1 ? side_bits[threadIdx.x] : bin_bits(index(s, j));
-    }
-};
-
-// All patterns, one window of them at a time, descending.
-struct WindowBins {
-    static constexpr bool kResident = false;
-    uint32_t *table;  // kWindow counts
-    Row row;
-    __device__ void load(int s) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < (int)kWindow / 4; i += kThreads) ((uint4 *)table)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-        uint32_t *tab = table;
-        for_elements(row, 0, row.nvec, true, true, [=](uint32_t b) {
-            const uint32_t key = key_of(b);
-            if (key_valid(key) && (int)(key >> 14) == kWindows - 1 - s)
-                atomicAdd(&tab[kWindow - 1 - (key & (kWindow - 1))], 1u);
-        });
-        __syncthreads();
-    }
-    __device__ __forceinline__ int nb(int) const { return kWindow / kThreads; }
-    __device__ __forceinline__ uint32_t count(int, int j) const { return table[threadIdx.x * (kWindow / kThreads) + j]; }
-    __device__ __forceinline__ uint32_t bits(int s, int j) const {
-        return bits_of((uint32_t)(kWindows - 1 - s) * kWindow + kWindow - 1 - (threadIdx.x * (kWindow / kThreads) + j));
-    }
-};
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
 // tail), in index order, by the whole workgroup; every thread gets it (-1 if there are
 // fewer, which a consistent histogram excludes).
-__device__ int locate(Scratch &sc, const Row &r, int vb, int ve, bool head, bool tail, uint32_t bits, uint32_t ordinal) {
+__device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bool head, bool tail, uint32_t bits, uint32_t ordinal) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     const bool zero = (bits & 0x7FFFu) == 0;  // both zeros are one value
     const uint32_t mask16 = zero ? 0x7FFFu : 0xFFFFu;
     auto same = [&](uint32_t b) { return ((b ^ bits) & mask16) == 0; };
     uint32_t left = ordinal;
-    __shared__ int found;
-    if (threadIdx.x == 0) found = -1;
+    if (threadIdx.x == 0) sh.at = -1;
     __syncthreads();
     if (head) {  // every wave looks at these few elements itself
         const bool eq = lane < r.head && same(r.p[lane]);
@@ -499,12 +580,12 @@ __device__ int locate(Scratch &sc, const Row &r, int vb, int ve, bool head, bool
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        if (lane == 0) sc.count[wave] = sum;
+        if (lane == 0) sh.count[wave] = sum;
         __syncthreads();
         uint32_t before = 0, all = 0;
         for (int v = 0; v < kWaves; ++v) {
             if (v == wave) before = all;
-            all += sc.count[v];
+            all += sh.count[v];
         }
         if (left < all) {
             if (before <= left && left < before + sum) {  // in this wave's part
@@ -531,7 +612,7 @@ __device__ int locate(Scratch &sc, const Row &r, int vb, int ve, bool head, bool
                                     }
                                     --skip;
                                 }
-                            found = at;
+                            sh.at = at;
                         }
                         break;
                     }
@@ -539,7 +620,7 @@ __device__ int locate(Scratch &sc, const Row &r, int vb, int ve, bool head, bool
                 }
             }
             __syncthreads();
-            return found;
+            return sh.at;
         }
         left -= all;
         __syncthreads();
@@ -556,102 +637,55 @@ __device__ int locate(Scratch &sc, const Row &r, int vb, int ve, bool head, bool
     return -1;
 }
 
-struct SelectShared {
-    union {
-        struct {
-            Hist h;
-            uint32_t sorted_bits[kThreads], sorted_count[kThreads];
-        } counted;
-        uint32_t table[kWindow];
-    };
-    Scratch sc;
-};
-
-// Draws from the histogram in sh (of the whole row), or the long way.
-__device__ Drawn draw_row(SelectShared &sh, const Row &row, const Params &par, int64_t m) {
-    Hist &h = sh.counted.h;
-    const uint32_t side_n = h.side_n, zeros = h.zeros;
-    if (h.odd || side_n > kSideMax) {
-        WindowBins bins{sh.table, row};
-        __syncthreads();
-        return draw<kWindows>(sh.sc, bins, par, m);
-    }
-    // order the list: a value's place is the number of larger entries, its first entry
-    // stands there for all equal ones (the places of the others stay empty); zero stands
-    // between the signs
-    const uint32_t sides = side_n + (zeros ? 1 : 0);
-    const uint32_t t = threadIdx.x;
-    sh.counted.sorted_count[t] = 0;
-    __syncthreads();
-    if (t < sides) {
-        const uint32_t mine = t < side_n ? h.side[t] : 0, key = key_of(mine);
-        uint32_t place = 0, equal = 0;
-        bool first = true;
-        for (uint32_t j = 0; j < side_n; ++j) {
-            const uint32_t o = key_of(h.side[j]);
-            place += o > key;
-            equal += o == key;
-            first = first && !(o == key && j < t);
-        }
-        if (t < side_n && zeros) place += 0x8000u > key;
-        if (first) {
-            sh.counted.sorted_bits[place] = mine;
-            sh.counted.sorted_count[place] = t < side_n ? equal : zeros;
-        }
-    }
-    __syncthreads();
-    CountedBins bins{h.bin, sh.counted.sorted_bits, sh.counted.sorted_count, (int)sides};
-    return draw<3>(sh.sc, bins, par, m);
-}
-
 // ---- kernels ------------------------------------------------------------------------------
 
 // One workgroup per row: count, draw, find.
 __global__ __launch_bounds__(kThreads) void sample_row_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
                                                               int32_t *__restrict__ tokens, float *__restrict__ logprobs,
                                                               int V) {
-    __shared__ __attribute__((aligned(16))) SelectShared sh;
+    __shared__ __attribute__((aligned(16))) Draw sh;
     const int64_t m = blockIdx.x;
     const Row row = make_row(logits + m * ld, V);
-    Hist &h = sh.counted.h;
-    hist_clear(h);
+    hist_clear(sh.h);
     __syncthreads();
-    for_elements(row, 0, row.nvec, true, true, [&](uint32_t b) { hist_add(h, b); });
+    hist_count(sh.h, row, 0, row.nvec, true, true);
     __syncthreads();
     const Drawn d = draw_row(sh, row, par, m);
     int token = -1;
-    if (d.any) token = locate(sh.sc, row, 0, row.nvec, true, true, d.bits, d.ordinal);
+    if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
     if (threadIdx.x == 0) {
         tokens[m] = token;
         if (logprobs) logprobs[m] = d.logprob;
     }
 }
 
-// Workspace of one (row, part): header, then the occurring bins (bin << 18 | count),
-// then the list of tiny magnitudes.
-constexpr uint32_t kHeader = 4;
-constexpr uint32_t kPartWords = kHeader + kBins + kSideMax + 1;
+// Workspace of one (row, part): header, then the occurring bins in descending order
+// (place in that order << 18 | count), then the smaller magnitudes.
+constexpr uint32_t kHeader = 8;
+constexpr uint32_t kPartWords = kHeader + kBins + kSideMax;
 constexpr uint32_t kCountBits = 18;
+constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 constexpr int64_t kMaxPartVectors = ((1 << kCountBits) - 16) / 8;  // a part's tokens fit the count
 constexpr int kMaxParts = kThreads;
 
 __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
                                                                 uint32_t *__restrict__ parts, int V, int C, int vpp) {
     __shared__ __attribute__((aligned(16))) Hist h;
-    __shared__ uint32_t wsum[kWaves][2];
+    __shared__ uint32_t wsum[kWaves][2], entries;
     const int64_t m = blockIdx.x / C;
     const int part = blockIdx.x % C;
     const Row row = make_row(logits + m * ld, V);
     hist_clear(h);
+    if (threadIdx.x == 0) entries = 0;
     __syncthreads();
     const int vb = min(part * vpp, row.nvec), ve = min(vb + vpp, row.nvec);
-    for_elements(row, vb, ve, part == 0, part == C - 1, [&](uint32_t b) { hist_add(h, b); });
+    hist_count(h, row, vb, ve, part == 0, part == C - 1);
     __syncthreads();
     // occurring bins in descending order, but none behind which top_k tokens of this
     // part already stand; (bins << 18 | tokens) are scanned in one word
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
-    const uint4 v0 = ((const uint4 *)h.bin)[t], v1 = ((const uint4 *)h.bin)[kBinsHalf / 4 + t];
-    const uint32_t n[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
+    const uint4 v0 = ((const uint4 *)h.bin)[kBinsHalf / 4 - 1 - t], v1 = ((const uint4 *)h.bin)[kBinsHalf / 4 + t];
+    const uint32_t n[2][4] = {{v0.w, v0.z, v0.y, v0.x}, {v1.x, v1.y, v1.z, v1.w}};
     uint32_t own[2], inc[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -676,38 +710,32 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     const uint32_t k = limit_of(par, m);
     const uint32_t middle = h.zeros + h.side_n;
     uint32_t run = 0;
-    __shared__ uint32_t entries;
-    if (t == 0) entries = 0;
-    __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         uint32_t before = run;
+#pragma unroll
         for (int v = 0; v < kWaves; ++v) {
             if (v == wave) before = run;
             run += wsum[v][s];
         }
-        uint32_t at = before + inc[s] - own[s];
-        uint32_t last = 0;
+        uint32_t at = before + inc[s] - own[s], last = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (n[s][j]) {
-                const uint32_t above = (at & ((1u << kCountBits) - 1)) + (s ? middle : 0), pos = at >> kCountBits;
+                const uint32_t above = (at & kCountMask) + (s ? middle : 0), pos = at >> kCountBits;
                 if (!k || above < k) {
-                    dst[kHeader + pos] = ((s ? kBinsHalf : 0) + 4 * t + j) << kCountBits | n[s][j];
+                    dst[kHeader + pos] = (s * kBinsHalf + 4 * t + j) << kCountBits | n[s][j];
                     last = pos + 1;
                 }
                 at += n[s][j] + (1u << kCountBits);
             }
         if (last) atomicMax(&entries, last);
     }
-    const uint32_t sides = min(h.side_n, kSideMax);
-    for (uint32_t i = t; i < sides; i += kThreads) dst[kHeader + kBins + i] = h.side[i];
+    if (t < (int)min(h.side_n, kSideMax)) dst[kHeader + kBins + t] = h.side[t];
     __syncthreads();
     if (t == 0) {
-        dst[0] = entries;
-        dst[1] = h.side_n;
-        dst[2] = h.zeros;
-        dst[3] = h.odd;
+        ((uint4 *)dst)[0] = make_uint4(entries, h.side_n, h.zeros, h.odd);
+        ((uint4 *)dst)[1] = make_uint4(h.low_n, h.low_bits, 0, 0);
     }
 }
 
@@ -715,41 +743,51 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
                                                                  const uint32_t *__restrict__ parts,
                                                                  int32_t *__restrict__ tokens,
                                                                  float *__restrict__ logprobs, int V, int C, int vpp) {
-    __shared__ __attribute__((aligned(16))) SelectShared sh;
+    __shared__ __attribute__((aligned(16))) Draw sh;
     __shared__ uint32_t in_part[kMaxParts];
     const int64_t m = blockIdx.x;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
     const Row row = make_row(logits + m * ld, V);
     const uint32_t *src = parts + (int64_t)m * C * kPartWords;
-    Hist &h = sh.counted.h;
+    Hist &h = sh.h;
     hist_clear(h);
     __syncthreads();
+    auto add = [&](uint32_t e) { atomicAdd(&h.bin[bin_order(e >> kCountBits)], e & kCountMask); };
+    constexpr int kAhead = 4;  // entries of a lane read along with the header
     for (int c = wave; c < C; c += kWaves) {
         const uint32_t *p = src + (int64_t)c * kPartWords;
-        const uint32_t entries = p[0], side_n = p[1], zeros = p[2], odd = p[3];
-        for (uint32_t i = lane; i < entries; i += 64) {
-            const uint32_t e = p[kHeader + i];
-            atomicAdd(&h.bin[e >> kCountBits], e & ((1u << kCountBits) - 1));
-        }
+        const uint4 a = ((const uint4 *)p)[0], b = ((const uint4 *)p)[1];
+        uint32_t e[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) e[i] = p[kHeader + 64 * i + lane];
+        const uint32_t entries = a.x, side_n = a.y;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (64 * i + lane < entries) add(e[i]);
+        for (uint32_t i = 64 * kAhead + lane; i < entries; i += 64) add(p[kHeader + i]);
         uint32_t at = 0;
         if (lane == 0) {
-            if (zeros) atomicAdd(&h.zeros, zeros);
-            if (odd) h.odd = 1;
+            if (a.z) atomicAdd(&h.zeros, a.z);
+            if (a.w) h.odd = 1;
             if (side_n) at = atomicAdd(&h.side_n, side_n);
+            if (b.x) hist_low(h, b.y, b.x);
         }
         at = __builtin_amdgcn_readfirstlane(at);
-        for (uint32_t i = lane; i < min(side_n, kSideMax); i += 64)
-            if (at + i < kSideMax) h.side[at + i] = p[kHeader + kBins + i];
+        if (lane < min(side_n, kSideMax) && at + lane < kSideMax) h.side[at + lane] = p[kHeader + kBins + lane];
     }
     __syncthreads();
     const Drawn d = draw_row(sh, row, par, m);
     int token = -1;
     if (d.any) {
         const uint32_t q = (d.bits & 0x7FFFu) - kMagLo;
+        int vb = 0, ve = row.nvec;
+        bool head = true, tail = true;
+        uint32_t left = d.ordinal;
         if (d.counted && q < kBinsHalf) {
             // the value's count in each part tells which part holds the occurrence; a
-            // part's entries ascend by bin: 64 samples, then the stretch between two
-            const uint32_t want = (d.bits & 0x8000u) ? kBinsHalf + q : kBinsHalf - 1 - q;
+            // part's entries ascend by place: 64 samples, then the stretch between two.
+            // (Zero, smaller and low values and the long way have no counts by part.)
+            const uint32_t want = bin_order((d.bits >> 15) * kBinsHalf + q);
             for (int c = wave; c < C; c += kWaves) {
                 const uint32_t *p = src + (int64_t)c * kPartWords;
                 const uint32_t entries = p[0], stride = (entries + 63) / 64;
@@ -761,22 +799,22 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
                 if (hit)
                     for (uint32_t i = lane; i < stride; i += 64) {
                         const uint32_t at = (hit - 1) * stride + i;
-                        const uint32_t e = at < entries ? p[at] : 0xFFFFFFFFu;
-                        if ((e >> kCountBits) == want) n = e & ((1u << kCountBits) - 1);
+                        const uint32_t e = at < entries ? p[at] : ~0u;
+                        if ((e >> kCountBits) == want) n = e & kCountMask;
                     }
 #pragma unroll
                 for (int x = 1; x < 64; x <<= 1) n += __shfl_xor(n, x);
                 if (lane == 0) in_part[c] = n;
             }
             __syncthreads();
-            uint32_t left = d.ordinal;
             int part = 0;
             while (part < C - 1 && left >= in_part[part]) left -= in_part[part++];
-            const int vb = min(part * vpp, row.nvec), ve = min(vb + vpp, row.nvec);
-            token = locate(sh.sc, row, vb, ve, part == 0, part == C - 1, d.bits, left);
-        } else {  // a tiny magnitude, zero, or the long way: no counts by part
-            token = locate(sh.sc, row, 0, row.nvec, true, true, d.bits, d.ordinal);
+            vb = min(part * vpp, row.nvec);
+            ve = min(vb + vpp, row.nvec);
+            head = part == 0;
+            tail = part == C - 1;
         }
+        token = locate(sh, row, vb, ve, head, tail, d.bits, left);
     }
     if (t == 0) {
         tokens[m] = token;
