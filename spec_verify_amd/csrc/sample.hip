@@ -63,36 +63,11 @@ __device__ __forceinline__ Row make_row(const uint16_t *p, int V) {
 
 __device__ __forceinline__ uint4 row_vec(const Row &r, int v) { return *(const uint4 *)(r.p + r.head + (int64_t)v * 8); }
 
-// Calls pair(word) for every two elements of vectors [vb, ve), and single(bits) for those
-// of the head and the tail where asked; any order.
-template <typename F, typename G>
-__device__ __forceinline__ void for_elements(const Row &r, int vb, int ve, bool head, bool tail, F pair, G single) {
-    const int t = threadIdx.x;
-    int v = vb + t;
-    for (; v + 3 * kThreads < ve; v += 4 * kThreads) {
-        uint4 q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = row_vec(r, v + i * kThreads);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            pair(q[i].x);
-            pair(q[i].y);
-            pair(q[i].z);
-            pair(q[i].w);
-        }
-    }
-    for (; v < ve; v += kThreads) {
-        const uint4 q = row_vec(r, v);
-        pair(q.x);
-        pair(q.y);
-        pair(q.z);
-        pair(q.w);
-    }
-    // one wave takes both ends
-    int at = -1;
-    if (head && t < r.head) at = t;
-    if (tail && t >= 8 && t < 8 + r.tail) at = r.head + 8 * r.nvec + t - 8;
-    if (at >= 0) single(r.p[at]);
+// Element i of the row's ends (head, then tail) for i < 16: its index, or -1.
+__device__ __forceinline__ int row_end(const Row &r, int i, bool head, bool tail) {
+    if (head && i < r.head) return i;
+    if (tail && i >= 8 && i < 8 + r.tail) return r.head + 8 * r.nvec + i - 8;
+    return -1;
 }
 
 // ---- patterns, order and weights ---------------------------------------------------
@@ -157,7 +132,9 @@ __device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
 // Counts vectors [vb, ve) of a row. Two elements at a time: subtracting kMagLo from both
 // halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14 say that
 // the magnitude has a bin (9 vector instructions and 2 LDS additions for two elements).
-// Zeros and mask values, which can be most of a row, are counted in registers.
+// A vector with anything else is read again by a loop of its own, which keeps the code of
+// the common case short; pairs of -inf, which can be most of a row, are nothing else.
+// Zeros and mask values are counted in registers.
 __device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve, bool head, bool tail) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     uint32_t zeros = 0, low_n = 0, low_bits = 0;
@@ -179,22 +156,79 @@ __device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve
             h.odd = 1;
         }
     };
-    auto pair = [&](uint32_t w) {
+    auto plain = [](uint32_t w) {
         const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo};
-        const uint32_t t = __builtin_bit_cast(uint32_t, (u16x2)(__builtin_bit_cast(u16x2, w) - lo));
+        return __builtin_bit_cast(uint32_t, (u16x2)(__builtin_bit_cast(u16x2, w) - lo));
+    };
+    // counts the pair if both have bins; whether something is left to do
+    auto pair = [&](uint32_t w) -> bool {
+        const uint32_t t = plain(w);
         if ((t & 0x70007000u) == 0) {
             const uint32_t a = ((t << 2) & 0x3FFC3FFCu) | ((t >> 1) & 0x40004000u);
             atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), 1u);
             atomicAdd((uint32_t *)(base + (a >> 16)), 1u);
-        } else {
-            single(w & 0xFFFFu);
-            single(w >> 16);
+            return false;
+        }
+        return w != 0xFF80FF80u;
+    };
+    auto rest = [&](int v) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = *(const uint32_t *)(r.p + r.head + (int64_t)v * 8 + 2 * i);
+            if ((plain(w) & 0x70007000u) != 0 && w != 0xFF80FF80u) {
+                single(w & 0xFFFFu);
+                single(w >> 16);
+            }
         }
     };
-    for_elements(r, vb, ve, head, tail, pair, single);
+    constexpr int kUnroll = 4;
+    for (int v0 = vb; v0 < ve; v0 += kUnroll * kThreads) {
+        const int v = v0 + (int)threadIdx.x;
+        uint4 q[kUnroll];
+        uint32_t todo = 0;
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            q[i] = v + i * kThreads < ve ? row_vec(r, v + i * kThreads)
+                                         : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint32_t left = (uint32_t)pair(q[i].x) | (uint32_t)pair(q[i].y) | (uint32_t)pair(q[i].z) | (uint32_t)pair(q[i].w);
+            todo |= left << i;
+        }
+        for (; todo; todo &= todo - 1) rest(v + (__builtin_ctz(todo)) * kThreads);
+    }
+    const int at = row_end(r, threadIdx.x, head, tail);
+    if (at >= 0) single(r.p[at]);
     if (zeros) atomicAdd(&h.zeros, zeros);
     if (low_n) hist_low(h, low_bits, low_n);
 }
+
+// ---- wave scans on the cross-lane data path -----------------------------------------------
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {  // lanes without a source get 0
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp0(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp0<CTRL, ROWS>((uint32_t)u) |
+                                          (uint64_t)dpp0<CTRL, ROWS>((uint32_t)(u >> 32)) << 32);
+}
+// Inclusive sums over the 64 lanes: within rows of 16, then the row ends forward.
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+    v += dpp0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += dpp0<0x112, 0xF>(v);
+    v += dpp0<0x114, 0xF>(v);
+    v += dpp0<0x118, 0xF>(v);
+    v += dpp0<0x142, 0xA>(v);  // lane 15 of the row before, to rows 1 and 3
+    v += dpp0<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+    return v;
+}
+// The value one lane down, 0 in lane 0.
+template <typename T>
+__device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
 
 // ---- the draw ---------------------------------------------------------------------------
 
@@ -223,12 +257,13 @@ struct Drawn {
 
 enum Seek { kMass, kTopP, kMinP, kDraw };
 
-// Draws from the whole row's histogram in sh.h. Used by whole workgroups.
-__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params &par, int64_t m) {
+// Draws from the whole row's histogram in sh.h, or window by window from the row itself.
+// Used by whole workgroups.
+template <bool longway>
+__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params &par, int64_t m) {
     Hist &h = sh.h;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
-    const bool longway = h.odd || h.side_n > kSideMax;
-    const int windows = longway ? kWindows : 1;
+    constexpr int windows = longway ? kWindows : 1;
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
     const bool greedy = is_greedy(par, m);
     Weight wt;
@@ -290,13 +325,17 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
                 const uint32_t key = key_of(b), place = 65535u - key - (uint32_t)win * kBins;
                 if (key_valid(key) && place < kBins) atomicAdd(&h.bin[place], 1u);
             };
-            for_elements(
-                row, 0, row.nvec, true, true,
-                [&](uint32_t x) {
-                    single(x & 0xFFFFu);
-                    single(x >> 16);
-                },
-                single);
+#pragma unroll 1
+            for (int v = t; v < row.nvec; v += kThreads) {
+                const uint4 q = row_vec(row, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    single((&q.x)[i] & 0xFFFFu);
+                    single((&q.x)[i] >> 16);
+                }
+            }
+            const int at = row_end(row, t, true, true);
+            if (at >= 0) single(row.p[at]);
             __syncthreads();
             const uint32_t key0 = 65535u - (uint32_t)win * kBins - kOwn * t;
             dir = key0 & 0x8000u ? -1 : 1;
@@ -327,9 +366,8 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
             else
                 for (int i = item_e - 1; i >= item_b; --i)
                     if (sh.item_count[i]) place = t * 128 + kOwn + i;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) place = min(place, (uint32_t)__shfl_xor((int)place, d));
-            if (lane == 0 && place != ~0u) atomicMin(&sh.first, place);
+            const uint64_t mask = __ballot(place != ~0u);  // places ascend with the lane
+            if (mask && lane == __builtin_ctzll(mask)) atomicMin(&sh.first, place);
             __syncthreads();
             const uint32_t first = sh.first;
             if (first != ~0u) {
@@ -363,31 +401,22 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
                 w += sh.item_count[i] * sh.item_weight[i];
             }
         // exclusive prefix over the threads, after the windows before this one
-        uint32_t ic = c;
-        double iw = w;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t pc = __shfl_up(ic, d);
-            const double pw = __shfl_up(iw, d);
-            if (lane >= d) {
-                ic += pc;
-                iw += pw;
-            }
-        }
+        const uint32_t ic = wave_scan(c);
+        const double iw = wave_scan(w);
         if (lane == 63) {
             sh.csum[wave] = ic;
             sh.wsum[wave] = iw;
         }
-        const uint32_t xc = __shfl_up(ic, 1);
-        const double xw = __shfl_up(iw, 1);
+        const uint32_t xc = wave_down(ic);
+        const double xw = wave_down(iw);
         __syncthreads();
         uint32_t bc = sh.win_count[win];
         double bw = sh.win_mass[win];
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) {
             if (v == wave) {
-                ec = bc + (lane ? xc : 0);
-                ew = bw + (lane ? xw : 0.0);
+                ec = bc + xc;
+                ew = bw + xw;
             }
             bc += sh.csum[v];
             bw += sh.wsum[v];
@@ -486,7 +515,7 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
                     }
                 }
                 pos += part;
-                before = end;
+                before = part == k ? end : before + part * v;
             }
             sh.found.pos = pos;
             sh.found.mass = before;
@@ -502,9 +531,9 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
     const float top_p = greedy || !par.top_p ? 1.f : par.top_p[m], min_p = greedy || !par.min_p ? 0.f : par.min_p[m];
     float u = par.u[m];
     u = u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;  // [0, 1), NaN as 0
-    // at most: W(n1), n2, n3, W(n), the draw
+    // W(n1), n2, n3 (each with its W) where they limit, the draw
 #pragma unroll 1
-    for (int step = 0; step < 5; ++step) {
+    for (int step = 0; step < 4; ++step) {
         Seek mode = kMass;
         double x = 0.0;
         if (step == 0) {
@@ -518,22 +547,33 @@ __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params
             if (!(min_p > 0.f)) continue;
             mode = kMinP;
             x = (double)min_p;
-        } else if (step == 3) {
-            if (!(top_p < 1.f) && !(min_p > 0.f)) continue;  // as step 0 left it
         } else {
             mode = kDraw;
             x = (double)u * mass;
         }
         seek(mode, n, x);
         const uint32_t pos = sh.found.pos;
-        if (mode == kMass) mass = sh.found.mass;
-        else if (mode != kDraw) n = min(n, max(pos, 1u));
+        if (mode == kMass) {
+            mass = sh.found.mass;
+        } else if (mode != kDraw && pos < n) {
+            n = max(pos, 1u);
+            mass = pos ? sh.found.mass : 1.0;  // the first token's weight
+        }
         __syncthreads();
     }
     out.bits = sh.found.bits;
     out.ordinal = sh.found.ord;
     out.logprob = (float)(wt.exponent(out.bits) - log(mass));
     return out;
+}
+
+__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const Params &par, int64_t m) {
+    return draw_way<true>(sh, row, par, m);
+}
+
+__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params &par, int64_t m) {
+    if (sh.h.odd || sh.h.side_n > kSideMax) return draw_long(sh, row, par, m);
+    return draw_way<false>(sh, row, par, m);
 }
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
@@ -558,12 +598,12 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
         }
         left -= n;
     }
-    auto matches = [&](const uint4 &q) {
+    auto matches = [&](const uint4 &q) {  // one bit per element
         uint32_t n = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const uint32_t x = (&q.x)[w];
-            n += (uint32_t)same(x & 0xFFFFu) + (uint32_t)same(x >> 16);
+            n |= (uint32_t)same(x & 0xFFFFu) << (2 * w) | (uint32_t)same(x >> 16) << (2 * w + 1);
         }
         return n;
     };
@@ -571,53 +611,39 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
     constexpr int kBlock = kThreads * kIter;    // vectors
     for (int b0 = vb; b0 < ve; b0 += kBlock) {
         const int w0 = b0 + wave * 64 * kIter;
-        uint32_t cnt[kIter], sum = 0;
+        uint32_t eq[kIter], sum = 0;
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
             const int v = w0 + i * 64 + lane;
-            cnt[i] = v < ve ? matches(row_vec(r, v)) : 0;
-            sum += cnt[i];
+            eq[i] = v < ve ? matches(row_vec(r, v)) : 0;
+            sum += __builtin_popcount(eq[i]);
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
         if (lane == 0) sh.count[wave] = sum;
         __syncthreads();
         uint32_t before = 0, all = 0;
+#pragma unroll
         for (int v = 0; v < kWaves; ++v) {
             if (v == wave) before = all;
             all += sh.count[v];
         }
         if (left < all) {
             if (before <= left && left < before + sum) {  // in this wave's part
-                uint32_t rest = left - before;
+                uint32_t skip = left - before;
 #pragma unroll
-                for (int i = 0; i < kIter; ++i) {
-                    uint32_t inc = cnt[i];
-                    for (int d = 1; d < 64; d <<= 1) {
-                        const uint32_t o = __shfl_up(inc, d);
-                        if (lane >= d) inc += o;
-                    }
-                    const uint32_t tot = __shfl(inc, 63);
-                    if (rest < tot) {
-                        const uint32_t mine = inc - cnt[i];
-                        if (mine <= rest && rest < inc) {
-                            const int v = w0 + i * 64 + lane;
-                            uint32_t skip = rest - mine;
-                            int at = -1;
-                            for (int e = 0; e < 8; ++e)
-                                if (same(r.p[r.head + (int64_t)v * 8 + e])) {
-                                    if (skip == 0) {
-                                        at = r.head + v * 8 + e;
-                                        break;
-                                    }
-                                    --skip;
-                                }
-                            sh.at = at;
+                for (int i = 0; i < kIter; ++i)
+                    for (uint64_t mask = __ballot(eq[i] != 0); mask; mask &= mask - 1) {
+                        const int owner = __builtin_ctzll(mask);
+                        uint32_t bitsq = __builtin_amdgcn_readlane(eq[i], owner);
+                        const uint32_t n = __builtin_popcount(bitsq);
+                        if (skip < n) {
+                            for (; skip; --skip) bitsq &= bitsq - 1;
+                            if (lane == 0) sh.at = r.head + (w0 + i * 64 + owner) * 8 + __builtin_ctz(bitsq);
+                            skip = ~0u;  // found: no later vector has that many
+                            break;
                         }
-                        break;
+                        skip -= n;
                     }
-                    rest -= tot;
-                }
             }
             __syncthreads();
             return sh.at;
@@ -639,10 +665,14 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
 
 // ---- kernels ------------------------------------------------------------------------------
 
-// One workgroup per row: count, draw, find.
-__global__ __launch_bounds__(kThreads) void sample_row_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
-                                                              int32_t *__restrict__ tokens, float *__restrict__ logprobs,
-                                                              int V) {
+// One workgroup per row: count, draw, find. Two workgroups share a compute unit (64
+// registers), so one's draw runs beside the other's reading; rows that need the long way
+// are marked and left to a launch of their own, whose workgroups otherwise end at once.
+constexpr int kLongWay = -2;
+
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))) void sample_row_kernel(
+    const uint16_t *__restrict__ logits, int64_t ld, Params par, int32_t *__restrict__ tokens,
+    float *__restrict__ logprobs, int V) {
     __shared__ __attribute__((aligned(16))) Draw sh;
     const int64_t m = blockIdx.x;
     const Row row = make_row(logits + m * ld, V);
@@ -650,7 +680,27 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(const uint16_t *__
     __syncthreads();
     hist_count(sh.h, row, 0, row.nvec, true, true);
     __syncthreads();
-    const Drawn d = draw_row(sh, row, par, m);
+    if (sh.h.odd || sh.h.side_n > kSideMax) {
+        if (threadIdx.x == 0) tokens[m] = kLongWay;
+        return;
+    }
+    const Drawn d = draw_way<false>(sh, row, par, m);
+    int token = -1;
+    if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
+    if (threadIdx.x == 0) {
+        tokens[m] = token;
+        if (logprobs) logprobs[m] = d.logprob;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
+                                                               int32_t *__restrict__ tokens, float *__restrict__ logprobs,
+                                                               int V) {
+    __shared__ __attribute__((aligned(16))) Draw sh;
+    const int64_t m = blockIdx.x;
+    if (tokens[m] != kLongWay) return;
+    const Row row = make_row(logits + m * ld, V);
+    const Drawn d = draw_way<true>(sh, row, par, m);
     int token = -1;
     if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
     if (threadIdx.x == 0) {
@@ -753,27 +803,43 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     hist_clear(h);
     __syncthreads();
     auto add = [&](uint32_t e) { atomicAdd(&h.bin[bin_order(e >> kCountBits)], e & kCountMask); };
-    constexpr int kAhead = 4;  // entries of a lane read along with the header
-    for (int c = wave; c < C; c += kWaves) {
-        const uint32_t *p = src + (int64_t)c * kPartWords;
-        const uint4 a = ((const uint4 *)p)[0], b = ((const uint4 *)p)[1];
-        uint32_t e[kAhead];
+    // A wave takes two parts at once, and keeps the first kAhead entries of a lane for the
+    // search below (all there are, as a rule, where top_k limits them).
+    constexpr int kAhead = 4, kTwo = 2;
+    uint32_t kept[kTwo][kAhead], entries[kTwo] = {0, 0};
+    for (int c0 = 0; c0 < C; c0 += kTwo * kWaves) {
+        uint4 a[kTwo], b[kTwo];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) e[i] = p[kHeader + 64 * i + lane];
-        const uint32_t entries = a.x, side_n = a.y;
+        for (int j = 0; j < kTwo; ++j) {
+            const int c = min(c0 + j * kWaves + wave, C - 1);
+            const uint32_t *p = src + (int64_t)c * kPartWords;
+            a[j] = ((const uint4 *)p)[0];
+            b[j] = ((const uint4 *)p)[1];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (64 * i + lane < entries) add(e[i]);
-        for (uint32_t i = 64 * kAhead + lane; i < entries; i += 64) add(p[kHeader + i]);
-        uint32_t at = 0;
-        if (lane == 0) {
-            if (a.z) atomicAdd(&h.zeros, a.z);
-            if (a.w) h.odd = 1;
-            if (side_n) at = atomicAdd(&h.side_n, side_n);
-            if (b.x) hist_low(h, b.y, b.x);
+            for (int i = 0; i < kAhead; ++i) kept[j][i] = p[kHeader + 64 * i + lane];
         }
-        at = __builtin_amdgcn_readfirstlane(at);
-        if (lane < min(side_n, kSideMax) && at + lane < kSideMax) h.side[at + lane] = p[kHeader + kBins + lane];
+#pragma unroll
+        for (int j = 0; j < kTwo; ++j) {
+            const int c = c0 + j * kWaves + wave;
+            if (c >= C) break;
+            const uint32_t *p = src + (int64_t)c * kPartWords;
+            entries[j] = a[j].x;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (64 * i + lane < entries[j]) add(kept[j][i]);
+#pragma unroll 4
+            for (uint32_t i = 64 * kAhead + lane; i < entries[j]; i += 64) add(p[kHeader + i]);
+            const uint32_t side_n = a[j].y;
+            uint32_t at = 0;
+            if (lane == 0) {
+                if (a[j].z) atomicAdd(&h.zeros, a[j].z);
+                if (a[j].w) h.odd = 1;
+                if (side_n) at = atomicAdd(&h.side_n, side_n);
+                if (b[j].x) hist_low(h, b[j].y, b[j].x);
+            }
+            at = __builtin_amdgcn_readfirstlane(at);
+            if (lane < min(side_n, kSideMax) && at + lane < kSideMax) h.side[at + lane] = p[kHeader + kBins + lane];
+        }
     }
     __syncthreads();
     const Drawn d = draw_row(sh, row, par, m);
@@ -788,23 +854,31 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             // part's entries ascend by place: 64 samples, then the stretch between two.
             // (Zero, smaller and low values and the long way have no counts by part.)
             const uint32_t want = bin_order((d.bits >> 15) * kBinsHalf + q);
-            for (int c = wave; c < C; c += kWaves) {
-                const uint32_t *p = src + (int64_t)c * kPartWords;
-                const uint32_t entries = p[0], stride = (entries + 63) / 64;
-                p += kHeader;
-                const uint32_t i0 = lane * stride;
-                const bool le = i0 < entries && (p[i0] >> kCountBits) <= want;
-                const int hit = __popcll(__ballot(le));  // samples at or before it
+            for (int c = wave, j = 0; c < C; c += kWaves, ++j) {
                 uint32_t n = 0;
-                if (hit)
-                    for (uint32_t i = lane; i < stride; i += 64) {
-                        const uint32_t at = (hit - 1) * stride + i;
-                        const uint32_t e = at < entries ? p[at] : ~0u;
-                        if ((e >> kCountBits) == want) n = e & kCountMask;
-                    }
+                if (C <= kTwo * kWaves && (j ? entries[1] : entries[0]) <= 64 * kAhead) {
 #pragma unroll
-                for (int x = 1; x < 64; x <<= 1) n += __shfl_xor(n, x);
-                if (lane == 0) in_part[c] = n;
+                    for (int i = 0; i < kAhead; ++i) {
+                        const uint32_t e = j ? kept[1][i] : kept[0][i];
+                        if (64 * i + lane < (j ? entries[1] : entries[0]) && (e >> kCountBits) == want) n = e & kCountMask;
+                    }
+                } else {
+                    const uint32_t *p = src + (int64_t)c * kPartWords;
+                    const uint32_t count = p[0], stride = (count + 63) / 64;
+                    p += kHeader;
+                    const uint32_t i0 = lane * stride;
+                    const bool le = i0 < count && (p[i0] >> kCountBits) <= want;
+                    const int hit = __popcll(__ballot(le));  // samples at or before it
+                    if (hit)
+                        for (uint32_t i = lane; i < stride; i += 64) {
+                            const uint32_t at = (hit - 1) * stride + i;
+                            const uint32_t e = at < count ? p[at] : ~0u;
+                            if ((e >> kCountBits) == want) n = e & kCountMask;
+                        }
+                }
+                const uint64_t has = __ballot(n != 0);  // one lane at most
+                if (lane == 0) in_part[c] = 0;
+                if (has && lane == __builtin_ctzll(has)) in_part[c] = n;
             }
             __syncthreads();
             int part = 0;
@@ -882,6 +956,10 @@ hipError_t launch_sample(const SamplePlan &p, const void *logits, int64_t ld, co
     const uint16_t *l = (const uint16_t *)logits;
     if (p.parts == 1) {
         hipLaunchKernelGGL(sample_row_kernel, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par, tokens, logprobs,
+                           (int)V);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par, tokens, logprobs,
                            (int)V);
         return hipGetLastError();
     }
