@@ -100,12 +100,24 @@ struct Params {
     const float *u, *temperature, *top_p, *min_p;
     const int32_t *top_k;
 };
-__device__ __forceinline__ bool is_greedy(const Params &p, int64_t m) { return p.temperature && !(p.temperature[m] > 0.f); }
-// Number of tokens top_k leaves (0: no limit).
-__device__ __forceinline__ uint32_t limit_of(const Params &p, int64_t m) {
-    if (is_greedy(p, m)) return 1;
-    const int k = p.top_k ? p.top_k[m] : 0;
-    return k > 0 ? (uint32_t)k : 0;
+// One row's parameters. Read where a kernel begins: the loads then pass behind the
+// reading of the logits.
+struct RowParams {
+    float u, top_p, min_p, temperature;
+    uint32_t k;  // tokens that top_k leaves (0: no limit)
+};
+__device__ __forceinline__ RowParams row_params(const Params &p, int64_t m) {
+    RowParams r{p.u[m], 1.f, 0.f, 1.f, 0};
+    int k = 0;
+    if (p.temperature) r.temperature = p.temperature[m];
+    if (p.top_k) k = p.top_k[m];
+    if (p.top_p) r.top_p = p.top_p[m];
+    if (p.min_p) r.min_p = p.min_p[m];
+    const bool greedy = !(r.temperature > 0.f);
+    r.k = greedy ? 1u : (k > 0 ? (uint32_t)k : 0u);
+    if (greedy) r.temperature = r.top_p = 1.f, r.min_p = 0.f;
+    r.u = r.u >= 0.f ? fminf(r.u, 0x1.fffffep-1f) : 0.f;  // [0, 1), NaN as 0
+    return r;
 }
 
 // ---- histogram of a row or of a part of it -------------------------------------------
@@ -226,6 +238,11 @@ __device__ __forceinline__ T wave_scan(T v) {
     v += dpp0<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
     return v;
 }
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, lane) |
+                                          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane) << 32);
+}
 // The value one lane down, 0 in lane 0.
 template <typename T>
 __device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
@@ -260,15 +277,14 @@ enum Seek { kMass, kTopP, kMinP, kDraw };
 // Draws from the whole row's histogram in sh.h, or window by window from the row itself.
 // Used by whole workgroups.
 template <bool longway>
-__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params &par, int64_t m) {
+__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par) {
     Hist &h = sh.h;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
     constexpr int windows = longway ? kWindows : 1;
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
-    const bool greedy = is_greedy(par, m);
     Weight wt;
     wt.max = 0.0;
-    wt.inv_t = greedy || !par.temperature ? 1.0 : 1.0 / (double)par.temperature[m];
+    wt.inv_t = 1.0 / (double)par.temperature;
     if (t < 8) sh.owner[t] = 0;
     if (t == 8) sh.first = ~0u;
     if (t == 9) {
@@ -305,7 +321,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
     __syncthreads();
 
     // this thread's bins, descending: patterns bits0, bits0 + dir, ...
-    uint32_t bits0 = 0, cnt[kOwn], c = 0, ec = 0;
+    uint32_t bits0 = 0, c = 0, ec = 0;
     int dir = 0, f = kOwn;        // f: its first occurring bin
     double wf = 0.0, ratio = 0.0, w = 0.0, ew = 0.0;  // that one's weight; W of the thread and before it
     int current = -1;
@@ -313,6 +329,16 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
     // Items of thread t after its bins: [item_b, item_e).
     const int item_b = t == kThreads - 1 ? kItems - 1 : 0;
     const int item_e = longway ? item_b : (t == kLastPositive ? sides : (t == kThreads - 1 ? kItems : 0));
+
+    // The thread's counts, in order.
+    auto counts = [&](uint32_t (&n)[kOwn]) {
+        const bool flip = !longway && t <= kLastPositive;
+        const uint4 *p = (const uint4 *)&h.bin[flip ? kBinsHalf - kOwn * (t + 1) : kOwn * t];
+        const uint4 a = p[flip ? 1 : 0], b = p[flip ? 0 : 1];
+        const uint32_t x[kOwn] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) n[j] = flip ? x[4 * (j / 4) + 3 - j % 4] : x[j];
+    };
 
     auto analyse = [&](int win) {
         // read before the barriers below, behind which it is set
@@ -340,19 +366,15 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
             const uint32_t key0 = 65535u - (uint32_t)win * kBins - kOwn * t;
             dir = key0 & 0x8000u ? -1 : 1;
             bits0 = key0 & 0x8000u ? key0 & 0x7FFFu : ~key0 & 0xFFFFu;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kOwn * t + j];
         } else if (t <= kLastPositive) {
             dir = -1;
             bits0 = kMagLo + kBinsHalf - 1 - kOwn * t;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kBinsHalf - 1 - kOwn * t - j];
         } else {
             dir = 1;
             bits0 = 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) cnt[j] = h.bin[kOwn * t + j];
         }
+        uint32_t cnt[kOwn];
+        counts(cnt);
         c = 0;
         f = kOwn;
 #pragma unroll
@@ -410,20 +432,19 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
         const uint32_t xc = wave_down(ic);
         const double xw = wave_down(iw);
         __syncthreads();
-        uint32_t bc = sh.win_count[win];
-        double bw = sh.win_mass[win];
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-            if (v == wave) {
-                ec = bc + xc;
-                ew = bw + xw;
-            }
-            bc += sh.csum[v];
-            bw += sh.wsum[v];
+        const uint32_t sc = wave_scan(lane < kWaves ? sh.csum[lane] : 0u);
+        const double sw = wave_scan(lane < kWaves ? sh.wsum[lane] : 0.0);
+        const uint32_t bc = sh.win_count[win];
+        const double bw = sh.win_mass[win];
+        ec = bc + xc;
+        ew = bw + xw;
+        if (wave) {
+            ec += __builtin_amdgcn_readlane(sc, wave - 1);
+            ew += lane_value(sw, wave - 1);
         }
         if (t == 0) {
-            sh.win_count[win + 1] = bc;
-            sh.win_mass[win + 1] = bw;
+            sh.win_count[win + 1] = bc + __builtin_amdgcn_readlane(sc, kWaves - 1);
+            sh.win_mass[win + 1] = bw + lane_value(sw, kWaves - 1);
         }
         // the weight of the window's first value, where it has any
         if (longway && c && ec == sh.win_count[win]) sh.win_first[win] = wf;
@@ -464,62 +485,57 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
         if (mask && lane == 0) atomicMax(&sh.owner[slot], (uint32_t)(wave * 64 + 64 - __builtin_clzll(mask)));
         __syncthreads();
         if (sh.owner[slot] == (uint32_t)t + 1) {
-            uint32_t pos = ec, bits = 0, ord = 0;
-            double before = ew, weight = wf;
-            bool done = false;
-            int j = f;
-            int i = item_b;
-            while (!done) {
-                uint32_t k, b;
-                double v;
-                if (j < kOwn) {
-                    k = longway ? h.bin[kOwn * t + j] : h.bin[t <= kLastPositive ? kBinsHalf - 1 - kOwn * t - j : kOwn * t + j];
-                    b = bits0 + dir * j;
-                    v = weight;
-                    weight *= ratio;
-                    ++j;
-                } else if (i < item_e) {
-                    k = sh.item_count[i];
-                    b = sh.item_bits[i];
-                    v = sh.item_weight[i];
-                    ++i;
-                } else break;
-                if (k == 0) continue;
-                if (mode != kTopP && mode != kMinP) {
-                    k = min(k, n - pos);  // no more than n tokens
-                    if (k == 0) break;
-                }
+            // the item that crosses, or else the last one with weight
+            uint32_t pos = ec, at_pos = ec, at_k = 0, at_bits = 0;
+            double before = ew, at_before = ew, at_v = 0.0;
+            bool crossed = false;
+            auto visit = [&](uint32_t k, uint32_t b, double v) {
+                if (k == 0 || crossed) return;
+                if (mode == kMass || mode == kDraw) k = min(k, n - pos);
                 const double end = before + k * v;
-                uint32_t part = k;
-                if (mode == kMinP) {
-                    done = v < x;
-                    if (done) part = 0;
-                } else if (mode == kTopP && end >= x) {
-                    // tokens whose W before them is below x
-                    const double y = v > 0.0 ? ceil((x - before) / v) : (double)k;
-                    part = y <= 0.0 ? 0 : (y >= (double)k ? k : (uint32_t)y);
-                    while (part > 0 && before + (part - 1) * v >= x) --part;
-                    while (part < k && before + part * v < x) ++part;
-                    done = true;
-                } else if (mode == kDraw) {
-                    if (v > 0.0 || pos == 0) {  // the last with weight, should rounding leave none crossing
-                        bits = b;
-                        ord = k - 1;
-                    }
-                    if (end > x) {
-                        const double y = (x - before) / v;
-                        ord = y <= 0.0 ? 0 : (y >= (double)k ? k - 1 : (uint32_t)y);
-                        while (ord > 0 && before + ord * v > x) --ord;
-                        while (ord + 1 < k && before + (ord + 1) * v <= x) ++ord;
-                        done = true;
-                    }
+                if (mode == kMass) crossed = pos + k >= n;
+                else if (mode == kTopP) crossed = end >= x;
+                else if (mode == kMinP) crossed = v < x;
+                else crossed = end > x;
+                if (crossed || mode != kDraw || v > 0.0 || at_k == 0) {
+                    at_pos = pos;
+                    at_before = before;
+                    at_k = k;
+                    at_v = v;
+                    at_bits = b;
                 }
-                pos += part;
-                before = part == k ? end : before + part * v;
+                crossed |= mode == kDraw && pos + k >= n;
+                pos += k;
+                before = end;
+            };
+            double weight = wf;
+            uint32_t cnt[kOwn];
+            counts(cnt);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                visit(cnt[j], bits0 + dir * j, weight);
+                if (j >= f) weight *= ratio;
             }
-            sh.found.pos = pos;
-            sh.found.mass = before;
-            sh.found.bits = bits;
+            for (int i = item_b; i < item_e; ++i) visit(sh.item_count[i], sh.item_bits[i], sh.item_weight[i]);
+            uint32_t part = at_k, ord = at_k ? at_k - 1 : 0;  // tokens of the item, or which of them
+            if (mode == kMinP) {
+                if (crossed) part = 0;
+            } else if (mode == kTopP || mode == kDraw) {
+                double y = at_v > 0.0 ? (x - at_before) / at_v : (double)at_k;
+                y = fmin(fmax(y, 0.0), (double)at_k);
+                if (mode == kTopP) {  // tokens whose W before them is below x
+                    part = (uint32_t)ceil(y);
+                    while (part > 0 && at_before + (part - 1) * at_v >= x) --part;
+                    while (part < at_k && at_before + part * at_v < x) ++part;
+                } else if (crossed && at_before + at_k * at_v > x) {
+                    ord = min((uint32_t)y, at_k - 1);
+                    while (ord > 0 && at_before + ord * at_v > x) --ord;
+                    while (ord + 1 < at_k && at_before + (ord + 1) * at_v <= x) ++ord;
+                }
+            }
+            sh.found.pos = at_pos + part;
+            sh.found.mass = at_before + part * at_v;
+            sh.found.bits = at_bits;
             sh.found.ord = ord;
         }
         __syncthreads();
@@ -527,10 +543,8 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
 
     uint32_t n = total;
     double mass = wtotal;
-    const uint32_t k = limit_of(par, m);
-    const float top_p = greedy || !par.top_p ? 1.f : par.top_p[m], min_p = greedy || !par.min_p ? 0.f : par.min_p[m];
-    float u = par.u[m];
-    u = u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;  // [0, 1), NaN as 0
+    const uint32_t k = par.k;
+    const float top_p = par.top_p, min_p = par.min_p;
     // W(n1), n2, n3 (each with its W) where they limit, the draw
 #pragma unroll 1
     for (int step = 0; step < 4; ++step) {
@@ -549,7 +563,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
             x = (double)min_p;
         } else {
             mode = kDraw;
-            x = (double)u * mass;
+            x = (double)par.u * mass;
         }
         seek(mode, n, x);
         const uint32_t pos = sh.found.pos;
@@ -567,13 +581,13 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const Params
     return out;
 }
 
-__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const Params &par, int64_t m) {
-    return draw_way<true>(sh, row, par, m);
+__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par) {
+    return draw_way<true>(sh, row, par);
 }
 
-__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const Params &par, int64_t m) {
-    if (sh.h.odd || sh.h.side_n > kSideMax) return draw_long(sh, row, par, m);
-    return draw_way<false>(sh, row, par, m);
+__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const RowParams &par) {
+    if (sh.h.odd || sh.h.side_n > kSideMax) return draw_long(sh, row, par);
+    return draw_way<false>(sh, row, par);
 }
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
@@ -621,12 +635,9 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
         sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
         if (lane == 0) sh.count[wave] = sum;
         __syncthreads();
-        uint32_t before = 0, all = 0;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-            if (v == wave) before = all;
-            all += sh.count[v];
-        }
+        const uint32_t scan = wave_scan(lane < kWaves ? sh.count[lane] : 0u);
+        const uint32_t all = __builtin_amdgcn_readlane((int)scan, kWaves - 1);
+        const uint32_t before = __builtin_amdgcn_readlane((int)scan, wave) - sum;
         if (left < all) {
             if (before <= left && left < before + sum) {  // in this wave's part
                 uint32_t skip = left - before;
@@ -676,6 +687,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
     __shared__ __attribute__((aligned(16))) Draw sh;
     const int64_t m = blockIdx.x;
     const Row row = make_row(logits + m * ld, V);
+    const RowParams rp = row_params(par, m);
     hist_clear(sh.h);
     __syncthreads();
     hist_count(sh.h, row, 0, row.nvec, true, true);
@@ -684,7 +696,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
         if (threadIdx.x == 0) tokens[m] = kLongWay;
         return;
     }
-    const Drawn d = draw_way<false>(sh, row, par, m);
+    const Drawn d = draw_way<false>(sh, row, rp);
     int token = -1;
     if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
     if (threadIdx.x == 0) {
@@ -700,7 +712,8 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
     const int64_t m = blockIdx.x;
     if (tokens[m] != kLongWay) return;
     const Row row = make_row(logits + m * ld, V);
-    const Drawn d = draw_way<true>(sh, row, par, m);
+    const RowParams rp = row_params(par, m);
+    const Drawn d = draw_way<true>(sh, row, rp);
     int token = -1;
     if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
     if (threadIdx.x == 0) {
@@ -725,6 +738,7 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     const int64_t m = blockIdx.x / C;
     const int part = blockIdx.x % C;
     const Row row = make_row(logits + m * ld, V);
+    const uint32_t k = row_params(par, m).k;
     hist_clear(h);
     if (threadIdx.x == 0) entries = 0;
     __syncthreads();
@@ -757,7 +771,6 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     }
     __syncthreads();
     uint32_t *dst = parts + ((int64_t)m * C + part) * kPartWords;
-    const uint32_t k = limit_of(par, m);
     const uint32_t middle = h.zeros + h.side_n;
     uint32_t run = 0;
 #pragma unroll
@@ -799,6 +812,7 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
     const Row row = make_row(logits + m * ld, V);
     const uint32_t *src = parts + (int64_t)m * C * kPartWords;
+    const RowParams rp = row_params(par, m);
     Hist &h = sh.h;
     hist_clear(h);
     __syncthreads();
@@ -842,7 +856,7 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
         }
     }
     __syncthreads();
-    const Drawn d = draw_row(sh, row, par, m);
+    const Drawn d = draw_row(sh, row, rp);
     int token = -1;
     if (d.any) {
         const uint32_t q = (d.bits & 0x7FFFu) - kMagLo;
@@ -882,7 +896,14 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             }
             __syncthreads();
             int part = 0;
-            while (part < C - 1 && left >= in_part[part]) left -= in_part[part++];
+            for (int c0 = 0; c0 < C; c0 += 64) {
+                const uint32_t inc = wave_scan(c0 + lane < C ? in_part[c0 + lane] : 0u);
+                const uint64_t past = __ballot(inc > left);
+                part = min(c0 + (past ? __builtin_ctzll(past) : 64), C - 1);
+                const uint32_t before = __builtin_amdgcn_readlane((int)inc, (past ? __builtin_ctzll(past) : 64) - 1 & 63);
+                if (!past || part > c0) left -= before;
+                if (past) break;
+            }
             vb = min(part * vpp, row.nvec);
             ve = min(vb + vpp, row.nvec);
             head = part == 0;
