@@ -24,6 +24,8 @@
 // (a mask value) are items of their own. Any other row is counted the long way:
 // eight windows of 8192 patterns, one scan of the row per window and step.
 #include <algorithm>
+#include <cstddef>
+#include <type_traits>
 
 #include "svq_launch.h"
 
@@ -124,6 +126,7 @@ __device__ __forceinline__ RowParams row_params(const Params &p, int64_t m) {
 
 struct Hist {
     uint32_t bin[kBins];
+    uint32_t none[64];            // where a lane's pair goes that is not counted here
     uint32_t side[kSideMax];
     uint32_t side_n, zeros, odd;  // odd: the row needs the long way
     uint32_t low_n, low_bits;     // tokens of the one pattern at or below -2^16
@@ -141,20 +144,26 @@ __device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
     atomicAdd(&h.low_n, n);
 }
 
-// Counts vectors [vb, ve) of a row. Two elements at a time: subtracting kMagLo from both
+// Counts vectors [vb, ve) of a row into `table` (h.bin, or a table with the same words
+// behind it), adding `inc` a token. Two elements at a time: subtracting kMagLo from both
 // halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14 say that
-// the magnitude has a bin (9 vector instructions and 2 LDS additions for two elements).
-// A vector with anything else is read again by a loop of its own, which keeps the code of
-// the common case short; pairs of -inf, which can be most of a row, are nothing else.
-// Zeros and mask values are counted in registers.
-__device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve, bool head, bool tail) {
+// the magnitude has a bin: ten vector instructions and two LDS additions for two elements,
+// without a branch (pairs that are not plain are counted in a word of the lane's own,
+// which nobody reads). A vector with such a pair is read again by a loop of its own, but
+// for pairs of -inf, which can be most of a row. Zeros and mask values are counted in
+// registers.
+__device__ __forceinline__ void hist_count(Hist &h, uint32_t *table, uint32_t inc, const Row &r, int vb, int ve, bool head,
+                                           bool tail) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    static_assert(offsetof(Hist, none) == kBins * 4 && offsetof(Hist, bin) == 0, "the lanes' own words follow the bins");
+    constexpr uint32_t kNoBin = 0x70007000u, kPairOfInf = 0xFF80FF80u;
     uint32_t zeros = 0, low_n = 0, low_bits = 0;
-    char *base = (char *)h.bin;
+    char *base = (char *)table;
+    const uint32_t none = (0x8000u + 4 * (threadIdx.x & 63)) * 0x10001u;
     auto single = [&](uint32_t b) {
         const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
         if (q < kBinsHalf) {
-            atomicAdd(&h.bin[(b >> 15) * kBinsHalf + q], 1u);
+            atomicAdd(&table[(b >> 15) * kBinsHalf + q], inc);
         } else if (mag == 0) {
             ++zeros;
         } else if (mag < kMagLo) {
@@ -170,24 +179,24 @@ __device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve
     };
     auto plain = [](uint32_t w) {
         const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo};
-        return __builtin_bit_cast(uint32_t, (u16x2)(__builtin_bit_cast(u16x2, w) - lo));
+        return __builtin_bit_cast(u16x2, w) - lo;
     };
-    // counts the pair if both have bins; whether something is left to do
-    auto pair = [&](uint32_t w) -> bool {
-        const uint32_t t = plain(w);
-        if ((t & 0x70007000u) == 0) {
-            const uint32_t a = ((t << 2) & 0x3FFC3FFCu) | ((t >> 1) & 0x40004000u);
-            atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), 1u);
-            atomicAdd((uint32_t *)(base + (a >> 16)), 1u);
-            return false;
-        }
-        return w != 0xFF80FF80u;
+    // counts the pair if both have bins; the bits that say it has not
+    auto pair = [&](uint32_t w) -> uint32_t {
+        const u16x2 t = plain(w);
+        const uint32_t tt = __builtin_bit_cast(uint32_t, t), bad = tt & kNoBin;
+        uint32_t a = __builtin_bit_cast(uint32_t, (u16x2)(t << 2)) | ((tt >> 1) & 0x40004000u);
+        a = bad ? none : a;
+        atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), inc);
+        atomicAdd((uint32_t *)(base + (a >> 16)), inc);
+        return bad;
     };
+    auto odd_word = [&](uint32_t w) { return (__builtin_bit_cast(uint32_t, plain(w)) & kNoBin) != 0 && w != kPairOfInf; };
     auto rest = [&](int v) {
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const uint32_t w = *(const uint32_t *)(r.p + r.head + (int64_t)v * 8 + 2 * i);
-            if ((plain(w) & 0x70007000u) != 0 && w != 0xFF80FF80u) {
+            if (odd_word(w)) {
                 single(w & 0xFFFFu);
                 single(w >> 16);
             }
@@ -201,11 +210,11 @@ __device__ __forceinline__ void hist_count(Hist &h, const Row &r, int vb, int ve
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
             q[i] = v + i * kThreads < ve ? row_vec(r, v + i * kThreads)
-                                         : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+                                         : make_uint4(kPairOfInf, kPairOfInf, kPairOfInf, kPairOfInf);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t left = (uint32_t)pair(q[i].x) | (uint32_t)pair(q[i].y) | (uint32_t)pair(q[i].z) | (uint32_t)pair(q[i].w);
-            todo |= left << i;
+            const uint32_t bad = pair(q[i].x) | pair(q[i].y) | pair(q[i].z) | pair(q[i].w);
+            if (bad && (odd_word(q[i].x) || odd_word(q[i].y) || odd_word(q[i].z) || odd_word(q[i].w))) todo |= 1u << i;
         }
         for (; todo; todo &= todo - 1) rest(v + (__builtin_ctz(todo)) * kThreads);
     }
@@ -266,6 +275,12 @@ struct Draw {
     Found found;
 };
 
+// A row's quarters: the second of two tables, where a kernel has one.
+struct DrawQuarters : Draw {
+    uint32_t bin2[kBins + 64];  // the first and second quarter are in bin, the others here
+};
+__device__ __forceinline__ uint32_t *second_table(Draw &sh) { return static_cast<DrawQuarters &>(sh).bin2; }
+
 struct Drawn {
     uint32_t bits, ordinal;
     float logprob;
@@ -274,12 +289,16 @@ struct Drawn {
 
 enum Seek { kMass, kTopP, kMinP, kDraw };
 
-// Draws from the whole row's histogram in sh.h, or window by window from the row itself.
-// Used by whole workgroups.
-template <bool longway>
+// How a row is counted: whole rows in h.bin; their quarters apart, 16 bits each, in h.bin
+// and a table behind it; or window by window from the row itself.
+enum Way { kWhole, kQuarters, kLong };
+
+// Draws a token's value and its ordinal. Used by whole workgroups.
+template <Way way>
 __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par) {
     Hist &h = sh.h;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
+    constexpr bool longway = way == kLong;
     constexpr int windows = longway ? kWindows : 1;
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
     Weight wt;
@@ -333,8 +352,16 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     // The thread's counts, in order.
     auto counts = [&](uint32_t (&n)[kOwn]) {
         const bool flip = !longway && t <= kLastPositive;
-        const uint4 *p = (const uint4 *)&h.bin[flip ? kBinsHalf - kOwn * (t + 1) : kOwn * t];
-        const uint4 a = p[flip ? 1 : 0], b = p[flip ? 0 : 1];
+        const int first = flip ? kBinsHalf - kOwn * (t + 1) : kOwn * t;
+        const uint4 *p = (const uint4 *)&h.bin[first];
+        uint4 a = p[flip ? 1 : 0], b = p[flip ? 0 : 1];
+        if constexpr (way == kQuarters) {
+            const uint4 *p2 = (const uint4 *)&second_table(sh)[first];
+            const uint4 a2 = p2[flip ? 1 : 0], b2 = p2[flip ? 0 : 1];
+            auto sum = [](uint32_t u, uint32_t v) { return (u & 0xFFFFu) + (u >> 16) + (v & 0xFFFFu) + (v >> 16); };
+            a = make_uint4(sum(a.x, a2.x), sum(a.y, a2.y), sum(a.z, a2.z), sum(a.w, a2.w));
+            b = make_uint4(sum(b.x, b2.x), sum(b.y, b2.y), sum(b.z, b2.z), sum(b.w, b2.w));
+        }
         const uint32_t x[kOwn] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) n[j] = flip ? x[4 * (j / 4) + 3 - j % 4] : x[j];
@@ -582,12 +609,12 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
 }
 
 __device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par) {
-    return draw_way<true>(sh, row, par);
+    return draw_way<kLong>(sh, row, par);
 }
 
 __device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const RowParams &par) {
     if (sh.h.odd || sh.h.side_n > kSideMax) return draw_long(sh, row, par);
-    return draw_way<false>(sh, row, par);
+    return draw_way<kWhole>(sh, row, par);
 }
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
@@ -612,6 +639,16 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
         }
         left -= n;
     }
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t want2 = bits * 0x10001u, mask2 = mask16 * 0x10001u;
+    auto differ = [&](uint32_t x) {  // per half: 0 if it is the value, else 1
+        const u16x2 d = __builtin_bit_cast(u16x2, (x ^ want2) & mask2), one = {1, 1};
+        return __builtin_elementwise_min(d, one);
+    };
+    auto misses = [&](const uint4 &q) -> uint32_t {  // elements that are not the value, 0..8
+        const u16x2 d = differ(q.x) + differ(q.y) + differ(q.z) + differ(q.w);
+        return (uint32_t)d.x + (uint32_t)d.y;
+    };
     auto matches = [&](const uint4 &q) {  // one bit per element
         uint32_t n = 0;
 #pragma unroll
@@ -625,12 +662,17 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
     constexpr int kBlock = kThreads * kIter;    // vectors
     for (int b0 = vb; b0 < ve; b0 += kBlock) {
         const int w0 = b0 + wave * 64 * kIter;
+        uint4 q[kIter];
         uint32_t eq[kIter], sum = 0;
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
             const int v = w0 + i * 64 + lane;
-            eq[i] = v < ve ? matches(row_vec(r, v)) : 0;
-            sum += __builtin_popcount(eq[i]);
+            q[i] = row_vec(r, min(v, ve - 1));
+        }
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            eq[i] = w0 + i * 64 + lane < ve ? 8 - misses(q[i]) : 0;
+            sum += eq[i];
         }
         sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
         if (lane == 0) sh.count[wave] = sum;
@@ -645,11 +687,12 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
                 for (int i = 0; i < kIter; ++i)
                     for (uint64_t mask = __ballot(eq[i] != 0); mask; mask &= mask - 1) {
                         const int owner = __builtin_ctzll(mask);
-                        uint32_t bitsq = __builtin_amdgcn_readlane(eq[i], owner);
-                        const uint32_t n = __builtin_popcount(bitsq);
+                        const uint32_t n = __builtin_amdgcn_readlane((int)eq[i], owner);
                         if (skip < n) {
-                            for (; skip; --skip) bitsq &= bitsq - 1;
-                            if (lane == 0) sh.at = r.head + (w0 + i * 64 + owner) * 8 + __builtin_ctz(bitsq);
+                            const int v = w0 + i * 64 + owner;
+                            uint32_t in = matches(row_vec(r, v));
+                            for (; skip; --skip) in &= in - 1;
+                            if (lane == 0) sh.at = r.head + v * 8 + __builtin_ctz(in);
                             skip = ~0u;  // found: no later vector has that many
                             break;
                         }
@@ -677,28 +720,59 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
 // ---- kernels ------------------------------------------------------------------------------
 
 // One workgroup per row: count, draw, find. Two workgroups share a compute unit (64
-// registers), so one's draw runs beside the other's reading; rows that need the long way
-// are marked and left to a launch of their own, whose workgroups otherwise end at once.
+// registers), so one's draw runs beside the other's reading. The row's quarters are
+// counted apart, which tells where to look for the occurrence: reading half a row again,
+// as a search from its beginning does on average, took a third of the time. Rows that
+// need the long way are marked and left to a launch of their own, whose workgroups
+// otherwise end at once.
 constexpr int kLongWay = -2;
+constexpr int64_t kMaxQuarter = 65535 / 8 - 2;  // vectors: a quarter's tokens fit 16 bits
 
+template <Way way>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))) void sample_row_kernel(
     const uint16_t *__restrict__ logits, int64_t ld, Params par, int32_t *__restrict__ tokens,
     float *__restrict__ logprobs, int V) {
-    __shared__ __attribute__((aligned(16))) Draw sh;
+    __shared__ __attribute__((aligned(16))) std::conditional_t<way == kQuarters, DrawQuarters, Draw> sh;
     const int64_t m = blockIdx.x;
     const Row row = make_row(logits + m * ld, V);
     const RowParams rp = row_params(par, m);
+    const int quarter = (row.nvec + 3) / 4;
     hist_clear(sh.h);
-    __syncthreads();
-    hist_count(sh.h, row, 0, row.nvec, true, true);
+    if constexpr (way == kQuarters) {
+        for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)sh.bin2)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q)
+            hist_count(sh.h, q & 2 ? sh.bin2 : sh.h.bin, q & 1 ? 0x10000u : 1u, row, min(q * quarter, row.nvec),
+                       min((q + 1) * quarter, row.nvec), q == 0, q == 3);
+    } else {
+        __syncthreads();
+        hist_count(sh.h, sh.h.bin, 1, row, 0, row.nvec, true, true);
+    }
     __syncthreads();
     if (sh.h.odd || sh.h.side_n > kSideMax) {
         if (threadIdx.x == 0) tokens[m] = kLongWay;
         return;
     }
-    const Drawn d = draw_way<false>(sh, row, rp);
+    const Drawn d = draw_way<way>(sh, row, rp);
     int token = -1;
-    if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
+    if (d.any) {
+        const uint32_t mag = (d.bits & 0x7FFFu) - kMagLo;
+        int vb = 0, ve = row.nvec, q = -1;
+        uint32_t left = d.ordinal;
+        if constexpr (way == kQuarters)
+            if (mag < kBinsHalf) {
+                const uint32_t bin = (d.bits >> 15) * kBinsHalf + mag, u = sh.h.bin[bin], v = sh.bin2[bin];
+                for (q = 0; q < 3; ++q) {
+                    const uint32_t x = q & 2 ? v : u, n = q & 1 ? x >> 16 : x & 0xFFFFu;
+                    if (left < n) break;
+                    left -= n;
+                }
+                vb = min(q * quarter, row.nvec);
+                ve = min((q + 1) * quarter, row.nvec);
+            }
+        token = locate(sh, row, vb, ve, q <= 0, q < 0 || q == 3, d.bits, left);
+    }
     if (threadIdx.x == 0) {
         tokens[m] = token;
         if (logprobs) logprobs[m] = d.logprob;
@@ -713,7 +787,7 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
     if (tokens[m] != kLongWay) return;
     const Row row = make_row(logits + m * ld, V);
     const RowParams rp = row_params(par, m);
-    const Drawn d = draw_way<true>(sh, row, rp);
+    const Drawn d = draw_way<kLong>(sh, row, rp);
     int token = -1;
     if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
     if (threadIdx.x == 0) {
@@ -743,7 +817,7 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     if (threadIdx.x == 0) entries = 0;
     __syncthreads();
     const int vb = min(part * vpp, row.nvec), ve = min(vb + vpp, row.nvec);
-    hist_count(h, row, vb, ve, part == 0, part == C - 1);
+    hist_count(h, h.bin, 1, row, vb, ve, part == 0, part == C - 1);
     __syncthreads();
     // occurring bins in descending order, but none behind which top_k tokens of this
     // part already stand; (bins << 18 | tokens) are scanned in one word
@@ -817,32 +891,37 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     hist_clear(h);
     __syncthreads();
     auto add = [&](uint32_t e) { atomicAdd(&h.bin[bin_order(e >> kCountBits)], e & kCountMask); };
-    // A wave takes two parts at once, and keeps the first kAhead entries of a lane for the
-    // search below (all there are, as a rule, where top_k limits them).
+    // A wave takes two parts at once (or, of few parts, several waves share one), and keeps
+    // the first kAhead entries of a lane for the search below (all there are, as a rule,
+    // where top_k limits them).
     constexpr int kAhead = 4, kTwo = 2;
+    const int shared = C < kWaves ? kWaves / C : 1;  // waves on one part
+    const int first = C < kWaves ? wave % C : wave, sub = C < kWaves ? wave / C : 0;
+    const uint32_t lane0 = sub * 64 + lane, step = shared * 64;
     uint32_t kept[kTwo][kAhead], entries[kTwo] = {0, 0};
     for (int c0 = 0; c0 < C; c0 += kTwo * kWaves) {
         uint4 a[kTwo], b[kTwo];
 #pragma unroll
         for (int j = 0; j < kTwo; ++j) {
-            const int c = min(c0 + j * kWaves + wave, C - 1);
+            const int c = min(c0 + j * kWaves + first, C - 1);
             const uint32_t *p = src + (int64_t)c * kPartWords;
             a[j] = ((const uint4 *)p)[0];
             b[j] = ((const uint4 *)p)[1];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) kept[j][i] = p[kHeader + 64 * i + lane];
+            for (int i = 0; i < kAhead; ++i) kept[j][i] = p[kHeader + min(step * i + lane0, kBins - 1)];
         }
 #pragma unroll
         for (int j = 0; j < kTwo; ++j) {
-            const int c = c0 + j * kWaves + wave;
-            if (c >= C) break;
+            const int c = c0 + j * kWaves + first;
+            if (c >= C || sub >= shared) break;
             const uint32_t *p = src + (int64_t)c * kPartWords;
             entries[j] = a[j].x;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (64 * i + lane < entries[j]) add(kept[j][i]);
+                if (step * i + lane0 < entries[j]) add(kept[j][i]);
 #pragma unroll 4
-            for (uint32_t i = 64 * kAhead + lane; i < entries[j]; i += 64) add(p[kHeader + i]);
+            for (uint32_t i = step * kAhead + lane0; i < entries[j]; i += step) add(p[kHeader + i]);
+            if (sub) continue;
             const uint32_t side_n = a[j].y;
             uint32_t at = 0;
             if (lane == 0) {
@@ -855,6 +934,7 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             if (lane < min(side_n, kSideMax) && at + lane < kSideMax) h.side[at + lane] = p[kHeader + kBins + lane];
         }
     }
+    for (int c = t; c < C; c += kThreads) in_part[c] = 0;
     __syncthreads();
     const Drawn d = draw_row(sh, row, rp);
     int token = -1;
@@ -868,15 +948,16 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             // part's entries ascend by place: 64 samples, then the stretch between two.
             // (Zero, smaller and low values and the long way have no counts by part.)
             const uint32_t want = bin_order((d.bits >> 15) * kBinsHalf + q);
-            for (int c = wave, j = 0; c < C; c += kWaves, ++j) {
+            for (int c = first, j = 0; c < C && sub < shared; c += kWaves, ++j) {
                 uint32_t n = 0;
-                if (C <= kTwo * kWaves && (j ? entries[1] : entries[0]) <= 64 * kAhead) {
+                const uint32_t count = C <= kTwo * kWaves ? (j ? entries[1] : entries[0]) : ~0u;
+                if (count <= step * kAhead) {
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) {
                         const uint32_t e = j ? kept[1][i] : kept[0][i];
-                        if (64 * i + lane < (j ? entries[1] : entries[0]) && (e >> kCountBits) == want) n = e & kCountMask;
+                        if (step * i + lane0 < count && (e >> kCountBits) == want) n = e & kCountMask;
                     }
-                } else {
+                } else if (sub == 0) {
                     const uint32_t *p = src + (int64_t)c * kPartWords;
                     const uint32_t count = p[0], stride = (count + 63) / 64;
                     p += kHeader;
@@ -890,9 +971,7 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
                             if ((e >> kCountBits) == want) n = e & kCountMask;
                         }
                 }
-                const uint64_t has = __ballot(n != 0);  // one lane at most
-                if (lane == 0) in_part[c] = 0;
-                if (has && lane == __builtin_ctzll(has)) in_part[c] = n;
+                if (n) in_part[c] = n;  // one lane at most
             }
             __syncthreads();
             int part = 0;
@@ -976,8 +1055,12 @@ hipError_t launch_sample(const SamplePlan &p, const void *logits, int64_t ld, co
     const Params par{u, temperature, top_p, min_p, top_k};
     const uint16_t *l = (const uint16_t *)logits;
     if (p.parts == 1) {
-        hipLaunchKernelGGL(sample_row_kernel, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par, tokens, logprobs,
-                           (int)V);
+        if (V / 8 + 1 <= 4 * kMaxQuarter)
+            hipLaunchKernelGGL(sample_row_kernel<kQuarters>, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,
+                               tokens, logprobs, (int)V);
+        else
+            hipLaunchKernelGGL(sample_row_kernel<kWhole>, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,
+                               tokens, logprobs, (int)V);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par, tokens, logprobs,
