@@ -252,6 +252,12 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
     return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)u, lane) |
                                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane) << 32);
 }
+// A value that every lane has, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ double uniform(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)uniform((uint32_t)u) | (uint64_t)uniform((uint32_t)(u >> 32)) << 32);
+}
 // The value one lane down, 0 in lane 0.
 template <typename T>
 __device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
@@ -289,6 +295,11 @@ struct Drawn {
 
 enum Seek { kMass, kTopP, kMinP, kDraw };
 
+// The next double below a positive one; of others, a negative number.
+__device__ __forceinline__ double below(double x) {
+    return x > 0.0 ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, x) - 1) : -1.0;
+}
+
 // How a row is counted: whole rows in h.bin; their quarters apart, 16 bits each, in h.bin
 // and a table behind it; or window by window from the row itself.
 enum Way { kWhole, kQuarters, kLong };
@@ -303,7 +314,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
     Weight wt;
     wt.max = 0.0;
-    wt.inv_t = 1.0 / (double)par.temperature;
+    wt.inv_t = uniform(1.0 / (double)par.temperature);
     if (t < 8) sh.owner[t] = 0;
     if (t == 8) sh.first = ~0u;
     if (t == 9) {
@@ -418,7 +429,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             const uint64_t mask = __ballot(place != ~0u);  // places ascend with the lane
             if (mask && lane == __builtin_ctzll(mask)) atomicMin(&sh.first, place);
             __syncthreads();
-            const uint32_t first = sh.first;
+            const uint32_t first = uniform(sh.first);
             if (first != ~0u) {
                 const uint32_t ft = first >> 7, fj = first & 127;
                 if (fj >= kOwn) wt.max = value_of(sh.item_bits[fj - kOwn]);
@@ -427,6 +438,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
                     wt.max = value_of(key & 0x8000u ? key & 0x7FFFu : ~key & 0xFFFFu);
                 } else if (ft <= kLastPositive) wt.max = value_of(kMagLo + kBinsHalf - 1 - kOwn * ft - fj);
                 else wt.max = value_of(0x8000u | (kMagLo + kOwn * (ft - kLastPositive - 1) + fj));
+                wt.max = uniform(wt.max);
                 // the items' weights, one a thread
                 if (t < kItems && sh.item_count[t]) sh.item_weight[t] = wt(sh.item_bits[t]);
             }
@@ -480,8 +492,8 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     };
 
     for (int win = 0; win < windows; ++win) analyse(win);
-    const uint32_t total = sh.win_count[windows];
-    const double wtotal = sh.win_mass[windows];
+    const uint32_t total = uniform(sh.win_count[windows]);
+    const double wtotal = uniform(sh.win_mass[windows]);
     if (total == 0) return out;  // nothing to draw from
     out.any = true;
 
@@ -512,37 +524,41 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
         if (mask && lane == 0) atomicMax(&sh.owner[slot], (uint32_t)(wave * 64 + 64 - __builtin_clzll(mask)));
         __syncthreads();
         if (sh.owner[slot] == (uint32_t)t + 1) {
-            // the item that crosses, or else the last one with weight
+            // the item that crosses, or else the last one with weight: the first whose
+            // measure (tokens, W, or less its weight) exceeds the bound
+            const double bound = mode == kMass ? (double)n - 0.5 : (mode == kTopP ? below(x) : (mode == kMinP ? -x : x));
             uint32_t pos = ec, at_pos = ec, at_k = 0, at_bits = 0;
             double before = ew, at_before = ew, at_v = 0.0;
             bool crossed = false;
             auto visit = [&](uint32_t k, uint32_t b, double v) {
-                if (k == 0 || crossed) return;
-                if (mode == kMass || mode == kDraw) k = min(k, n - pos);
+                k = min(k, n - pos);  // no more than n tokens
+                const bool live = k != 0 && !crossed;
                 const double end = before + k * v;
-                if (mode == kMass) crossed = pos + k >= n;
-                else if (mode == kTopP) crossed = end >= x;
-                else if (mode == kMinP) crossed = v < x;
-                else crossed = end > x;
-                if (crossed || mode != kDraw || v > 0.0 || at_k == 0) {
+                const double measure = mode == kMass ? (double)(pos + k) : (mode == kMinP ? -v : end);
+                const bool over = measure > bound;
+                if (live && (over || v > 0.0 || at_k == 0)) {
                     at_pos = pos;
                     at_before = before;
                     at_k = k;
                     at_v = v;
                     at_bits = b;
                 }
-                crossed |= mode == kDraw && pos + k >= n;
-                pos += k;
-                before = end;
+                if (live) {
+                    pos += k;
+                    before = end;
+                    crossed = over;
+                }
             };
-            double weight = wf;
+            double weight = wf, by = ratio;
+            asm volatile("" : "+v"(weight), "+v"(by));  // not computed ahead of the steps that need it
             uint32_t cnt[kOwn];
             counts(cnt);
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
                 visit(cnt[j], bits0 + dir * j, weight);
-                if (j >= f) weight *= ratio;
+                if (j >= f) weight *= by;
             }
+#pragma unroll 1
             for (int i = item_b; i < item_e; ++i) visit(sh.item_count[i], sh.item_bits[i], sh.item_weight[i]);
             uint32_t part = at_k, ord = at_k ? at_k - 1 : 0;  // tokens of the item, or which of them
             if (mode == kMinP) {
@@ -554,7 +570,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
                     part = (uint32_t)ceil(y);
                     while (part > 0 && at_before + (part - 1) * at_v >= x) --part;
                     while (part < at_k && at_before + part * at_v < x) ++part;
-                } else if (crossed && at_before + at_k * at_v > x) {
+                } else if (crossed) {
                     ord = min((uint32_t)y, at_k - 1);
                     while (ord > 0 && at_before + ord * at_v > x) --ord;
                     while (ord + 1 < at_k && at_before + (ord + 1) * at_v <= x) ++ord;
@@ -593,17 +609,17 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             x = (double)par.u * mass;
         }
         seek(mode, n, x);
-        const uint32_t pos = sh.found.pos;
+        const uint32_t pos = uniform(sh.found.pos);
         if (mode == kMass) {
-            mass = sh.found.mass;
+            mass = uniform(sh.found.mass);
         } else if (mode != kDraw && pos < n) {
             n = max(pos, 1u);
-            mass = pos ? sh.found.mass : 1.0;  // the first token's weight
+            mass = pos ? uniform(sh.found.mass) : 1.0;  // the first token's weight
         }
         __syncthreads();
     }
-    out.bits = sh.found.bits;
-    out.ordinal = sh.found.ord;
+    out.bits = uniform(sh.found.bits);
+    out.ordinal = uniform(sh.found.ord);
     out.logprob = (float)(wt.exponent(out.bits) - log(mass));
     return out;
 }
