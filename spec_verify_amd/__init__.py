@@ -531,60 +531,77 @@ def ct_to_gptq(weight_packed, weight_scale, group_size=128, qweight=None, scales
 
 
 # ---- per-request operators of a verify chunk ----------------------------------------
+# Calls of a few microseconds: arguments are looked at once, and passed as integers.
 
-def _typed(t, name, kinds, shape, device):
-    """Device pointer of a contiguous tensor of one of the dtypes `kinds`, of the
-    given shape, on `device`."""
+def _ptr(t, name, dtypes, shape, device):
+    """Address of a contiguous tensor of one of `dtypes`, of the given shape, on `device`."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in kinds:
-        raise TypeError(f"{name} must be {' or '.join(str(k) for k in kinds)}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return _dev_ptr(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _row_matrix(t, name, kinds):
-    """(pointer, row stride) of a matrix whose rows are contiguous and apart."""
+def _rows_of(t, name, dtypes):
+    """(address, row stride) of a device matrix whose rows are contiguous and apart."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
-    if t.dtype not in kinds:
-        raise TypeError(f"{name} must be {' or '.join(str(k) for k in kinds)}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor, got {t.device}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    by_row, by_col = t.stride()
+    if cols > 1 and by_col != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
+    if rows <= 1:
+        return t.data_ptr(), cols
+    if by_row < cols:
         raise ValueError(f"{name}'s rows overlap")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), by_row
 
 
-def _bf16_kinds():
+def _bf16_dtypes():
     torch = _torch()
     return (torch.bfloat16, torch.int16, torch.uint16)
 
 
+def _on_device(device, call):
+    """call(stream handle) with `device` current: the library launches on the current device."""
+    torch = _torch()
+    index = device.index
+    # the handle alone where PyTorch offers it: a Stream object takes 2.7 us to make
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if torch.cuda.current_device() == index:
+        return call(raw(index) if raw else torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return call(raw(index) if raw else torch.cuda.current_stream(device).cuda_stream)
+
+
 def _scratch(nbytes, workspace, device):
-    """(pointer, bytes) of the caller's workspace, or of one from PyTorch's allocator
-    on the current stream: it need not be cleared, no other call shares it, and a
-    call that is captured gets its own from the graph's pool. Also returns the
-    tensor, which the caller keeps until the launch is enqueued."""
+    """The caller's workspace, or one from PyTorch's allocator on the current stream: it
+    need not be cleared, no other call shares it, and a call that is captured gets its own
+    from the graph's pool. (tensor, address, bytes); the caller keeps the tensor until the
+    launch is enqueued."""
     torch = _torch()
     if workspace is None:
         if nbytes == 0:
-            return None, 0, None
+            return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
-    return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+        return workspace, workspace.data_ptr(), nbytes
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def adapter_workspace_bytes(M, N, K, R, slots) -> int:
@@ -603,28 +620,34 @@ def adapter_add(base, x, a, b, rows, scales, out=None, workspace=None):
     matrices, and out may be base itself.
     """
     torch = _torch()
-    kinds = _bf16_kinds()
-    base_ptr, ld_base = _row_matrix(base, "base", kinds)
+    bf16 = _bf16_dtypes()
+    base_ptr, ld_base = _rows_of(base, "base", bf16)
     dev = base.device
     M, N = base.shape
     if x.dim() != 2 or a.dim() != 3:
         raise ValueError("x must be [M, K] and a [slots, R, K]")
     K = x.shape[1]
-    slots, R = a.shape[0], a.shape[1]
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        out_ptr, ld_out = _row_matrix(out, "out", kinds)
-        if tuple(out.shape) != (M, N) or out.device != dev:
+    slots, R, _ = a.shape
+    x_ptr = _ptr(x, "x", bf16, (M, K), dev)
+    a_ptr = _ptr(a, "a", bf16, (slots, R, K), dev)
+    b_ptr = _ptr(b, "b", bf16, (slots, N, R), dev)
+    rows_ptr = _ptr(rows, "rows", (torch.int32,), (M,), dev)
+    scales_ptr = _ptr(scales, "scales", (torch.float32,), (slots,), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out_ptr, ld_out = out.data_ptr(), N
+    else:
+        out_ptr, ld_out = _rows_of(out, "out", bf16)
+        if out.shape != (M, N) or out.device != dev:
             raise ValueError(f"out must have shape {(M, N)} on {dev}")
-        nbytes = adapter_workspace_bytes(M, N, K, R, slots)
-        ws_ptr, ws_bytes, keep = _scratch(nbytes, workspace, dev)
-        _check(lib().svq_adapter_add(base_ptr, ld_base, _typed(x, "x", kinds, (M, K), dev),
-                                     _typed(a, "a", kinds, (slots, R, K), dev),
-                                     _typed(b, "b", kinds, (slots, N, R), dev),
-                                     _typed(rows, "rows", (torch.int32,), (M,), dev),
-                                     _typed(scales, "scales", (torch.float32,), (slots,), dev), out_ptr, ld_out,
-                                     M, N, K, R, slots, ws_ptr, ws_bytes, _stream_ptr(base)), "svq_adapter_add")
+
+    def call(stream):
+        need = 0 if workspace is not None else adapter_workspace_bytes(M, N, K, R, slots)
+        keep, ws, ws_bytes = _scratch(need, workspace, dev)
+        _check(lib().svq_adapter_add(base_ptr, ld_base, x_ptr, a_ptr, b_ptr, rows_ptr, scales_ptr, out_ptr, ld_out,
+                                     M, N, K, R, slots, ws, ws_bytes, stream), "svq_adapter_add")
+
+    _on_device(dev, call)
     return out
 
 
@@ -645,24 +668,25 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, work
     may be a column slice of a wider matrix.
     """
     torch = _torch()
-    ptr, ld = _row_matrix(logits, "logits", _bf16_kinds())
+    ptr, ld = _rows_of(logits, "logits", _bf16_dtypes())
     dev = logits.device
     M, V = logits.shape
-    f32, i32 = (torch.float32,), (torch.int32,)
+    f32, i32, per_row = (torch.float32,), (torch.int32,), (M,)
+    u_ptr = _ptr(u, "u", f32, per_row, dev)
+    t_ptr = None if temperature is None else _ptr(temperature, "temperature", f32, per_row, dev)
+    k_ptr = None if top_k is None else _ptr(top_k, "top_k", i32, per_row, dev)
+    p_ptr = None if top_p is None else _ptr(top_p, "top_p", f32, per_row, dev)
+    m_ptr = None if min_p is None else _ptr(min_p, "min_p", f32, per_row, dev)
+    tokens = torch.empty(M, dtype=torch.int32, device=dev)
+    logprobs = torch.empty(M, dtype=torch.float32, device=dev)
 
-    def per_row(t, name, kinds):
-        return None if t is None else _typed(t, name, kinds, (M,), dev)
+    def call(stream):
+        need = 0 if workspace is not None else sample_workspace_bytes(M, V)
+        keep, ws, ws_bytes = _scratch(need, workspace, dev)
+        _check(lib().svq_sample(ptr, ld, u_ptr, t_ptr, k_ptr, p_ptr, m_ptr, tokens.data_ptr(), logprobs.data_ptr(),
+                                M, V, ws, ws_bytes, stream), "svq_sample")
 
-    with torch.cuda.device(dev):
-        nbytes = sample_workspace_bytes(M, V)
-        tokens = torch.empty(M, dtype=torch.int32, device=dev)
-        logprobs = torch.empty(M, dtype=torch.float32, device=dev)
-        ws_ptr, ws_bytes, keep = _scratch(nbytes, workspace, dev)
-        _check(lib().svq_sample(ptr, ld, _typed(u, "u", f32, (M,), dev), per_row(temperature, "temperature", f32),
-                                per_row(top_k, "top_k", i32), per_row(top_p, "top_p", f32),
-                                per_row(min_p, "min_p", f32), _dev_ptr(tokens, "tokens"),
-                                _dev_ptr(logprobs, "logprobs"), M, V, ws_ptr, ws_bytes, _stream_ptr(logits)),
-               "svq_sample")
+    _on_device(dev, call)
     return tokens, logprobs
 
 
@@ -680,13 +704,15 @@ def accept_drafts(tokens, inputs, starts):
     if tokens.dim() != 1 or starts.dim() != 1 or starts.shape[0] < 2:
         raise ValueError("tokens must be [M] and starts [S + 1] with S >= 1")
     dev, M, S = tokens.device, tokens.shape[0], starts.shape[0] - 1
-    tp = _typed(tokens, "tokens", i32, (M,), dev)
-    ip, sp = _typed(inputs, "inputs", i32, (M,), dev), _typed(starts, "starts", i32, (S + 1,), dev)
-    with torch.cuda.device(dev):
-        accepted = torch.empty(S, dtype=torch.int32, device=dev)
-        following = torch.empty(S, dtype=torch.int32, device=dev)
-        committed = torch.empty(M, dtype=torch.int32, device=dev)
-        _check(lib().svq_accept_drafts(tp, ip, sp, _dev_ptr(accepted, "accepted"), _dev_ptr(following, "next"),
-                                       _dev_ptr(committed, "committed"), M, S, _stream_ptr(tokens)),
-               "svq_accept_drafts")
+    t_ptr = _ptr(tokens, "tokens", i32, (M,), dev)
+    i_ptr = _ptr(inputs, "inputs", i32, (M,), dev)
+    s_ptr = _ptr(starts, "starts", i32, (S + 1,), dev)
+    if not tokens.is_cuda:
+        raise ValueError(f"tokens must be a device tensor, got {dev}")
+    accepted = torch.empty(S, dtype=torch.int32, device=dev)
+    following = torch.empty(S, dtype=torch.int32, device=dev)
+    committed = torch.empty(M, dtype=torch.int32, device=dev)
+    _on_device(dev, lambda stream: _check(
+        lib().svq_accept_drafts(t_ptr, i_ptr, s_ptr, accepted.data_ptr(), following.data_ptr(), committed.data_ptr(),
+                                M, S, stream), "svq_accept_drafts"))
     return accepted, following, committed

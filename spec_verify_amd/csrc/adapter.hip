@@ -48,24 +48,28 @@ __device__ __forceinline__ uint32_t tile_leaders(int slot, int lane, bool with_b
     return (uint32_t)__ballot(first);
 }
 
-// RT rank tiles of 16 per workgroup.
+// RT rank tiles of 16 per workgroup. The K range is the fastest block index (their number
+// is padded to a multiple of 8 where it is above 4): workgroups that read one range of A,
+// for other rows, then run on one XCD and find it in its L2.
 template <int RT>
 __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
     const uint16_t *__restrict__ x, const uint16_t *__restrict__ a, const int32_t *__restrict__ rows,
-    float *__restrict__ part, int64_t M, int K, int R, int slots, int ways, int rank_chunks, int splits, int T) {
+    float *__restrict__ part, int64_t M, int K, int R, int slots, int ways, int rank_chunks, int range_blocks, int T) {
+    static_assert(RT <= kDownWaves, "one wave sums one rank tile");
     __shared__ f32x4 red[kDownWaves][RT][64];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
     int b = blockIdx.x;
-    const int ks = b % splits;
-    b /= splits;
+    const int ks = b % range_blocks;
+    b /= range_blocks;
     const int rc = b % rank_chunks;
     b /= rank_chunks;
     const int way = b % ways;
     const int64_t row0 = (int64_t)(b / ways) * 16;
+    const int KT = K >> 7, kend = min(KT, (ks + 1) * T);
+    if (ks * T >= KT) return;
     const int slot = tile_slot(rows, row0, M, slots, lane);
     uint32_t leaders = tile_leaders(slot, lane, false);
-    const int KT = K >> 7, kend = min(KT, (ks + 1) * T);
     const int64_t xrow = min(row0 + r, M - 1);
     const uint16_t *xp = x + xrow * K + 8 * g;
     const int rank0 = rc * 16 * RT;
@@ -101,8 +105,6 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
 #pragma unroll
         for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i];
         __syncthreads();
-        // rank tile `wave` (for RT > 8 there would be more tiles than waves)
-        static_assert(RT <= kDownWaves, "one wave sums one rank tile");
         if (wave < RT) {
             f32x4 sum = red[0][wave][lane];
 #pragma unroll
@@ -118,107 +120,168 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
     }
 }
 
-// NS: 32-rank steps.
+// NS: 32-rank steps. A workgroup takes 256 columns of `tiles` consecutive row tiles and
+// keeps B in registers from one to the next while the adapter is the same (a prompt's
+// tiles). Column groups are the fastest block index, padded to a multiple of 8: the
+// groups' parts of B stay in one XCD's L2 as A's ranges do.
 template <int NS>
 __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
     const uint16_t *base, const float *__restrict__ part, const uint16_t *__restrict__ b,
     const int32_t *__restrict__ rows, const float *__restrict__ scales, uint16_t *out, int64_t M, int N, int R,
-    int slots, int64_t ld_base, int64_t ld_out, int ways, int col_groups, int splits) {
-    constexpr int kPitch = 32 * NS + 8;  // bf16 elements: rows 16 bytes apart in banks
-    __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
+    int slots, int64_t ld_base, int64_t ld_out, int ways, int col_blocks, int tiles, int splits) {
+    constexpr int kPitch = 32 * NS + 8;      // bf16 elements: rows 16 bytes apart in banks
+    constexpr int kEach = 2 * NS;            // ranks of a thread where t is put together
+    constexpr int kVec = kEach < 4 ? kEach : 4;
+    __shared__ __attribute__((aligned(16))) uint16_t thi[2][16][kPitch], tlo[2][16][kPitch];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
     int blk = blockIdx.x;
-    const int cg = blk % col_groups;
-    blk /= col_groups;
+    const int cg = blk % col_blocks;
+    blk /= col_blocks;
     const int way = blk % ways;
-    const int64_t row0 = (int64_t)(blk / ways) * 16;
-    const int slot = tile_slot(rows, row0, M, slots, lane);
-    uint32_t leaders = tile_leaders(slot, lane, true);
+    const int64_t tile0 = (int64_t)(blk / ways) * tiles;
+    if (cg * kUpWaves * 64 >= N) return;
     const int col0 = (cg * kUpWaves + wave) * 64;
-    const int col = col0 + 16 * g;       // this lane's 16 output columns
-    const int64_t m = row0 + r;          // and its row
+    const int col = col0 + 16 * g;           // this lane's 16 output columns
+    uint4 bv[NS][4];
+    int have = -1, buf = 0;                  // the adapter in bv; the half of LDS to write
 
-    for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
-        if (ord % ways != way) continue;
-        const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
-        const bool mine = slot == s && col < N;
-        uint4 y[2];
-        if (s < 0) {  // rows without an adapter
-            if (mine && (const uint16_t *)out != base) {
+    for (int64_t row0 = tile0 * 16; row0 < min((tile0 + tiles) * 16, M); row0 += 16) {
+        const int slot = tile_slot(rows, row0, M, slots, lane);
+        uint32_t leaders = tile_leaders(slot, lane, true);
+        const int64_t m = row0 + r;          // this lane's row
+        for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
+            if (ord % ways != way) continue;
+            const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
+            const bool mine = slot == s && col < N;
+            uint4 y[2];
+            if (s < 0) {  // rows without an adapter
+                if (mine && (const uint16_t *)out != base) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *(uint4 *)(out + m * ld_out + col + 8 * h) = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+                    for (int h = 0; h < 2; ++h)
+                        *(uint4 *)(out + m * ld_out + col + 8 * h) = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+                }
+                continue;
             }
-            continue;
-        }
-        // scale * t of this adapter's rows, rounded in two halves
-        const float scale = scales[s];
-        for (int i = threadIdx.x; i < 16 * 32 * NS; i += 64 * kUpWaves) {
-            const int row = i / (32 * NS), rank = i % (32 * NS);
-            float t = 0.f;
-            if (rank < R && row0 + row < M && rows[row0 + row] == s) {
-                const float *p = part + (row0 + row) * R + rank;
-                for (int ks = 0; ks < splits; ++ks) t += p[(int64_t)ks * M * R];
-                t *= scale;
+            // t of this thread's row and ranks: all K ranges in flight, summed in order
+            const int trow = threadIdx.x >> 4, rank0 = (threadIdx.x & 15) * kEach;
+            const bool has = __shfl(slot, trow) == s;
+            float t[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) t[i] = 0.f;
+            {
+                const float *p = part + (row0 + trow) * R + rank0;
+                constexpr int kAhead = NS > 2 ? 4 : 8;
+                for (int k0 = 0; k0 < splits; k0 += kAhead) {
+                    float v[kAhead][kEach];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                        for (int i = 0; i < kEach; i += kVec) {
+                            const bool in = has && k0 + k < splits && rank0 + i < R;
+                            const float *q = p + (int64_t)(k0 + k) * M * R + i;
+                            if constexpr (kVec == 2) {
+                                const float2 f = in ? *(const float2 *)q : make_float2(0.f, 0.f);
+                                v[k][i] = f.x, v[k][i + 1] = f.y;
+                            } else {
+                                const float4 f = in ? *(const float4 *)q : make_float4(0.f, 0.f, 0.f, 0.f);
+                                v[k][i] = f.x, v[k][i + 1] = f.y, v[k][i + 2] = f.z, v[k][i + 3] = f.w;
+                            }
+                        }
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                        for (int i = 0; i < kEach; ++i) t[i] += v[k][i];
+                }
             }
-            const uint16_t hi = f32_to_bf16_rne(t);
-            const float rest = t - bits_f32((uint32_t)hi << 16);
-            thi[row][rank] = hi;
-            tlo[row][rank] = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(rest);
-        }
-        f32x4 acc[4];
+            if (s != have) {
+                have = s;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (mine) {
+                for (int st = 0; st < NS; ++st)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
-        }
-        __syncthreads();
+                    for (int q = 0; q < 4; ++q) {
+                        // MFMA row 4 g' + i of product q is column 16 g' + 4 q + i
+                        const int n = col0 + 16 * (r >> 2) + 4 * q + (r & 3), rank = 32 * st + 8 * g;
+                        bv[st][q] = make_uint4(0, 0, 0, 0);
+                        if (n < N && rank < R) bv[st][q] = *(const uint4 *)(b + ((int64_t)s * N + n) * R + rank);
+                    }
+            }
+            if (mine) {
 #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-            const uint4 hi = *(const uint4 *)&thi[r][32 * st + 8 * g], lo = *(const uint4 *)&tlo[r][32 * st + 8 * g];
+                for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+            }
+            // scale * t, rounded in two halves
+            const float scale = scales[s];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // MFMA row 4 g' + i of product q is column 16 g' + 4 q + i
-                const int n = col0 + 16 * (r >> 2) + 4 * q + (r & 3), rank = 32 * st + 8 * g;
-                uint4 bv = make_uint4(0, 0, 0, 0);
-                if (n < N && rank < R) bv = *(const uint4 *)(b + ((int64_t)s * N + n) * R + rank);
-                acc[q] = mfma16x16x32(bv, hi, acc[q]);
-                acc[q] = mfma16x16x32(bv, lo, acc[q]);
+            for (int i = 0; i < kEach; i += 2) {
+                uint32_t hi2 = 0, lo2 = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = scale * t[i + e];
+                    const uint32_t hi = f32_to_bf16_rne(f);
+                    const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
+                    hi2 |= hi << (16 * e);
+                    lo2 |= lo << (16 * e);
+                }
+                *(uint32_t *)&thi[buf][trow][rank0 + i] = hi2;
+                *(uint32_t *)&tlo[buf][trow][rank0 + i] = lo2;
+            }
+            lds_barrier();
+            f32x4 acc[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                const uint4 hi = *(const uint4 *)&thi[buf][r][32 * st + 8 * g];
+                const uint4 lo = *(const uint4 *)&tlo[buf][r][32 * st + 8 * g];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    acc[q] = mfma16x16x32(bv[st][q], hi, acc[q]);
+                    acc[q] = mfma16x16x32(bv[st][q], lo, acc[q]);
+                }
+            }
+            buf ^= 1;  // the other half: a wave writes it while others still read this one
+            if (mine) {
+                uint32_t o[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const uint32_t v = (&y[w >> 2].x)[w & 3];
+                    const float lo = bits_f32(v << 16) + acc[w >> 1][2 * (w & 1)];
+                    const float hi = bits_f32(v & 0xFFFF0000u) + acc[w >> 1][2 * (w & 1) + 1];
+                    o[w] = (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
+                }
+                *(uint4 *)(out + m * ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+                *(uint4 *)(out + m * ld_out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
             }
         }
-        if (mine) {
-            uint32_t o[8];
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t v = (&y[w >> 2].x)[w & 3];
-                const float lo = bits_f32(v << 16) + acc[w >> 1][2 * (w & 1)];
-                const float hi = bits_f32(v & 0xFFFF0000u) + acc[w >> 1][2 * (w & 1) + 1];
-                o[w] = (uint32_t)f32_to_bf16_rne(lo) | ((uint32_t)f32_to_bf16_rne(hi) << 16);
-            }
-            *(uint4 *)(out + m * ld_out + col) = make_uint4(o[0], o[1], o[2], o[3]);
-            *(uint4 *)(out + m * ld_out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-        __syncthreads();
     }
 }
 
 }  // namespace
 
-AdapterPlan plan_adapter(int64_t M, int64_t K, int64_t R, int64_t slots) {
+AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slots) {
     AdapterPlan p{};
     p.row_tiles = (M + 15) / 16;
-    // adapters of one tile side by side while tiles alone do not fill the chip
-    const int64_t most = std::min<int64_t>(std::min<int64_t>(M, 16), slots);
-    p.ways = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / p.row_tiles));
+    const int64_t distinct = std::min<int64_t>(std::min<int64_t>(M, 16), slots);  // adapters in a tile, at most
     p.rank_tiles = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
     p.rank_chunks = (int)((R + 16 * p.rank_tiles - 1) / (16 * p.rank_tiles));
-    const int64_t KT = K / 128, most_splits = (KT + kDownWaves - 1) / kDownWaves;
-    const int64_t groups = p.row_tiles * p.rank_chunks;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most_splits, (512 + groups - 1) / groups));
-    p.tiles_per_split = (int)((KT + want - 1) / want);
+    // K ranges: one 128-element tile a wave while that fills the chip, longer ones for
+    // many rows; a power of two, or a multiple of 8 blocks
+    const int64_t KT = K / 128, groups = p.row_tiles * p.rank_chunks;
+    int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((KT + kDownWaves - 1) / kDownWaves, 512 / groups));
+    if (blocks > 4) blocks = (blocks + 7) / 8 * 8;
+    else if (blocks == 3) blocks = 4;
+    p.tiles_per_split = (int)((KT + blocks - 1) / blocks);
     p.splits = (int)((KT + p.tiles_per_split - 1) / p.tiles_per_split);
+    p.range_blocks = (int)blocks;
+    // adapters of one tile side by side while tiles alone do not fill the chip
+    p.down_ways = (int)std::max<int64_t>(1, std::min<int64_t>(distinct, 1024 / (groups * blocks)));
+    p.col_blocks = (int)((N + 64 * kUpWaves - 1) / (64 * kUpWaves));
+    if (p.col_blocks > 4) p.col_blocks = (p.col_blocks + 7) / 8 * 8;
+    // rows without an adapter are a group of their own
+    p.up_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(8, p.row_tiles * p.col_blocks / 1024));
+    const int64_t up_groups = (p.row_tiles + p.up_tiles - 1) / p.up_tiles * p.col_blocks;
+    p.up_ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(distinct + 1, 16), 2560 / up_groups));
     p.workspace_bytes = kCounterBytes + (size_t)p.splits * M * R * 4;
     return p;
 }
@@ -228,25 +291,22 @@ hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld
                               int64_t M, int64_t N, int64_t K, int R, int slots, void *workspace,
                               hipStream_t stream) {
     float *part = (float *)ws_partials(workspace);
-    const dim3 down((uint32_t)(p.row_tiles * p.ways * p.rank_chunks * p.splits));
+    const dim3 down((uint32_t)(p.row_tiles * p.down_ways * p.rank_chunks * p.range_blocks));
 #define SVQ_DOWN(RT)                                                                                                 \
     hipLaunchKernelGGL((adapter_down_kernel<RT>), down, dim3(64 * kDownWaves), 0, stream, (const uint16_t *)x,       \
-                       (const uint16_t *)a, rows, part, M, (int)K, R, slots, p.ways, p.rank_chunks, p.splits,        \
-                       p.tiles_per_split)
+                       (const uint16_t *)a, rows, part, M, (int)K, R, slots, p.down_ways, p.rank_chunks,             \
+                       p.range_blocks, p.tiles_per_split)
     if (p.rank_tiles == 1) SVQ_DOWN(1);
     else if (p.rank_tiles == 2) SVQ_DOWN(2);
     else SVQ_DOWN(4);
 #undef SVQ_DOWN
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int col_groups = (int)((N + 64 * kUpWaves - 1) / (64 * kUpWaves));
-    // one way more than adapters: rows without one are a group of their own
-    const int ways = (int)std::min<int64_t>(p.ways == 1 ? 1 : p.ways + 1, 16);
-    const dim3 up((uint32_t)(p.row_tiles * ways * col_groups));
+    const dim3 up((uint32_t)((p.row_tiles + p.up_tiles - 1) / p.up_tiles * p.up_ways * p.col_blocks));
 #define SVQ_UP(NS)                                                                                                  \
     hipLaunchKernelGGL((adapter_up_kernel<NS>), up, dim3(64 * kUpWaves), 0, stream, (const uint16_t *)base, part,   \
                        (const uint16_t *)b, rows, scales, (uint16_t *)out, M, (int)N, R, slots, ld_base, ld_out,    \
-                       ways, col_groups, p.splits)
+                       p.up_ways, p.col_blocks, p.up_tiles, p.splits)
     if (R <= 32) SVQ_UP(1);
     else if (R <= 64) SVQ_UP(2);
     else if (R <= 128) SVQ_UP(4);

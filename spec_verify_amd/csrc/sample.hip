@@ -797,18 +797,21 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
 
 __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
                                                                int32_t *__restrict__ tokens, float *__restrict__ logprobs,
-                                                               int V) {
+                                                               int64_t M, int V) {
     __shared__ __attribute__((aligned(16))) Draw sh;
-    const int64_t m = blockIdx.x;
-    if (tokens[m] != kLongWay) return;
-    const Row row = make_row(logits + m * ld, V);
-    const RowParams rp = row_params(par, m);
-    const Drawn d = draw_way<kLong>(sh, row, rp);
-    int token = -1;
-    if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
-    if (threadIdx.x == 0) {
-        tokens[m] = token;
-        if (logprobs) logprobs[m] = d.logprob;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        const bool mine = tokens[m] == kLongWay;
+        __syncthreads();  // every thread has read the mark, and the row before is done with
+        if (!mine) continue;
+        const Row row = make_row(logits + m * ld, V);
+        const RowParams rp = row_params(par, m);
+        const Drawn d = draw_way<kLong>(sh, row, rp);
+        int token = -1;
+        if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
+        if (threadIdx.x == 0) {
+            tokens[m] = token;
+            if (logprobs) logprobs[m] = d.logprob;
+        }
     }
 }
 
@@ -1079,8 +1082,8 @@ hipError_t launch_sample(const SamplePlan &p, const void *logits, int64_t ld, co
                                tokens, logprobs, (int)V);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par, tokens, logprobs,
-                           (int)V);
+        hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)std::min<int64_t>(M, 256)), dim3(kThreads), 0, stream, l, ld,
+                           par, tokens, logprobs, M, (int)V);
         return hipGetLastError();
     }
     uint32_t *parts = (uint32_t *)ws_partials(workspace);

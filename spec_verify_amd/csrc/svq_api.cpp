@@ -613,7 +613,7 @@ bool any_overlap(const Span *outs, int no, const Span *ins, int ni) {
 
 size_t svq_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R, int32_t slots) {
     if (check_adapter_shape(M, N, K, R, slots) != SVQ_OK) return (size_t)-1;
-    return plan_adapter(M, K, R, slots).workspace_bytes;
+    return plan_adapter(M, N, K, R, slots).workspace_bytes;
 }
 
 int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void *a, const void *b,
@@ -627,7 +627,7 @@ int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void
     if (!aligned(base, 16) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(rows, 4) ||
         !aligned(scales, 4) || !aligned(out, 16))
         return SVQ_ERR_ALIGN;
-    const AdapterPlan plan = plan_adapter(M, K, R, slots);
+    const AdapterPlan plan = plan_adapter(M, N, K, R, slots);
     if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)) return SVQ_ERR_WORKSPACE;
     const size_t base_bytes = ((size_t)(M - 1) * ld_base + N) * 2;
     const Span outs[] = {{out, ((size_t)(M - 1) * ld_out + N) * 2}, {workspace, plan.workspace_bytes}};

@@ -147,15 +147,17 @@ hipError_t launch_mxfp8_quantize(const void *w, int optimized, uint8_t *codes, u
 hipError_t launch_rtn_quantize(const void *w, int bits, int G, void *codes, void *scales, int64_t N,
                                int64_t K, hipStream_t stream);
 
-// Low-rank adapters: tiles of 16 rows; `ways` workgroups take a tile's adapters side
-// by side; rank_tiles x 16 ranks and one of `splits` K ranges (of tiles_per_split
-// 128-element tiles) per workgroup of the first launch.
+// Low-rank adapters: tiles of 16 rows, whose adapters `*_ways` workgroups take side by
+// side. First launch: rank_tiles x 16 ranks and one of `splits` K ranges (of
+// tiles_per_split 128-element tiles; range_blocks block indexes) per workgroup. Second:
+// 256 columns (col_blocks block indexes) of up_tiles row tiles.
 struct AdapterPlan {
     int64_t row_tiles;
-    int ways, rank_tiles, rank_chunks, splits, tiles_per_split;
+    int rank_tiles, rank_chunks, splits, tiles_per_split, range_blocks, down_ways;
+    int col_blocks, up_tiles, up_ways;
     size_t workspace_bytes;
 };
-AdapterPlan plan_adapter(int64_t M, int64_t K, int64_t R, int64_t slots);
+AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slots);
 hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld_base, const void *x, const void *a,
                               const void *b, const int32_t *rows, const float *scales, void *out, int64_t ld_out,
                               int64_t M, int64_t N, int64_t K, int R, int slots, void *workspace, hipStream_t stream);
