@@ -39,20 +39,34 @@ __device__ __forceinline__ int tile_slot(const int32_t *rows, int64_t row0, int6
     return (uint32_t)s < (uint32_t)slots ? s : -1;
 }
 
-// Lanes (of the first 16) whose row is the tile's first one with its adapter.
-__device__ __forceinline__ uint32_t tile_leaders(int slot, int lane, bool with_bare) {
-    bool first = lane < 16 && (slot >= 0 || (with_bare && slot == -1));
+// Lane of the first row with this lane's adapter (lanes 0..15; their rows).
+__device__ __forceinline__ int tile_first(int slot, int lane) {
+    int first = 15;
 #pragma unroll
-    for (int j = 0; j < 15; ++j)
-        if (__builtin_amdgcn_readlane(slot, j) == slot && j < lane) first = false;
-    return (uint32_t)__ballot(first);
+    for (int j = 14; j >= 0; --j)
+        if (__builtin_amdgcn_readlane(slot, j) == slot) first = j;
+    return min(first, lane & 15);
+}
+
+// The adapters of a tile as the lanes of their first rows; rows without one are a group
+// of their own where `bare` asks for them.
+__device__ __forceinline__ uint32_t tile_leaders(int slot, int first, int lane, bool bare) {
+    return (uint32_t)__ballot(lane < 16 && first == lane && (slot >= 0 || (bare && slot == -1)));
+}
+
+// Those that fall to one of `ways` workgroups.
+__device__ __forceinline__ uint32_t of_way(uint32_t leaders, int ways, int way) {
+    uint32_t mine = 0;
+    for (int ord = 0; leaders; leaders &= leaders - 1, ++ord)
+        if (ord % ways == way) mine |= leaders & -leaders;
+    return mine;
 }
 
 // RT rank tiles of 16 per workgroup. The K range is the fastest block index (their number
 // is padded to a multiple of 8 where it is above 4): workgroups that read one range of A,
 // for other rows, then run on one XCD and find it in its L2.
 template <int RT>
-__global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
+__global__ __launch_bounds__(64 * kDownWaves) __attribute__((amdgpu_waves_per_eu(4))) void adapter_down_kernel(
     const uint16_t *__restrict__ x, const uint16_t *__restrict__ a, const int32_t *__restrict__ rows,
     float *__restrict__ part, int64_t M, int K, int R, int slots, int ways, int rank_chunks, int range_blocks, int T) {
     static_assert(RT <= kDownWaves, "one wave sums one rank tile");
@@ -64,19 +78,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
     b /= range_blocks;
     const int rc = b % rank_chunks;
     b /= rank_chunks;
-    const int way = b % ways;
-    const int64_t row0 = (int64_t)(b / ways) * 16;
+    const int row_tiles = (int)((M + 15) >> 4);
+    const int way = b / row_tiles;  // slowest: workgroups that find no adapter come last
+    const int64_t row0 = (int64_t)(b % row_tiles) * 16;
     const int KT = K >> 7, kend = min(KT, (ks + 1) * T);
     if (ks * T >= KT) return;
     const int slot = tile_slot(rows, row0, M, slots, lane);
-    uint32_t leaders = tile_leaders(slot, lane, false);
+    uint32_t mine = of_way(tile_leaders(slot, tile_first(slot, lane), lane, false), ways, way);
     const int64_t xrow = min(row0 + r, M - 1);
     const uint16_t *xp = x + xrow * K + 8 * g;
     const int rank0 = rc * 16 * RT;
 
-    for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
-        if (ord % ways != way) continue;
-        const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
+    for (; mine; mine &= mine - 1) {
+        const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(mine));
         const uint16_t *ap[RT];
         bool in[RT];
 #pragma unroll
@@ -120,113 +134,128 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(
     }
 }
 
-// NS: 32-rank steps. A workgroup takes 256 columns of `tiles` consecutive row tiles and
-// keeps B in registers from one to the next while the adapter is the same (a prompt's
-// tiles). Column groups are the fastest block index, padded to a multiple of 8: the
-// groups' parts of B stay in one XCD's L2 as A's ranges do.
+// NS: 32-rank steps. A workgroup takes 256 columns of `tiles` consecutive row tiles. t of
+// all of a tile's rows is put together once; then B of one adapter after the other is
+// multiplied with it (the next one's loads are issued as soon as the registers are free)
+// and each result row keeps its own adapter's product. B stays in registers from one tile
+// to the next while the adapter is the same (a prompt's tiles). Column groups are the
+// fastest block index, padded to a multiple of 8: the groups' parts of B stay in one
+// XCD's L2 as A's ranges do.
 template <int NS>
-__global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
-    const uint16_t *base, const float *__restrict__ part, const uint16_t *__restrict__ b,
-    const int32_t *__restrict__ rows, const float *__restrict__ scales, uint16_t *out, int64_t M, int N, int R,
-    int slots, int64_t ld_base, int64_t ld_out, int ways, int col_blocks, int tiles, int splits) {
+__global__ __launch_bounds__(64 * kUpWaves) void
+adapter_up_kernel(const uint16_t *base, const float *__restrict__ part, const uint16_t *__restrict__ b,
+                  const int32_t *__restrict__ rows, const float *__restrict__ scales, uint16_t *out, int64_t M, int N,
+                  int R, int slots, int64_t ld_base, int64_t ld_out, int ways, int col_blocks, int tiles, int splits) {
     constexpr int kPitch = 32 * NS + 8;      // bf16 elements: rows 16 bytes apart in banks
     constexpr int kEach = 2 * NS;            // ranks of a thread where t is put together
     constexpr int kVec = kEach < 4 ? kEach : 4;
+    constexpr int kAhead = NS == 1 ? 8 : (NS == 8 ? 2 : 4);  // K ranges of t in flight
     __shared__ __attribute__((aligned(16))) uint16_t thi[2][16][kPitch], tlo[2][16][kPitch];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
     int blk = blockIdx.x;
     const int cg = blk % col_blocks;
     blk /= col_blocks;
-    const int way = blk % ways;
-    const int64_t tile0 = (int64_t)(blk / ways) * tiles;
+    const int row_tiles = (int)((M + 15) >> 4), tile_groups = (row_tiles + tiles - 1) / tiles;
+    const int way = blk / tile_groups;       // slowest, as in the first launch
+    const int tile0 = blk % tile_groups * tiles, tile1 = min(tile0 + tiles, row_tiles);
     if (cg * kUpWaves * 64 >= N) return;
     const int col0 = (cg * kUpWaves + wave) * 64;
     const int col = col0 + 16 * g;           // this lane's 16 output columns
+    const int trow = threadIdx.x >> 4, rank0 = (threadIdx.x & 15) * kEach;  // and its row and ranks of t
+    // MFMA row 4 g' + i of product q is column 16 g' + 4 q + i. Addresses are a scalar base
+    // and a 32-bit offset.
+    const int brow = 16 * (r >> 2) + (r & 3);
+    const uint32_t b_off = (uint32_t)(brow * R + 8 * g) * 2, t_off = (uint32_t)(trow * R + rank0) * 4;
     uint4 bv[NS][4];
-    int have = -1, buf = 0;                  // the adapter in bv; the half of LDS to write
-
-    for (int64_t row0 = tile0 * 16; row0 < min((tile0 + tiles) * 16, M); row0 += 16) {
-        const int slot = tile_slot(rows, row0, M, slots, lane);
-        uint32_t leaders = tile_leaders(slot, lane, true);
-        const int64_t m = row0 + r;          // this lane's row
-        for (int ord = 0; leaders; leaders &= leaders - 1, ++ord) {
-            if (ord % ways != way) continue;
-            const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(leaders));
-            const bool mine = slot == s && col < N;
-            uint4 y[2];
-            if (s < 0) {  // rows without an adapter
-                if (mine && (const uint16_t *)out != base) {
+    int have = -1;                           // the adapter in bv
+    auto load_b = [&](int s) {
+        if (s == have) return;
+        have = s;
+        const char *p = (const char *)(b + ((int64_t)s * N + col0) * R);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *(uint4 *)(out + m * ld_out + col + 8 * h) = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                bv[st][q] = make_uint4(0, 0, 0, 0);
+                if (col0 + brow + 4 * q < N && 32 * st + 8 * g < R)
+                    bv[st][q] = *(const uint4 *)(p + (int64_t)8 * q * R + 64 * st + b_off);
+            }
+    };
+
+    for (int tile = tile0, buf = 0; tile < tile1; ++tile, buf ^= 1) {
+        const int64_t row0 = (int64_t)tile * 16, m = row0 + r;  // m: this lane's row
+        const int slot = tile_slot(rows, row0, M, slots, lane);
+        const int first = tile_first(slot, lane);
+        const uint32_t leaders = tile_leaders(slot, first, lane, true);
+        uint32_t mine = of_way(leaders, ways, way);
+        if (!mine) continue;
+        const int s0 = __builtin_amdgcn_readlane(slot, __builtin_ctz(mine));
+        if (s0 >= 0) load_b(s0);
+        // t of this thread's row and ranks, summed over the K ranges in order
+        const int tslot = __shfl(slot, trow);
+        float t[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) t[i] = 0.f;
+        {
+            const char *p = (const char *)(part + row0 * R);
+            for (int k0 = 0; k0 < splits; k0 += kAhead) {
+                float v[kAhead][kEach];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const char *pk = p + (int64_t)(k0 + k) * M * R * 4;
+#pragma unroll
+                    for (int i = 0; i < kEach; i += kVec) {
+                        const bool in = tslot >= 0 && k0 + k < splits && rank0 + i < R;
+                        if constexpr (kVec == 2) {
+                            const float2 f = in ? *(const float2 *)(pk + t_off + 4 * i) : make_float2(0.f, 0.f);
+                            v[k][i] = f.x, v[k][i + 1] = f.y;
+                        } else {
+                            const float4 f = in ? *(const float4 *)(pk + t_off + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            v[k][i] = f.x, v[k][i + 1] = f.y, v[k][i + 2] = f.z, v[k][i + 3] = f.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) t[i] += v[k][i];
+            }
+        }
+        const float scale = tslot >= 0 ? scales[tslot] : 0.f;
+        const bool my_row = slot >= -1 && (mine >> first & 1) && col < N;
+        uint4 y[2];
+        if (my_row) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
+        }
+        // scale * t, rounded in two halves
+#pragma unroll
+        for (int i = 0; i < kEach; i += 2) {
+            uint32_t hi2 = 0, lo2 = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = scale * t[i + e];
+                const uint32_t hi = f32_to_bf16_rne(f);
+                const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
+                hi2 |= hi << (16 * e);
+                lo2 |= lo << (16 * e);
+            }
+            *(uint32_t *)&thi[buf][trow][rank0 + i] = hi2;
+            *(uint32_t *)&tlo[buf][trow][rank0 + i] = lo2;
+        }
+        lds_barrier();  // one a tile: the next tile writes the other half
+        while (mine) {
+            const int s = __builtin_amdgcn_readlane(slot, __builtin_ctz(mine));
+            mine &= mine - 1;
+            if (s < 0) {  // rows without an adapter
+                if (my_row && slot == s && (const uint16_t *)out != base) {
+                    *(uint4 *)(out + m * ld_out + col) = y[0];
+                    *(uint4 *)(out + m * ld_out + col + 8) = y[1];
                 }
                 continue;
             }
-            // t of this thread's row and ranks: all K ranges in flight, summed in order
-            const int trow = threadIdx.x >> 4, rank0 = (threadIdx.x & 15) * kEach;
-            const bool has = __shfl(slot, trow) == s;
-            float t[kEach];
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) t[i] = 0.f;
-            {
-                const float *p = part + (row0 + trow) * R + rank0;
-                constexpr int kAhead = NS > 2 ? 4 : 8;
-                for (int k0 = 0; k0 < splits; k0 += kAhead) {
-                    float v[kAhead][kEach];
-#pragma unroll
-                    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-                        for (int i = 0; i < kEach; i += kVec) {
-                            const bool in = has && k0 + k < splits && rank0 + i < R;
-                            const float *q = p + (int64_t)(k0 + k) * M * R + i;
-                            if constexpr (kVec == 2) {
-                                const float2 f = in ? *(const float2 *)q : make_float2(0.f, 0.f);
-                                v[k][i] = f.x, v[k][i + 1] = f.y;
-                            } else {
-                                const float4 f = in ? *(const float4 *)q : make_float4(0.f, 0.f, 0.f, 0.f);
-                                v[k][i] = f.x, v[k][i + 1] = f.y, v[k][i + 2] = f.z, v[k][i + 3] = f.w;
-                            }
-                        }
-#pragma unroll
-                    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-                        for (int i = 0; i < kEach; ++i) t[i] += v[k][i];
-                }
-            }
-            if (s != have) {
-                have = s;
-#pragma unroll
-                for (int st = 0; st < NS; ++st)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // MFMA row 4 g' + i of product q is column 16 g' + 4 q + i
-                        const int n = col0 + 16 * (r >> 2) + 4 * q + (r & 3), rank = 32 * st + 8 * g;
-                        bv[st][q] = make_uint4(0, 0, 0, 0);
-                        if (n < N && rank < R) bv[st][q] = *(const uint4 *)(b + ((int64_t)s * N + n) * R + rank);
-                    }
-            }
-            if (mine) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
-            }
-            // scale * t, rounded in two halves
-            const float scale = scales[s];
-#pragma unroll
-            for (int i = 0; i < kEach; i += 2) {
-                uint32_t hi2 = 0, lo2 = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = scale * t[i + e];
-                    const uint32_t hi = f32_to_bf16_rne(f);
-                    const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
-                    hi2 |= hi << (16 * e);
-                    lo2 |= lo << (16 * e);
-                }
-                *(uint32_t *)&thi[buf][trow][rank0 + i] = hi2;
-                *(uint32_t *)&tlo[buf][trow][rank0 + i] = lo2;
-            }
-            lds_barrier();
+            load_b(s);  // (the first, and what follows rows without one: others are on their way)
             f32x4 acc[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -240,8 +269,11 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
                     acc[q] = mfma16x16x32(bv[st][q], lo, acc[q]);
                 }
             }
-            buf ^= 1;  // the other half: a wave writes it while others still read this one
             if (mine) {
+                const int next = __builtin_amdgcn_readlane(slot, __builtin_ctz(mine));
+                if (next >= 0) load_b(next);
+            }
+            if (my_row && slot == s) {
                 uint32_t o[8];
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {
@@ -269,9 +301,12 @@ AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slo
     // many rows; a power of two, or a multiple of 8 blocks
     const int64_t KT = K / 128, groups = p.row_tiles * p.rank_chunks;
     int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((KT + kDownWaves - 1) / kDownWaves, 512 / groups));
-    if (blocks > 4) blocks = (blocks + 7) / 8 * 8;
-    else if (blocks == 3) blocks = 4;
+    if (groups < 64 && blocks > 4) blocks = (blocks + 7) / 8 * 8;
     p.tiles_per_split = (int)((KT + blocks - 1) / blocks);
+    if (groups >= 64) {  // (a range of many rows' x is not shared: whole rounds of the waves)
+        p.tiles_per_split = (p.tiles_per_split + kDownWaves - 1) / kDownWaves * kDownWaves;
+        blocks = (KT + p.tiles_per_split - 1) / p.tiles_per_split;
+    }
     p.splits = (int)((KT + p.tiles_per_split - 1) / p.tiles_per_split);
     p.range_blocks = (int)blocks;
     // adapters of one tile side by side while tiles alone do not fill the chip
