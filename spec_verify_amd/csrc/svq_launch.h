@@ -147,14 +147,14 @@ hipError_t launch_mxfp8_quantize(const void *w, int optimized, uint8_t *codes, u
 hipError_t launch_rtn_quantize(const void *w, int bits, int G, void *codes, void *scales, int64_t N,
                                int64_t K, hipStream_t stream);
 
-// Low-rank adapters: tiles of 16 rows, whose adapters `*_ways` workgroups take side by
-// side. First launch: rank_tiles x 16 ranks and one of `splits` K ranges (of
-// tiles_per_split 128-element tiles; range_blocks block indexes) per workgroup. Second:
-// 256 columns (col_blocks block indexes) of up_tiles row tiles.
+// Low-rank adapters: blocks of 256 rows, in each at most `items` groups of up to 16 rows
+// of one adapter. First launch: an item, rank_tiles x 16 ranks and one of `splits` K
+// ranges (of tiles_per_split 128-element tiles; range_blocks block indexes) per workgroup.
+// Second: an item and 256 columns (col_blocks block indexes).
 struct AdapterPlan {
-    int64_t row_tiles;
-    int rank_tiles, rank_chunks, splits, tiles_per_split, range_blocks, down_ways;
-    int col_blocks, up_tiles, up_ways;
+    int64_t row_blocks;
+    int items, rank_tiles, rank_chunks, splits, tiles_per_split, range_blocks;
+    int col_blocks;
     size_t workspace_bytes;
 };
 AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slots);
