@@ -39,10 +39,11 @@ constexpr uint32_t kBinsHalf = 4096;         // 32 exponents x 128 mantissas of 
 constexpr uint32_t kBins = 2 * kBinsHalf;    // of raw index sign << 12 | (magnitude - kMagLo)
 constexpr int kOwn = kBins / kThreads;       // bins of a thread
 constexpr uint32_t kMagLo = 111u << 7;       // pattern of 2^-16
-constexpr uint32_t kSideMax = 64;            // smaller magnitudes; zero and the low pattern are two more items
-constexpr int kItems = kSideMax + 2;
+constexpr uint32_t kSideMax = 55;            // smaller magnitudes; with zero and a thread's bins they are one per lane
 constexpr int kWindows = 65536 / kBins;
 constexpr int kLastPositive = kThreads / 2 - 1;  // its bins are followed by the side items
+constexpr int kSideWave = kLastPositive / 64;    // whose last lane it is
+static_assert(kLastPositive % 64 == 63 && kOwn + kSideMax + 1 <= 64 && kThreads % 64 == 0, "one wave owns the side items");
 
 // ---- a row of logits -------------------------------------------------------------
 
@@ -79,6 +80,7 @@ __device__ __forceinline__ uint32_t key_of(uint32_t b) {
     if (b == 0x8000u) b = 0;
     return (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
 }
+__device__ __forceinline__ uint32_t bits_of(uint32_t key) { return (key & 0x8000u) ? (key & 0x7FFFu) : (~key & 0xFFFFu); }
 // NaN and -inf are never drawn: finite values and +inf have keys in [0x80, 0xFF80].
 __device__ __forceinline__ bool key_valid(uint32_t key) { return key - 0x80u <= 0xFF00u; }
 __device__ __forceinline__ double value_of(uint32_t bits) { return (double)bits_f32(bits << 16); }
@@ -265,17 +267,17 @@ __device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
 // ---- the draw ---------------------------------------------------------------------------
 
 struct Found {
-    double mass, logprob;    // W, and of a draw its log-probability
+    double mass;             // W
     uint32_t pos, bits, ord; // tokens counted; of a draw the value and which of its occurrences
 };
 
 struct Draw {
     Hist h;
-    uint32_t item_bits[kItems], item_count[kItems];
-    double item_weight[kItems];
+    uint32_t item_bits[kSideMax + 1], item_count[kSideMax + 1];  // side items in order
+    double item_weight[kSideMax + 1], low_weight;
     double wsum[kWaves], win_mass[kWindows + 1], win_first[kWindows];
     uint32_t csum[kWaves], win_count[kWindows + 1];
-    uint32_t first, owner[8];
+    uint32_t first, owner[4];
     uint32_t count[kWaves];  // locate's
     int at;
     Found found;
@@ -295,92 +297,101 @@ struct Drawn {
 
 enum Seek { kMass, kTopP, kMinP, kDraw };
 
-// The next double below a positive one; of others, a negative number.
-__device__ __forceinline__ double below(double x) {
-    return x > 0.0 ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, x) - 1) : -1.0;
-}
-
 // How a row is counted: whole rows in h.bin; their quarters apart, 16 bits each, in h.bin
 // and a table behind it; or window by window from the row itself.
 enum Way { kWhole, kQuarters, kLong };
 
-// Draws a token's value and its ordinal. Used by whole workgroups.
+// A thread's bins in a counted row, descending: patterns bits0, bits0 + dir, ..., each
+// weight `ratio` times the one before.
+struct Own {
+    uint32_t bits0;
+    int dir;
+    double ratio;
+    __device__ __forceinline__ void geometry(const Weight &wt) {
+        ratio = exp((value_of(bits0 + dir) - value_of(bits0)) * wt.inv_t);
+    }
+};
+__device__ __forceinline__ Own own_bins(const Weight &wt) {
+    const int t = threadIdx.x;
+    Own o;
+    o.dir = t <= kLastPositive ? -1 : 1;
+    o.bits0 = t <= kLastPositive ? kMagLo + kBinsHalf - 1 - kOwn * t : 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
+    o.geometry(wt);
+    return o;
+}
+__device__ __forceinline__ Weight weight_of(const RowParams &par) {
+    return Weight{0.0, uniform(1.0 / (double)par.temperature)};
+}
+
+// Set by one thread per word before the barrier that precedes draw_way.
+__device__ __forceinline__ void draw_clear(Draw &sh) {
+    const int t = threadIdx.x;
+    if (t < 4) sh.owner[t] = 0;
+    if (t == 4) sh.first = ~0u;
+    if (t == 5) sh.win_count[0] = 0;
+    if (t == 6) sh.win_mass[0] = 0.0;
+}
+
+// Draws a token's value and its ordinal. Used by whole workgroups. max_key: the key of the
+// row's largest value where it is known (0: not).
 template <Way way>
-__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par) {
+__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par, Weight wt, Own own,
+                                          uint32_t max_key) {
     Hist &h = sh.h;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
     constexpr bool longway = way == kLong;
     constexpr int windows = longway ? kWindows : 1;
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
-    Weight wt;
-    wt.max = 0.0;
-    wt.inv_t = uniform(1.0 / (double)par.temperature);
-    if (t < 8) sh.owner[t] = 0;
-    if (t == 8) sh.first = ~0u;
-    if (t == 9) {
-        sh.win_count[0] = 0;
-        sh.win_mass[0] = 0.0;
+    if (max_key) wt.max = value_of(bits_of(max_key));
+
+    // Side items in order, by the wave that owns them: a value's place is the number of
+    // larger entries and its first entry stands there for all equal ones (the places of the
+    // others stay empty); zero stands between the signs. The low pattern comes after every
+    // bin, the last thread's.
+    const int side_n = longway ? 0 : (int)h.side_n, zeros = longway ? 0 : (int)h.zeros;
+    const int sides = side_n + (zeros ? 1 : 0);
+    const uint32_t low_n = !longway && t == kThreads - 1 ? h.low_n : 0;
+    if (wave == kSideWave && lane <= (int)kSideMax) {
+        sh.item_count[lane] = 0;
+        if (lane < sides) {
+            const uint32_t mine = lane < side_n ? h.side[lane] : 0, key = key_of(mine);
+            uint32_t place = 0, equal = 0;
+            bool lead = true;
+            for (int j = 0; j < side_n; ++j) {
+                const uint32_t o = key_of(h.side[j]);
+                place += o > key;
+                equal += o == key;
+                lead = lead && !(o == key && j < lane);
+            }
+            if (lane < side_n && zeros) place += 0x8000u > key;
+            if (lead) {
+                sh.item_bits[place] = mine;
+                sh.item_count[place] = lane < side_n ? equal : zeros;
+            }
+        }
     }
 
-    // side items in order: a value's place is the number of larger entries and its first
-    // entry stands there for all equal ones (the places of the others stay empty); zero
-    // stands between the signs. The low pattern is the last item, after every bin.
-    const uint32_t side_n = longway ? 0 : h.side_n, zeros = longway ? 0 : h.zeros, low_n = longway ? 0 : h.low_n;
-    const int sides = (int)(side_n + (zeros ? 1 : 0));
-    if (t < kItems) sh.item_count[t] = 0;
-    __syncthreads();
-    if (t < sides) {
-        const uint32_t mine = t < (int)side_n ? h.side[t] : 0, key = key_of(mine);
-        uint32_t place = 0, equal = 0;
-        bool lead = true;
-        for (uint32_t j = 0; j < side_n; ++j) {
-            const uint32_t o = key_of(h.side[j]);
-            place += o > key;
-            equal += o == key;
-            lead = lead && !(o == key && (int)j < t);
-        }
-        if (t < (int)side_n && zeros) place += 0x8000u > key;
-        if (lead) {
-            sh.item_bits[place] = mine;
-            sh.item_count[place] = t < (int)side_n ? equal : zeros;
-        }
-    } else if (t == kThreads - 1) {
-        sh.item_bits[kItems - 1] = h.low_bits;
-        sh.item_count[kItems - 1] = low_n;
-    }
-    __syncthreads();
-
-    // this thread's bins, descending: patterns bits0, bits0 + dir, ...
-    uint32_t bits0 = 0, c = 0, ec = 0;
-    int dir = 0, f = kOwn;        // f: its first occurring bin
-    double wf = 0.0, ratio = 0.0, w = 0.0, ew = 0.0;  // that one's weight; W of the thread and before it
+    uint32_t c = 0, ec = 0;
+    int f = kOwn;                        // the thread's first occurring bin
+    double wf = 0.0, w = 0.0, ew = 0.0;  // that one's weight; W of the thread and before it
+    double head = 0.0;                   // the weight of its first value, bins or items
+    uint32_t total = 0;
+    double wtotal = 0.0;
     int current = -1;
 
-    // Items of thread t after its bins: [item_b, item_e).
-    const int item_b = t == kThreads - 1 ? kItems - 1 : 0;
-    const int item_e = longway ? item_b : (t == kLastPositive ? sides : (t == kThreads - 1 ? kItems : 0));
-
-    // The thread's counts, in order.
-    auto counts = [&](uint32_t (&n)[kOwn]) {
-        const bool flip = !longway && t <= kLastPositive;
-        const int first = flip ? kBinsHalf - kOwn * (t + 1) : kOwn * t;
-        const uint4 *p = (const uint4 *)&h.bin[first];
-        uint4 a = p[flip ? 1 : 0], b = p[flip ? 0 : 1];
+    auto bin_at = [&](int thread, int j) -> uint32_t {  // a thread's j-th bin
+        const int at = !longway && thread <= kLastPositive ? kBinsHalf - 1 - kOwn * thread - j : kOwn * thread + j;
+        uint32_t n = h.bin[at];
         if constexpr (way == kQuarters) {
-            const uint4 *p2 = (const uint4 *)&second_table(sh)[first];
-            const uint4 a2 = p2[flip ? 1 : 0], b2 = p2[flip ? 0 : 1];
-            auto sum = [](uint32_t u, uint32_t v) { return (u & 0xFFFFu) + (u >> 16) + (v & 0xFFFFu) + (v >> 16); };
-            a = make_uint4(sum(a.x, a2.x), sum(a.y, a2.y), sum(a.z, a2.z), sum(a.w, a2.w));
-            b = make_uint4(sum(b.x, b2.x), sum(b.y, b2.y), sum(b.z, b2.z), sum(b.w, b2.w));
+            const uint32_t n2 = second_table(sh)[at];
+            n = (n & 0xFFFFu) + (n >> 16) + (n2 & 0xFFFFu) + (n2 >> 16);
         }
-        const uint32_t x[kOwn] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) n[j] = flip ? x[4 * (j / 4) + 3 - j % 4] : x[j];
+        return n;
     };
 
     auto analyse = [&](int win) {
         // read before the barriers below, behind which it is set
-        const bool find_max = current < 0 || sh.first == ~0u;
+        const bool find_max = !max_key && (current < 0 || sh.first == ~0u);
         if (longway) {  // count this window's patterns
             __syncthreads();
             for (int i = t; i < (int)kBins / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
@@ -402,17 +413,13 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             if (at >= 0) single(row.p[at]);
             __syncthreads();
             const uint32_t key0 = 65535u - (uint32_t)win * kBins - kOwn * t;
-            dir = key0 & 0x8000u ? -1 : 1;
-            bits0 = key0 & 0x8000u ? key0 & 0x7FFFu : ~key0 & 0xFFFFu;
-        } else if (t <= kLastPositive) {
-            dir = -1;
-            bits0 = kMagLo + kBinsHalf - 1 - kOwn * t;
-        } else {
-            dir = 1;
-            bits0 = 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
+            own.dir = key0 & 0x8000u ? -1 : 1;
+            own.bits0 = bits_of(key0);
+            own.geometry(wt);
         }
         uint32_t cnt[kOwn];
-        counts(cnt);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) cnt[j] = bin_at(t, j);
         c = 0;
         f = kOwn;
 #pragma unroll
@@ -420,47 +427,49 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             c += cnt[j];
             if (cnt[j]) f = j;
         }
-        if (find_max) {  // the largest value, once
+        if (find_max) {  // the largest value, once: its key's place from the top
             uint32_t place = ~0u;
-            if (f < kOwn) place = t * 128 + f;
-            else
-                for (int i = item_e - 1; i >= item_b; --i)
-                    if (sh.item_count[i]) place = t * 128 + kOwn + i;
+            if (f < kOwn) place = 65535u - key_of(own.bits0 + own.dir * f);
+            else if (t == kLastPositive && sides) place = 65535u - key_of(sh.item_bits[0]);
+            else if (low_n) place = 65535u - key_of(h.low_bits);
             const uint64_t mask = __ballot(place != ~0u);  // places ascend with the lane
             if (mask && lane == __builtin_ctzll(mask)) atomicMin(&sh.first, place);
             __syncthreads();
             const uint32_t first = uniform(sh.first);
-            if (first != ~0u) {
-                const uint32_t ft = first >> 7, fj = first & 127;
-                if (fj >= kOwn) wt.max = value_of(sh.item_bits[fj - kOwn]);
-                else if (longway) {
-                    const uint32_t key = 65535u - (uint32_t)win * kBins - (kOwn * ft + fj);
-                    wt.max = value_of(key & 0x8000u ? key & 0x7FFFu : ~key & 0xFFFFu);
-                } else if (ft <= kLastPositive) wt.max = value_of(kMagLo + kBinsHalf - 1 - kOwn * ft - fj);
-                else wt.max = value_of(0x8000u | (kMagLo + kOwn * (ft - kLastPositive - 1) + fj));
-                wt.max = uniform(wt.max);
-                // the items' weights, one a thread
-                if (t < kItems && sh.item_count[t]) sh.item_weight[t] = wt(sh.item_bits[t]);
-            }
-            __syncthreads();
+            if (first != ~0u) wt.max = uniform(value_of(bits_of(65535u - first)));
         }
         w = 0.0;
         if (f < kOwn) {
-            wf = wt(bits0 + dir * f);
-            const double gap = value_of(bits0) - value_of(bits0 + dir);
-            ratio = exp(-gap * wt.inv_t);
+            wf = head = wt(own.bits0 + own.dir * f);
             double x = wf;
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
                 if (cnt[j]) w += cnt[j] * x;
-                if (j >= f) x *= ratio;
+                if (j >= f) x *= own.ratio;
             }
         }
-        for (int i = item_b; i < item_e; ++i)
-            if (sh.item_count[i]) {
-                c += sh.item_count[i];
-                w += sh.item_count[i] * sh.item_weight[i];
+        if (!longway && wave == kSideWave && sides) {  // the items' counts and weights to its last lane
+            uint32_t n = 0;
+            double v = 0.0;
+            if (lane < sides) {
+                n = sh.item_count[lane];
+                if (n) sh.item_weight[lane] = v = wt(sh.item_bits[lane]);
             }
+            const uint32_t items = wave_scan(n);
+            const double weight = wave_scan(n * v);
+            if (lane == 63) {
+                if (c == 0) head = sh.item_weight[0];
+                c += items;
+                w += weight;
+            }
+        }
+        if (low_n) {
+            const double v = wt(h.low_bits);
+            sh.low_weight = v;
+            if (c == 0) head = v;
+            c += low_n;
+            w += low_n * v;
+        }
         // exclusive prefix over the threads, after the windows before this one
         const uint32_t ic = wave_scan(c);
         const double iw = wave_scan(w);
@@ -473,33 +482,35 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
         __syncthreads();
         const uint32_t sc = wave_scan(lane < kWaves ? sh.csum[lane] : 0u);
         const double sw = wave_scan(lane < kWaves ? sh.wsum[lane] : 0.0);
-        const uint32_t bc = sh.win_count[win];
-        const double bw = sh.win_mass[win];
+        const uint32_t bc = longway ? sh.win_count[win] : 0;
+        const double bw = longway ? sh.win_mass[win] : 0.0;
         ec = bc + xc;
         ew = bw + xw;
         if (wave) {
-            ec += __builtin_amdgcn_readlane(sc, wave - 1);
+            ec += __builtin_amdgcn_readlane((int)sc, wave - 1);
             ew += lane_value(sw, wave - 1);
         }
-        if (t == 0) {
-            sh.win_count[win + 1] = bc + __builtin_amdgcn_readlane(sc, kWaves - 1);
-            sh.win_mass[win + 1] = bw + lane_value(sw, kWaves - 1);
+        total = bc + __builtin_amdgcn_readlane((int)sc, kWaves - 1);
+        wtotal = bw + lane_value(sw, kWaves - 1);
+        if (longway) {
+            if (t == 0) {
+                sh.win_count[win + 1] = total;
+                sh.win_mass[win + 1] = wtotal;
+            }
+            if (c && ec == bc) sh.win_first[win] = head;
+            __syncthreads();
         }
-        // the weight of the window's first value, where it has any
-        if (longway && c && ec == sh.win_count[win]) sh.win_first[win] = wf;
-        __syncthreads();
         current = win;
     };
 
     for (int win = 0; win < windows; ++win) analyse(win);
-    const uint32_t total = uniform(sh.win_count[windows]);
-    const double wtotal = uniform(sh.win_mass[windows]);
     if (total == 0) return out;  // nothing to draw from
     out.any = true;
+    uint32_t n = total;
+    double mass = wtotal;
 
-    // Finds the thread that crosses n tokens or mass x, and in it the item.
-    int seeks = 0;
-    auto seek = [&](Seek mode, uint32_t n, double x) {
+    // Finds the thread that crosses n tokens or mass x, and in it the value.
+    auto seek = [&](int slot, Seek mode, double x) {
         if (longway) {
             int win = 0;
             for (int i = 0; i < kWindows; ++i) {
@@ -514,101 +525,99 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             }
             if (win != current) analyse(win);
         }
-        const int slot = seeks++ & 7;
         // holds for a leading stretch of the threads that own tokens
-        const bool in = c && (mode == kMass ? ec < n
-                              : mode == kTopP ? ec == 0 || ew < x
-                              : mode == kMinP ? (f < kOwn ? wf : sh.item_weight[item_b]) >= x || ec == 0
-                                              : ec < n && (ec == 0 || ew <= x));
+        const bool in = c && (ec == 0 || (mode == kMass ? ec < n
+                                          : mode == kTopP ? ew < x
+                                          : mode == kMinP ? head >= x
+                                                          : ec < n && ew <= x));
         const uint64_t mask = __ballot(in);
         if (mask && lane == 0) atomicMax(&sh.owner[slot], (uint32_t)(wave * 64 + 64 - __builtin_clzll(mask)));
         __syncthreads();
-        if (sh.owner[slot] == (uint32_t)t + 1) {
-            // the item that crosses, or else the last one with weight: the first whose
-            // measure (tokens, W, or less its weight) exceeds the bound
-            const double bound = mode == kMass ? (double)n - 0.5 : (mode == kTopP ? below(x) : (mode == kMinP ? -x : x));
-            uint32_t pos = ec, at_pos = ec, at_k = 0, at_bits = 0;
-            double before = ew, at_before = ew, at_v = 0.0;
-            bool crossed = false;
-            auto visit = [&](uint32_t k, uint32_t b, double v) {
-                k = min(k, n - pos);  // no more than n tokens
-                const bool live = k != 0 && !crossed;
-                const double end = before + k * v;
-                const double measure = mode == kMass ? (double)(pos + k) : (mode == kMinP ? -v : end);
-                const bool over = measure > bound;
-                if (live && (over || v > 0.0 || at_k == 0)) {
-                    at_pos = pos;
-                    at_before = before;
-                    at_k = k;
-                    at_v = v;
-                    at_bits = b;
+        const int owner = (int)uniform(sh.owner[slot]) - 1;
+        if (owner >> 6 == wave) {
+            // its wave looks at its values, one a lane: the bins, then the items behind them
+            const int ol = owner & 63;
+            const uint32_t first = __builtin_amdgcn_readlane((int)ec, ol);
+            const double start = lane_value(ew, ol), r1 = lane_value(own.ratio, ol);
+            const int of = __builtin_amdgcn_readlane(f, ol);
+            uint32_t k = 0, bits = 0;
+            double v = 0.0;
+            if (lane < kOwn) {
+                k = bin_at(owner, lane);
+                bits = __builtin_amdgcn_readlane((int)own.bits0, ol) + __builtin_amdgcn_readlane(own.dir, ol) * lane;
+                const int d = max(lane - of, 0);
+                const double r2 = r1 * r1;
+                v = lane_value(wf, ol) * (d & 1 ? r1 : 1.0) * (d & 2 ? r2 : 1.0) * (d & 4 ? r2 * r2 : 1.0);
+            } else if (!longway) {
+                const int i = lane - kOwn;
+                if (owner == kLastPositive && i < sides) {
+                    k = sh.item_count[i];
+                    bits = sh.item_bits[i];
+                    v = sh.item_weight[i];
+                } else if (owner == kThreads - 1 && i == 0 && h.low_n) {
+                    k = h.low_n;
+                    bits = h.low_bits;
+                    v = sh.low_weight;
                 }
-                if (live) {
-                    pos += k;
-                    before = end;
-                    crossed = over;
-                }
-            };
-            double weight = wf, by = ratio;
-            asm volatile("" : "+v"(weight), "+v"(by));  // not computed ahead of the steps that need it
-            uint32_t cnt[kOwn];
-            counts(cnt);
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                visit(cnt[j], bits0 + dir * j, weight);
-                if (j >= f) weight *= by;
             }
-#pragma unroll 1
-            for (int i = item_b; i < item_e; ++i) visit(sh.item_count[i], sh.item_bits[i], sh.item_weight[i]);
-            uint32_t part = at_k, ord = at_k ? at_k - 1 : 0;  // tokens of the item, or which of them
+            if (k == 0) v = 0.0;  // (an unoccurring pattern's may be anything)
+            const uint32_t pos = first + wave_down(wave_scan(k));
+            k = pos < n ? min(k, n - pos) : 0;  // no more than n tokens
+            const double before = start + wave_down(wave_scan(k * v)), end = before + k * v;
+            // the value that crosses, or else the last one with weight
+            const bool over = k && (mode == kMass ? pos + k >= n : mode == kTopP ? end >= x : mode == kMinP ? v < x : end > x);
+            const uint64_t crossing = __ballot(over), weighty = __ballot(k && v > 0.0), any = __ballot(k != 0);
+            const int at = crossing ? __builtin_ctzll(crossing)
+                                    : (weighty ? 63 - __builtin_clzll(weighty) : __builtin_ctzll(any | 1ull << 63));
+            const uint32_t ak = __builtin_amdgcn_readlane((int)k, at), apos = __builtin_amdgcn_readlane((int)pos, at);
+            const double av = lane_value(v, at), ab = lane_value(before, at);
+            uint32_t part = ak, ord = ak ? ak - 1 : 0;  // tokens of the value, or which of them
             if (mode == kMinP) {
-                if (crossed) part = 0;
+                if (crossing) part = 0;
             } else if (mode == kTopP || mode == kDraw) {
-                double y = at_v > 0.0 ? (x - at_before) / at_v : (double)at_k;
-                y = fmin(fmax(y, 0.0), (double)at_k);
+                double y = av > 0.0 ? (x - ab) / av : (double)ak;
+                y = fmin(fmax(y, 0.0), (double)ak);
                 if (mode == kTopP) {  // tokens whose W before them is below x
                     part = (uint32_t)ceil(y);
-                    while (part > 0 && at_before + (part - 1) * at_v >= x) --part;
-                    while (part < at_k && at_before + part * at_v < x) ++part;
-                } else if (crossed) {
-                    ord = min((uint32_t)y, at_k - 1);
-                    while (ord > 0 && at_before + ord * at_v > x) --ord;
-                    while (ord + 1 < at_k && at_before + (ord + 1) * at_v <= x) ++ord;
+                    while (part > 0 && ab + (part - 1) * av >= x) --part;
+                    while (part < ak && ab + part * av < x) ++part;
+                } else if (crossing) {
+                    ord = min((uint32_t)y, ak - 1);
+                    while (ord > 0 && ab + ord * av > x) --ord;
+                    while (ord + 1 < ak && ab + (ord + 1) * av <= x) ++ord;
                 }
             }
-            sh.found.pos = at_pos + part;
-            sh.found.mass = at_before + part * at_v;
-            sh.found.bits = at_bits;
-            sh.found.ord = ord;
+            if (lane == at) {
+                sh.found.pos = apos + part;
+                sh.found.mass = ab + part * av;
+                sh.found.bits = bits;
+                sh.found.ord = ord;
+            }
         }
-        __syncthreads();
+        __syncthreads();  // (and the next seek's first barrier is behind every look at found)
     };
 
-    uint32_t n = total;
-    double mass = wtotal;
-    const uint32_t k = par.k;
-    const float top_p = par.top_p, min_p = par.min_p;
     // W(n1), n2, n3 (each with its W) where they limit, the draw
 #pragma unroll 1
     for (int step = 0; step < 4; ++step) {
         Seek mode = kMass;
         double x = 0.0;
         if (step == 0) {
-            if (!(k && k < n)) continue;
-            n = k;
+            if (!(par.k && par.k < n)) continue;
+            n = par.k;
         } else if (step == 1) {
-            if (!(top_p < 1.f)) continue;
+            if (!(par.top_p < 1.f)) continue;
             mode = kTopP;
-            x = (double)top_p * mass;
+            x = (double)par.top_p * mass;
         } else if (step == 2) {
-            if (!(min_p > 0.f)) continue;
+            if (!(par.min_p > 0.f)) continue;
             mode = kMinP;
-            x = (double)min_p;
+            x = (double)par.min_p;
         } else {
             mode = kDraw;
             x = (double)par.u * mass;
         }
-        seek(mode, n, x);
+        seek(step, mode, x);
         const uint32_t pos = uniform(sh.found.pos);
         if (mode == kMass) {
             mass = uniform(sh.found.mass);
@@ -616,7 +625,6 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             n = max(pos, 1u);
             mass = pos ? uniform(sh.found.mass) : 1.0;  // the first token's weight
         }
-        __syncthreads();
     }
     out.bits = uniform(sh.found.bits);
     out.ordinal = uniform(sh.found.ord);
@@ -624,13 +632,8 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     return out;
 }
 
-__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par) {
-    return draw_way<kLong>(sh, row, par);
-}
-
-__device__ __forceinline__ Drawn draw_row(Draw &sh, const Row &row, const RowParams &par) {
-    if (sh.h.odd || sh.h.side_n > kSideMax) return draw_long(sh, row, par);
-    return draw_way<kWhole>(sh, row, par);
+__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par, const Weight &wt) {
+    return draw_way<kLong>(sh, row, par, wt, Own{}, 0);
 }
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
@@ -754,6 +757,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
     const RowParams rp = row_params(par, m);
     const int quarter = (row.nvec + 3) / 4;
     hist_clear(sh.h);
+    draw_clear(sh);
     if constexpr (way == kQuarters) {
         for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)sh.bin2)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
@@ -765,12 +769,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
         __syncthreads();
         hist_count(sh.h, sh.h.bin, 1, row, 0, row.nvec, true, true);
     }
+    const Weight wt = weight_of(rp);
+    const Own own = own_bins(wt);
     __syncthreads();
     if (sh.h.odd || sh.h.side_n > kSideMax) {
         if (threadIdx.x == 0) tokens[m] = kLongWay;
         return;
     }
-    const Drawn d = draw_way<way>(sh, row, rp);
+    const Drawn d = draw_way<way>(sh, row, rp, wt, own, 0);
     int token = -1;
     if (d.any) {
         const uint32_t mag = (d.bits & 0x7FFFu) - kMagLo;
@@ -803,9 +809,11 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
         const bool mine = tokens[m] == kLongWay;
         __syncthreads();  // every thread has read the mark, and the row before is done with
         if (!mine) continue;
+        draw_clear(sh);
+        __syncthreads();
         const Row row = make_row(logits + m * ld, V);
         const RowParams rp = row_params(par, m);
-        const Drawn d = draw_way<kLong>(sh, row, rp);
+        const Drawn d = draw_way<kLong>(sh, row, rp, weight_of(rp), Own{}, 0);
         int token = -1;
         if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
         if (threadIdx.x == 0) {
@@ -827,13 +835,13 @@ constexpr int kMaxParts = kThreads;
 __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
                                                                 uint32_t *__restrict__ parts, int V, int C, int vpp) {
     __shared__ __attribute__((aligned(16))) Hist h;
-    __shared__ uint32_t wsum[kWaves][2], entries;
+    __shared__ uint32_t wsum[kWaves][2], entries, largest;
     const int64_t m = blockIdx.x / C;
     const int part = blockIdx.x % C;
     const Row row = make_row(logits + m * ld, V);
     const uint32_t k = row_params(par, m).k;
     hist_clear(h);
-    if (threadIdx.x == 0) entries = 0;
+    if (threadIdx.x == 0) entries = largest = 0;
     __syncthreads();
     const int vb = min(part * vpp, row.nvec), ve = min(vb + vpp, row.nvec);
     hist_count(h, h.bin, 1, row, vb, ve, part == 0, part == C - 1);
@@ -880,18 +888,28 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
             if (n[s][j]) {
                 const uint32_t above = (at & kCountMask) + (s ? middle : 0), pos = at >> kCountBits;
                 if (!k || above < k) {
-                    dst[kHeader + pos] = (s * kBinsHalf + 4 * t + j) << kCountBits | n[s][j];
+                    const uint32_t place = s * kBinsHalf + 4 * t + j;
+                    dst[kHeader + pos] = place << kCountBits | n[s][j];
                     last = pos + 1;
+                    if (pos == 0) {
+                        const uint32_t bin = bin_order(place);
+                        atomicMax(&largest, key_of((bin / kBinsHalf << 15) | (kMagLo + bin % kBinsHalf)));
+                    }
                 }
                 at += n[s][j] + (1u << kCountBits);
             }
         if (last) atomicMax(&entries, last);
     }
-    if (t < (int)min(h.side_n, kSideMax)) dst[kHeader + kBins + t] = h.side[t];
+    if (t < (int)min(h.side_n, kSideMax)) {
+        dst[kHeader + kBins + t] = h.side[t];
+        atomicMax(&largest, key_of(h.side[t]));
+    }
+    if (t == 0 && h.zeros) atomicMax(&largest, 0x8000u);
+    if (t == 0 && h.low_n) atomicMax(&largest, key_of(h.low_bits));
     __syncthreads();
     if (t == 0) {
         ((uint4 *)dst)[0] = make_uint4(entries, h.side_n, h.zeros, h.odd);
-        ((uint4 *)dst)[1] = make_uint4(h.low_n, h.low_bits, 0, 0);
+        ((uint4 *)dst)[1] = make_uint4(h.low_n, h.low_bits, largest, 0);
     }
 }
 
@@ -918,6 +936,10 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     const int first = C < kWaves ? wave % C : wave, sub = C < kWaves ? wave / C : 0;
     const uint32_t lane0 = sub * 64 + lane, step = shared * 64;
     uint32_t kept[kTwo][kAhead], entries[kTwo] = {0, 0};
+    Weight wt;
+    Own own;
+    uint32_t largest = 0;
+    for (int c = lane; c < C; c += 64) largest = max(largest, src[(int64_t)c * kPartWords + 6]);
     for (int c0 = 0; c0 < C; c0 += kTwo * kWaves) {
         uint4 a[kTwo], b[kTwo];
 #pragma unroll
@@ -928,6 +950,10 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             b[j] = ((const uint4 *)p)[1];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) kept[j][i] = p[kHeader + min(step * i + lane0, kBins - 1)];
+        }
+        if (c0 == 0) {  // beside the loads
+            wt = weight_of(rp);
+            own = own_bins(wt);
         }
 #pragma unroll
         for (int j = 0; j < kTwo; ++j) {
@@ -954,8 +980,12 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
         }
     }
     for (int c = t; c < C; c += kThreads) in_part[c] = 0;
+    draw_clear(sh);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, x));
     __syncthreads();
-    const Drawn d = draw_row(sh, row, rp);
+    const Drawn d = h.odd || h.side_n > kSideMax ? draw_long(sh, row, rp, wt)
+                                                 : draw_way<kWhole>(sh, row, rp, wt, own, uniform(largest));
     int token = -1;
     if (d.any) {
         const uint32_t q = (d.bits & 0x7FFFu) - kMagLo;
@@ -1061,6 +1091,7 @@ SamplePlan plan_sample(int64_t M, int64_t V, int num_cus) {
     const int64_t nvec = V / 8 + 1;
     // parts of a row: enough workgroups to fill the chip, at least one vector a thread
     int64_t C = std::min<int64_t>((num_cus + M - 1) / M, (nvec + kThreads - 1) / kThreads);
+    C = C < 4 ? 1 : std::min<int64_t>(C, 8);
     if (C > 1) C = std::max<int64_t>(C, (nvec + kMaxPartVectors - 1) / kMaxPartVectors);
     p.parts = (int)std::max<int64_t>(C, 1);
     p.vectors_per_part = (int)((nvec + p.parts - 1) / p.parts);
