@@ -260,7 +260,7 @@ __device__ __forceinline__ double uniform(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     return __builtin_bit_cast(double, (uint64_t)uniform((uint32_t)u) | (uint64_t)uniform((uint32_t)(u >> 32)) << 32);
 }
-// The value one lane down, 0 in lane 0.
+// The value one lane down, 0 in lane 0. All lanes take part in these scans.
 template <typename T>
 __device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
 
@@ -275,12 +275,12 @@ struct Draw {
     Hist h;
     uint32_t item_bits[kSideMax + 1], item_count[kSideMax + 1];  // side items in order
     double item_weight[kSideMax + 1], low_weight;
-    double wsum[kWaves], win_mass[kWindows + 1], win_first[kWindows];
+    double wsum[kWaves], whead[kWaves], win_mass[kWindows + 1], win_first[kWindows];
     uint32_t csum[kWaves], win_count[kWindows + 1];
-    uint32_t first, owner[4];
+    uint32_t first;
     uint32_t count[kWaves];  // locate's
     int at;
-    Found found;
+    Found found[4];          // one for each seek: no wave waits for the others to have read the last
 };
 
 // A row's quarters: the second of two tables, where a kernel has one.
@@ -326,7 +326,6 @@ __device__ __forceinline__ Weight weight_of(const RowParams &par) {
 // Set by one thread per word before the barrier that precedes draw_way.
 __device__ __forceinline__ void draw_clear(Draw &sh) {
     const int t = threadIdx.x;
-    if (t < 4) sh.owner[t] = 0;
     if (t == 4) sh.first = ~0u;
     if (t == 5) sh.win_count[0] = 0;
     if (t == 6) sh.win_mass[0] = 0.0;
@@ -375,8 +374,8 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     int f = kOwn;                        // the thread's first occurring bin
     double wf = 0.0, w = 0.0, ew = 0.0;  // that one's weight; W of the thread and before it
     double head = 0.0;                   // the weight of its first value, bins or items
-    uint32_t total = 0;
-    double wtotal = 0.0;
+    uint32_t total = 0, sc = 0, wave_c = 0;  // sc, sw: in lane v, tokens and W up to wave v's end
+    double wtotal = 0.0, sw = 0.0, wave_w = 0.0, wave_head = 0.0;  // wave_*: and before it
     int current = -1;
 
     auto bin_at = [&](int thread, int j) -> uint32_t {  // a thread's j-th bin
@@ -477,21 +476,26 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             sh.csum[wave] = ic;
             sh.wsum[wave] = iw;
         }
+        const uint64_t some = __ballot(c != 0);
+        if (some && lane == __builtin_ctzll(some)) sh.whead[wave] = head;
         const uint32_t xc = wave_down(ic);
         const double xw = wave_down(iw);
         __syncthreads();
-        const uint32_t sc = wave_scan(lane < kWaves ? sh.csum[lane] : 0u);
-        const double sw = wave_scan(lane < kWaves ? sh.wsum[lane] : 0.0);
         const uint32_t bc = longway ? sh.win_count[win] : 0;
         const double bw = longway ? sh.win_mass[win] : 0.0;
-        ec = bc + xc;
-        ew = bw + xw;
-        if (wave) {
-            ec += __builtin_amdgcn_readlane((int)sc, wave - 1);
-            ew += lane_value(sw, wave - 1);
+        sc = bc + wave_scan(lane < kWaves ? sh.csum[lane] : 0u);
+        sw = bw + wave_scan(lane < kWaves ? sh.wsum[lane] : 0.0);
+        wave_head = lane < kWaves ? sh.whead[lane] : 0.0;
+        wave_c = wave_down(sc);  // (not within the choice: a lane that is switched off gives nothing)
+        wave_w = wave_down(sw);
+        if (lane == 0) {
+            wave_c = bc;
+            wave_w = bw;
         }
-        total = bc + __builtin_amdgcn_readlane((int)sc, kWaves - 1);
-        wtotal = bw + lane_value(sw, kWaves - 1);
+        ec = __builtin_amdgcn_readlane((int)wave_c, wave) + xc;
+        ew = lane_value(wave_w, wave) + xw;
+        total = __builtin_amdgcn_readlane((int)sc, kWaves - 1);
+        wtotal = lane_value(sw, kWaves - 1);
         if (longway) {
             if (t == 0) {
                 sh.win_count[win + 1] = total;
@@ -509,7 +513,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     uint32_t n = total;
     double mass = wtotal;
 
-    // Finds the thread that crosses n tokens or mass x, and in it the value.
+    // Finds the wave, in it the thread, and in that the value that crosses n tokens or mass x.
     auto seek = [&](int slot, Seek mode, double x) {
         if (longway) {
             int win = 0;
@@ -525,18 +529,18 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             }
             if (win != current) analyse(win);
         }
-        // holds for a leading stretch of the threads that own tokens
-        const bool in = c && (ec == 0 || (mode == kMass ? ec < n
-                                          : mode == kTopP ? ew < x
-                                          : mode == kMinP ? head >= x
-                                                          : ec < n && ew <= x));
-        const uint64_t mask = __ballot(in);
-        if (mask && lane == 0) atomicMax(&sh.owner[slot], (uint32_t)(wave * 64 + 64 - __builtin_clzll(mask)));
-        __syncthreads();
-        const int owner = (int)uniform(sh.owner[slot]) - 1;
-        if (owner >> 6 == wave) {
+        // whether it is not before this stretch of tokens: holds for a leading part of them
+        auto within = [&](uint32_t before_n, double before_w, double first) {
+            return before_n == 0 || (mode == kMass ? before_n < n
+                                     : mode == kTopP ? before_w < x
+                                     : mode == kMinP ? first >= x
+                                                     : before_n < n && before_w <= x);
+        };
+        const uint64_t waves = __ballot(lane < kWaves && sc != wave_c && within(wave_c, wave_w, wave_head));
+        if (waves && 63 - __builtin_clzll(waves) == wave) {  // every wave finds the same one
+            const uint64_t mask = __ballot(c && within(ec, ew, head));
+            const int ol = mask ? 63 - __builtin_clzll(mask) : 0, owner = wave * 64 + ol;
             // its wave looks at its values, one a lane: the bins, then the items behind them
-            const int ol = owner & 63;
             const uint32_t first = __builtin_amdgcn_readlane((int)ec, ol);
             const double start = lane_value(ew, ol), r1 = lane_value(own.ratio, ol);
             const int of = __builtin_amdgcn_readlane(f, ol);
@@ -587,14 +591,9 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
                     while (ord + 1 < ak && ab + (ord + 1) * av <= x) ++ord;
                 }
             }
-            if (lane == at) {
-                sh.found.pos = apos + part;
-                sh.found.mass = ab + part * av;
-                sh.found.bits = bits;
-                sh.found.ord = ord;
-            }
+            if (lane == at) sh.found[slot] = Found{ab + part * av, apos + part, bits, ord};
         }
-        __syncthreads();  // (and the next seek's first barrier is behind every look at found)
+        __syncthreads();
     };
 
     // W(n1), n2, n3 (each with its W) where they limit, the draw
@@ -618,16 +617,16 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             x = (double)par.u * mass;
         }
         seek(step, mode, x);
-        const uint32_t pos = uniform(sh.found.pos);
+        const uint32_t pos = uniform(sh.found[step].pos);
         if (mode == kMass) {
-            mass = uniform(sh.found.mass);
+            mass = uniform(sh.found[step].mass);
         } else if (mode != kDraw && pos < n) {
             n = max(pos, 1u);
-            mass = pos ? uniform(sh.found.mass) : 1.0;  // the first token's weight
+            mass = pos ? uniform(sh.found[step].mass) : 1.0;  // the first token's weight
         }
     }
-    out.bits = uniform(sh.found.bits);
-    out.ordinal = uniform(sh.found.ord);
+    out.bits = uniform(sh.found[3].bits);
+    out.ordinal = uniform(sh.found[3].ord);
     out.logprob = (float)(wt.exponent(out.bits) - log(mass));
     return out;
 }
