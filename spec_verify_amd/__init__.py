@@ -533,10 +533,33 @@ def ct_to_gptq(weight_packed, weight_scale, group_size=128, qweight=None, scales
 # ---- per-request operators of a verify chunk ----------------------------------------
 # Calls of a few microseconds: arguments are looked at once, and passed as integers.
 
+class _Kinds:
+    """What the calls below look at in PyTorch, looked up once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.Tensor, self.empty, self.cuda = torch.Tensor, torch.empty, torch.cuda
+        self.uint8, self.bfloat16, self.float32, self.int32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
+        self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)
+        self.f32, self.i32 = (torch.float32,), (torch.int32,)
+        # the stream's handle alone where PyTorch offers it: a Stream object takes 2.7 us to make
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_kinds_once = None
+
+
+def _kinds():
+    global _kinds_once
+    if _kinds_once is None:
+        _kinds_once = _Kinds()
+    return _kinds_once
+
+
 def _ptr(t, name, dtypes, shape, device):
     """Address of a contiguous tensor of one of `dtypes`, of the given shape, on `device`."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _kinds().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
@@ -551,8 +574,7 @@ def _ptr(t, name, dtypes, shape, device):
 
 def _rows_of(t, name, dtypes):
     """(address, row stride) of a device matrix whose rows are contiguous and apart."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _kinds().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
@@ -571,35 +593,37 @@ def _rows_of(t, name, dtypes):
     return t.data_ptr(), by_row
 
 
-def _bf16_dtypes():
-    torch = _torch()
-    return (torch.bfloat16, torch.int16, torch.uint16)
-
-
-def _on_device(device, call):
-    """call(stream handle) with `device` current: the library launches on the current device."""
-    torch = _torch()
+def _enqueue(device, where, function, *args):
+    """function(*args, stream) with `device` current: the library launches on the current device."""
+    k = _kinds()
     index = device.index
-    # the handle alone where PyTorch offers it: a Stream object takes 2.7 us to make
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if torch.cuda.current_device() == index:
-        return call(raw(index) if raw else torch.cuda.current_stream(device).cuda_stream)
-    with torch.cuda.device(device):
-        return call(raw(index) if raw else torch.cuda.current_stream(device).cuda_stream)
+    if k.cuda.current_device() == index:
+        status = function(*args, k.stream(index))
+    else:
+        with k.cuda.device(device):
+            status = function(*args, k.stream(index))
+    if status:
+        raise SvqError(status, where)
 
 
-def _scratch(nbytes, workspace, device):
+def _scratch(query, shape, workspace, device):
     """The caller's workspace, or one from PyTorch's allocator on the current stream: it
     need not be cleared, no other call shares it, and a call that is captured gets its own
     from the graph's pool. (tensor, address, bytes); the caller keeps the tensor until the
     launch is enqueued."""
-    torch = _torch()
+    k = _kinds()
     if workspace is None:
+        # (asked on the tensors' device, whose size the plans depend on)
+        if k.cuda.current_device() == device.index:
+            nbytes = query(*shape)
+        else:
+            with k.cuda.device(device):
+                nbytes = query(*shape)
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = k.empty(nbytes, dtype=k.uint8, device=device)
         return workspace, workspace.data_ptr(), nbytes
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+    if not isinstance(workspace, k.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -619,8 +643,8 @@ def adapter_add(base, x, a, b, rows, scales, out=None, workspace=None):
     adapter), scales float32 [slots]. base and out may be column slices of wider
     matrices, and out may be base itself.
     """
-    torch = _torch()
-    bf16 = _bf16_dtypes()
+    kd = _kinds()
+    bf16 = kd.bf16
     base_ptr, ld_base = _rows_of(base, "base", bf16)
     dev = base.device
     M, N = base.shape
@@ -631,23 +655,18 @@ def adapter_add(base, x, a, b, rows, scales, out=None, workspace=None):
     x_ptr = _ptr(x, "x", bf16, (M, K), dev)
     a_ptr = _ptr(a, "a", bf16, (slots, R, K), dev)
     b_ptr = _ptr(b, "b", bf16, (slots, N, R), dev)
-    rows_ptr = _ptr(rows, "rows", (torch.int32,), (M,), dev)
-    scales_ptr = _ptr(scales, "scales", (torch.float32,), (slots,), dev)
+    rows_ptr = _ptr(rows, "rows", kd.i32, (M,), dev)
+    scales_ptr = _ptr(scales, "scales", kd.f32, (slots,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = kd.empty((M, N), dtype=kd.bfloat16, device=dev)
         out_ptr, ld_out = out.data_ptr(), N
     else:
         out_ptr, ld_out = _rows_of(out, "out", bf16)
         if out.shape != (M, N) or out.device != dev:
             raise ValueError(f"out must have shape {(M, N)} on {dev}")
-
-    def call(stream):
-        need = 0 if workspace is not None else adapter_workspace_bytes(M, N, K, R, slots)
-        keep, ws, ws_bytes = _scratch(need, workspace, dev)
-        _check(lib().svq_adapter_add(base_ptr, ld_base, x_ptr, a_ptr, b_ptr, rows_ptr, scales_ptr, out_ptr, ld_out,
-                                     M, N, K, R, slots, ws, ws_bytes, stream), "svq_adapter_add")
-
-    _on_device(dev, call)
+    keep, ws, ws_bytes = _scratch(adapter_workspace_bytes, (M, N, K, R, slots), workspace, dev)
+    _enqueue(dev, "svq_adapter_add", lib().svq_adapter_add, base_ptr, ld_base, x_ptr, a_ptr, b_ptr, rows_ptr, scales_ptr,
+             out_ptr, ld_out, M, N, K, R, slots, ws, ws_bytes)
     return out
 
 
@@ -667,26 +686,21 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, work
     temperature <= 0 is greedy. A row with nothing to draw gives -1 and -inf. logits
     may be a column slice of a wider matrix.
     """
-    torch = _torch()
-    ptr, ld = _rows_of(logits, "logits", _bf16_dtypes())
+    kd = _kinds()
+    ptr, ld = _rows_of(logits, "logits", kd.bf16)
     dev = logits.device
     M, V = logits.shape
-    f32, i32, per_row = (torch.float32,), (torch.int32,), (M,)
+    f32, per_row = kd.f32, (M,)
     u_ptr = _ptr(u, "u", f32, per_row, dev)
     t_ptr = None if temperature is None else _ptr(temperature, "temperature", f32, per_row, dev)
-    k_ptr = None if top_k is None else _ptr(top_k, "top_k", i32, per_row, dev)
+    k_ptr = None if top_k is None else _ptr(top_k, "top_k", kd.i32, per_row, dev)
     p_ptr = None if top_p is None else _ptr(top_p, "top_p", f32, per_row, dev)
     m_ptr = None if min_p is None else _ptr(min_p, "min_p", f32, per_row, dev)
-    tokens = torch.empty(M, dtype=torch.int32, device=dev)
-    logprobs = torch.empty(M, dtype=torch.float32, device=dev)
-
-    def call(stream):
-        need = 0 if workspace is not None else sample_workspace_bytes(M, V)
-        keep, ws, ws_bytes = _scratch(need, workspace, dev)
-        _check(lib().svq_sample(ptr, ld, u_ptr, t_ptr, k_ptr, p_ptr, m_ptr, tokens.data_ptr(), logprobs.data_ptr(),
-                                M, V, ws, ws_bytes, stream), "svq_sample")
-
-    _on_device(dev, call)
+    tokens = kd.empty(M, dtype=kd.int32, device=dev)
+    logprobs = kd.empty(M, dtype=kd.float32, device=dev)
+    keep, ws, ws_bytes = _scratch(sample_workspace_bytes, (M, V), workspace, dev)
+    _enqueue(dev, "svq_sample", lib().svq_sample, ptr, ld, u_ptr, t_ptr, k_ptr, p_ptr, m_ptr, tokens.data_ptr(),
+             logprobs.data_ptr(), M, V, ws, ws_bytes)
     return tokens, logprobs
 
 
@@ -699,8 +713,8 @@ def accept_drafts(tokens, inputs, starts):
     committed [M]), int32: the number of accepted drafts, the token that follows
     them, and both in place, -1 elsewhere.
     """
-    torch = _torch()
-    i32 = (torch.int32,)
+    kd = _kinds()
+    i32 = kd.i32
     if tokens.dim() != 1 or starts.dim() != 1 or starts.shape[0] < 2:
         raise ValueError("tokens must be [M] and starts [S + 1] with S >= 1")
     dev, M, S = tokens.device, tokens.shape[0], starts.shape[0] - 1
@@ -709,10 +723,9 @@ def accept_drafts(tokens, inputs, starts):
     s_ptr = _ptr(starts, "starts", i32, (S + 1,), dev)
     if not tokens.is_cuda:
         raise ValueError(f"tokens must be a device tensor, got {dev}")
-    accepted = torch.empty(S, dtype=torch.int32, device=dev)
-    following = torch.empty(S, dtype=torch.int32, device=dev)
-    committed = torch.empty(M, dtype=torch.int32, device=dev)
-    _on_device(dev, lambda stream: _check(
-        lib().svq_accept_drafts(t_ptr, i_ptr, s_ptr, accepted.data_ptr(), following.data_ptr(), committed.data_ptr(),
-                                M, S, stream), "svq_accept_drafts"))
+    accepted = kd.empty(S, dtype=kd.int32, device=dev)
+    following = kd.empty(S, dtype=kd.int32, device=dev)
+    committed = kd.empty(M, dtype=kd.int32, device=dev)
+    _enqueue(dev, "svq_accept_drafts", lib().svq_accept_drafts, t_ptr, i_ptr, s_ptr, accepted.data_ptr(),
+             following.data_ptr(), committed.data_ptr(), M, S)
     return accepted, following, committed
