@@ -225,7 +225,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
     constexpr int kPitch = 32 * NS + 8;      // bf16 elements: rows 16 bytes apart in banks
     constexpr int kEach = 2 * NS;            // ranks of a thread where t is put together
     constexpr int kVec = kEach < 4 ? kEach : 4;
-    constexpr int kAhead = NS < 8 ? 4 : 2;  // K ranges of t in flight
+    constexpr int kAhead = NS <= 2 ? 8 : (NS == 4 ? 4 : 2);  // K ranges of t in flight
     __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
@@ -254,8 +254,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
         }
         return;
     }
-    // t of this thread's row and ranks, summed over the K ranges in order. The first ranges'
-    // loads are issued before those of B and base, which take longer and are waited for later.
+    // t of this thread's row and ranks, summed over the K ranges in order. Loads complete in
+    // order: those of B and base, which take longer, are issued behind the last ranges'.
     float t[kEach], v[kAhead][kEach];
     const char *tp = (const char *)(part + row0 * R);
     const uint32_t t_off = (uint32_t)(tid * R + rank0) * 4;
@@ -276,7 +276,20 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
             }
         }
     };
-    ranges(0);
+    auto add = [&] {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) t[i] += v[k][i];
+    };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) t[i] = 0.f;
+    int k0 = 0;
+    for (; k0 + kAhead < splits; k0 += kAhead) {
+        ranges(k0);
+        add();
+    }
+    ranges(k0);
     uint4 bv[NS][4];
     const char *bp = (const char *)(b + ((int64_t)s * N + col0) * R);
 #pragma unroll
@@ -291,17 +304,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) y[h] = *(const uint4 *)(base + m * ld_base + col + 8 * h);
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) t[i] = 0.f;
-    for (int k0 = 0;;) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) t[i] += v[k][i];
-        k0 += kAhead;
-        if (k0 >= splits) break;
-        ranges(k0);
-    }
+    add();
     const float scale = scales[s];
     // scale * t, rounded in two halves
 #pragma unroll
