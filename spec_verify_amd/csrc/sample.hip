@@ -87,6 +87,9 @@ __device__ __forceinline__ double value_of(uint32_t bits) { return (double)bits_
 // Raw bin index <-> place in descending order (an involution).
 __device__ __forceinline__ uint32_t bin_order(uint32_t bin) { return bin < kBinsHalf ? kBinsHalf - 1 - bin : bin; }
 
+// The pattern of a bf16 value.
+__device__ __forceinline__ uint32_t max_bits(double v) { return f32_bits((float)v) >> 16; }
+
 struct Weight {
     double max, inv_t;
     __device__ __forceinline__ double exponent(uint32_t bits) const {
@@ -146,26 +149,31 @@ __device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
     atomicAdd(&h.low_n, n);
 }
 
-// Counts vectors [vb, ve) of a row into `table` (h.bin, or a table with the same words
-// behind it), adding `inc` a token. Two elements at a time: subtracting kMagLo from both
-// halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14 say that
-// the magnitude has a bin: ten vector instructions and two LDS additions for two elements,
-// without a branch (pairs that are not plain are counted in a word of the lane's own,
-// which nobody reads). A vector with such a pair is read again by a loop of its own, but
-// for pairs of -inf, which can be most of a row. Zeros and mask values are counted in
-// registers.
-__device__ __forceinline__ void hist_count(Hist &h, uint32_t *table, uint32_t inc, const Row &r, int vb, int ve, bool head,
-                                           bool tail) {
+// Counts vectors [vb, ve) of a row into h.bin, or (quarters) a whole row's four quarters
+// apart, 16 bits each, in h.bin and `bin2`. Two elements at a time: subtracting kMagLo
+// from both halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14
+// say that the magnitude has a bin: ten vector instructions and two LDS additions for two
+// elements, without a branch (pairs that are not plain are counted in a word of the lane's
+// own, which nobody reads). A vector with such a pair is read again by a loop of its own,
+// but for pairs of -inf, which can be most of a row. Zeros and mask values are counted in
+// registers. A step's four loads (of the four quarters, in that case) are issued a step
+// ahead.
+template <bool quarters>
+__device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r, int vb, int ve, bool head, bool tail) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     static_assert(offsetof(Hist, none) == kBins * 4 && offsetof(Hist, bin) == 0, "the lanes' own words follow the bins");
     constexpr uint32_t kNoBin = 0x70007000u, kPairOfInf = 0xFF80FF80u;
+    constexpr int kUnroll = 4, kStep = quarters ? kThreads : kUnroll * kThreads;
+    const int apart = quarters ? (ve - vb + 3) / 4 : kThreads;  // from one of a step's vectors to the next
+    const int end = quarters ? vb + apart : ve;                 // of the first one
     uint32_t zeros = 0, low_n = 0, low_bits = 0;
-    char *base = (char *)table;
     const uint32_t none = (0x8000u + 4 * (threadIdx.x & 63)) * 0x10001u;
-    auto single = [&](uint32_t b) {
+    auto table = [&](int i) { return quarters && (i & 2) ? bin2 : h.bin; };
+    auto unit = [](int i) { return quarters && (i & 1) ? 0x10000u : 1u; };
+    auto single = [&](uint32_t b, int i) {
         const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
         if (q < kBinsHalf) {
-            atomicAdd(&table[(b >> 15) * kBinsHalf + q], inc);
+            atomicAdd(&table(i)[(b >> 15) * kBinsHalf + q], unit(i));
         } else if (mag == 0) {
             ++zeros;
         } else if (mag < kMagLo) {
@@ -184,44 +192,54 @@ __device__ __forceinline__ void hist_count(Hist &h, uint32_t *table, uint32_t in
         return __builtin_bit_cast(u16x2, w) - lo;
     };
     // counts the pair if both have bins; the bits that say it has not
-    auto pair = [&](uint32_t w) -> uint32_t {
+    auto pair = [&](uint32_t w, int i) -> uint32_t {
         const u16x2 t = plain(w);
         const uint32_t tt = __builtin_bit_cast(uint32_t, t), bad = tt & kNoBin;
         uint32_t a = __builtin_bit_cast(uint32_t, (u16x2)(t << 2)) | ((tt >> 1) & 0x40004000u);
         a = bad ? none : a;
-        atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), inc);
-        atomicAdd((uint32_t *)(base + (a >> 16)), inc);
+        char *base = (char *)table(i);
+        atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), unit(i));
+        atomicAdd((uint32_t *)(base + (a >> 16)), unit(i));
         return bad;
     };
     auto odd_word = [&](uint32_t w) { return (__builtin_bit_cast(uint32_t, plain(w)) & kNoBin) != 0 && w != kPairOfInf; };
-    auto rest = [&](int v) {
+    auto rest = [&](int v, int i) {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = *(const uint32_t *)(r.p + r.head + (int64_t)v * 8 + 2 * i);
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = *(const uint32_t *)(r.p + r.head + (int64_t)v * 8 + 2 * j);
             if (odd_word(w)) {
-                single(w & 0xFFFFu);
-                single(w >> 16);
+                single(w & 0xFFFFu, i);
+                single(w >> 16, i);
             }
         }
     };
-    constexpr int kUnroll = 4;
-    for (int v0 = vb; v0 < ve; v0 += kUnroll * kThreads) {
-        const int v = v0 + (int)threadIdx.x;
-        uint4 q[kUnroll];
-        uint32_t todo = 0;
+    auto load = [&](uint4 (&q)[kUnroll], int v) {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            q[i] = v + i * kThreads < ve ? row_vec(r, v + i * kThreads)
-                                         : make_uint4(kPairOfInf, kPairOfInf, kPairOfInf, kPairOfInf);
+            q[i] = v < end && v + i * apart < ve ? row_vec(r, v + i * apart)
+                                                 : make_uint4(kPairOfInf, kPairOfInf, kPairOfInf, kPairOfInf);
+    };
+    uint4 next[kUnroll];
+    int v = vb + (int)threadIdx.x;
+    if (vb < end) load(next, v);
+    for (int v0 = vb; v0 < end; v0 += kStep, v += kStep) {
+        uint4 q[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) q[i] = next[i];
+        if (v0 + kStep < end) load(next, v + kStep);
+        uint32_t todo = 0;
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t bad = pair(q[i].x) | pair(q[i].y) | pair(q[i].z) | pair(q[i].w);
+            const uint32_t bad = pair(q[i].x, i) | pair(q[i].y, i) | pair(q[i].z, i) | pair(q[i].w, i);
             if (bad && (odd_word(q[i].x) || odd_word(q[i].y) || odd_word(q[i].z) || odd_word(q[i].w))) todo |= 1u << i;
         }
-        for (; todo; todo &= todo - 1) rest(v + (__builtin_ctz(todo)) * kThreads);
+        for (; todo; todo &= todo - 1) {
+            const int i = __builtin_ctz(todo);
+            rest(v + i * apart, i);
+        }
     }
     const int at = row_end(r, threadIdx.x, head, tail);
-    if (at >= 0) single(r.p[at]);
+    if (at >= 0) single(r.p[at], at < r.head ? 0 : 3);
     if (zeros) atomicAdd(&h.zeros, zeros);
     if (low_n) hist_low(h, low_bits, low_n);
 }
@@ -274,6 +292,7 @@ struct Found {
 struct Draw {
     Hist h;
     uint32_t item_bits[kSideMax + 1], item_count[kSideMax + 1];  // side items in order
+    double ratio[32], anchor[64], inv_t;  // of binades
     double item_weight[kSideMax + 1], low_weight;
     double wsum[kWaves], whead[kWaves], win_mass[kWindows + 1], win_first[kWindows];
     uint32_t csum[kWaves], win_count[kWindows + 1];
@@ -301,26 +320,37 @@ enum Seek { kMass, kTopP, kMinP, kDraw };
 // and a table behind it; or window by window from the row itself.
 enum Way { kWhole, kQuarters, kLong };
 
-// A thread's bins in a counted row, descending: patterns bits0, bits0 + dir, ..., each
-// weight `ratio` times the one before.
+// A thread's bins in order, descending: patterns bits0, bits0 + dir, ..., each weight
+// `ratio` times the one before.
 struct Own {
     uint32_t bits0;
     int dir;
     double ratio;
-    __device__ __forceinline__ void geometry(const Weight &wt) {
-        ratio = exp((value_of(bits0 + dir) - value_of(bits0)) * wt.inv_t);
-    }
 };
-__device__ __forceinline__ Own own_bins(const Weight &wt) {
-    const int t = threadIdx.x;
-    Own o;
-    o.dir = t <= kLastPositive ? -1 : 1;
-    o.bits0 = t <= kLastPositive ? kMagLo + kBinsHalf - 1 - kOwn * t : 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
-    o.geometry(wt);
-    return o;
+
+__device__ __forceinline__ double inverse_t(const RowParams &par) { return uniform(1.0 / (double)par.temperature); }
+
+// Exponentials of a counted row. fp64 is slow in all sixteen waves at once (an exponential
+// in each took 1.6 us), so one wave takes them for all: a binade's patterns are 2^(e-7)
+// apart, whatever the sign, so its ratio is one of 32; and a binade's largest value (or
+// the row's, if that is in it) is its anchor, from which its weights are powers of the
+// ratio. `draw_ratios` needs the temperature alone and runs beside the counting.
+__device__ __forceinline__ void draw_ratios(Draw &sh, const RowParams &par) {
+    if (wave_id() != 0) return;
+    const int lane = threadIdx.x & 63;
+    const double inv_t = inverse_t(par);
+    // lane e: patterns kMagLo + 128 e ...: the step of that binade
+    const uint32_t bits = kMagLo + 128 * (lane & 31);
+    const double r = exp((value_of(bits) - value_of(bits + 1)) * inv_t);
+    if (lane < 32) sh.ratio[lane] = r;
+    if (lane == 0) sh.inv_t = inv_t;
 }
-__device__ __forceinline__ Weight weight_of(const RowParams &par) {
-    return Weight{0.0, uniform(1.0 / (double)par.temperature)};
+__device__ __forceinline__ void draw_anchors(Draw &sh, const Weight &wt) {
+    if (wave_id() != 0) return;
+    // lanes 0..31: positive binades, whose largest pattern is the last; 32..63: negative ones
+    const int lane = threadIdx.x & 63;
+    const uint32_t bits = lane < 32 ? kMagLo + 128 * lane + 127 : 0x8000u | (kMagLo + 128 * (lane - 32));
+    sh.anchor[lane] = exp((fmin(value_of(bits), wt.max) - wt.max) * wt.inv_t);
 }
 
 // Set by one thread per word before the barrier that precedes draw_way.
@@ -331,17 +361,23 @@ __device__ __forceinline__ void draw_clear(Draw &sh) {
     if (t == 6) sh.win_mass[0] = 0.0;
 }
 
-// Draws a token's value and its ordinal. Used by whole workgroups. max_key: the key of the
-// row's largest value where it is known (0: not).
+// Draws a token's value and its ordinal. Used by whole workgroups, behind draw_clear and
+// (counted rows) draw_ratios. max_key: the key of the row's largest value where it is known
+// and its draw_anchors done (0: not).
 template <Way way>
-__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par, Weight wt, Own own,
-                                          uint32_t max_key) {
+__device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowParams &par, uint32_t max_key) {
     Hist &h = sh.h;
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
     constexpr bool longway = way == kLong;
     constexpr int windows = longway ? kWindows : 1;
     Drawn out{0, 0, -__builtin_inff(), false, !longway};
-    if (max_key) wt.max = value_of(bits_of(max_key));
+    Weight wt;
+    wt.max = max_key ? value_of(bits_of(max_key)) : 0.0;
+    wt.inv_t = longway ? inverse_t(par) : uniform(sh.inv_t);
+    Own own;
+    own.dir = t <= kLastPositive ? -1 : 1;
+    own.bits0 = t <= kLastPositive ? kMagLo + kBinsHalf - 1 - kOwn * t : 0x8000u | (kMagLo + kOwn * (t - kLastPositive - 1));
+    own.ratio = 0.0;
 
     // Side items in order, by the wave that owns them: a value's place is the number of
     // larger entries and its first entry stands there for all equal ones (the places of the
@@ -414,7 +450,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             const uint32_t key0 = 65535u - (uint32_t)win * kBins - kOwn * t;
             own.dir = key0 & 0x8000u ? -1 : 1;
             own.bits0 = bits_of(key0);
-            own.geometry(wt);
+            own.ratio = exp((value_of(own.bits0 + own.dir) - value_of(own.bits0)) * wt.inv_t);
         }
         uint32_t cnt[kOwn];
 #pragma unroll
@@ -436,10 +472,31 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             __syncthreads();
             const uint32_t first = uniform(sh.first);
             if (first != ~0u) wt.max = uniform(value_of(bits_of(65535u - first)));
+            if (!longway) {
+                draw_anchors(sh, wt);
+                __syncthreads();
+            }
         }
         w = 0.0;
         if (f < kOwn) {
-            wf = head = wt(own.bits0 + own.dir * f);
+            const uint32_t bits = own.bits0 + own.dir * f;
+            if (longway) {
+                wf = wt(bits);
+            } else {
+                // steps down from the anchor: the binade's largest value, or the row's
+                const uint32_t binade = ((bits & 0x7FFFu) - kMagLo) >> 7, sign = bits >> 15;
+                const double largest = value_of(sign ? bits & 0xFF80u : bits | 0x7Fu);
+                const uint32_t top = largest <= wt.max ? (sign ? bits & 0xFF80u : bits | 0x7Fu) : max_bits(wt.max);
+                const uint32_t steps = sign ? bits - top : top - bits;
+                double p = own.ratio = sh.ratio[binade];
+                wf = sh.anchor[32 * sign + binade];
+#pragma unroll
+                for (int b = 0; b < 7; ++b) {
+                    if (steps >> b & 1) wf *= p;
+                    p *= p;
+                }
+            }
+            head = wf;
             double x = wf;
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
@@ -631,8 +688,9 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     return out;
 }
 
-__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par, const Weight &wt) {
-    return draw_way<kLong>(sh, row, par, wt, Own{}, 0);
+// Out of line: the kernels hardly ever call it.
+__device__ __attribute__((noinline)) Drawn draw_long(Draw &sh, const Row &row, const RowParams &par) {
+    return draw_way<kLong>(sh, row, par, 0);
 }
 
 // Index of the ordinal-th element equal to `bits` among vectors [vb, ve) (and head or
@@ -737,17 +795,21 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
 
 // ---- kernels ------------------------------------------------------------------------------
 
-// One workgroup per row: count, draw, find. Two workgroups share a compute unit (64
-// registers), so one's draw runs beside the other's reading. The row's quarters are
-// counted apart, which tells where to look for the occurrence: reading half a row again,
-// as a search from its beginning does on average, took a third of the time. Rows that
-// need the long way are marked and left to a launch of their own, whose workgroups
-// otherwise end at once.
-constexpr int kLongWay = -2;
+// One workgroup per row: count, draw, find. The row's quarters are counted apart, which
+// tells where to look for the occurrence: reading half a row again, as a search from its
+// beginning does on average, took a third of the time.
+//
+// With more rows than compute units two workgroups share one (64 registers), so that one's
+// draw runs beside the other's reading. A call of the long way, never taken, would cost
+// them its stack and spilled registers (M = 1024, V = 248320: 134 us instead of 115), so
+// rows that need it are marked and left to a launch of their own, whose workgroups
+// otherwise end at once (3 us). With fewer rows the call is the cheaper one (M = 1: 13 us
+// instead of 15).
 constexpr int64_t kMaxQuarter = 65535 / 8 - 2;  // vectors: a quarter's tokens fit 16 bits
+constexpr int kLongWay = -2;
 
-template <Way way>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))) void sample_row_kernel(
+template <Way way, bool mark>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(mark ? 8 : 4, 8))) void sample_row_kernel(
     const uint16_t *__restrict__ logits, int64_t ld, Params par, int32_t *__restrict__ tokens,
     float *__restrict__ logprobs, int V) {
     __shared__ __attribute__((aligned(16))) std::conditional_t<way == kQuarters, DrawQuarters, Draw> sh;
@@ -760,29 +822,26 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
     if constexpr (way == kQuarters) {
         for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)sh.bin2)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q)
-            hist_count(sh.h, q & 2 ? sh.bin2 : sh.h.bin, q & 1 ? 0x10000u : 1u, row, min(q * quarter, row.nvec),
-                       min((q + 1) * quarter, row.nvec), q == 0, q == 3);
+        hist_count<true>(sh.h, sh.bin2, row, 0, row.nvec, true, true);
     } else {
         __syncthreads();
-        hist_count(sh.h, sh.h.bin, 1, row, 0, row.nvec, true, true);
+        hist_count<false>(sh.h, nullptr, row, 0, row.nvec, true, true);
     }
-    const Weight wt = weight_of(rp);
-    const Own own = own_bins(wt);
+    draw_ratios(sh, rp);
     __syncthreads();
-    if (sh.h.odd || sh.h.side_n > kSideMax) {
+    const bool longway = sh.h.odd || sh.h.side_n > kSideMax;
+    if (mark && longway) {
         if (threadIdx.x == 0) tokens[m] = kLongWay;
         return;
     }
-    const Drawn d = draw_way<way>(sh, row, rp, wt, own, 0);
+    const Drawn d = !mark && longway ? draw_long(sh, row, rp) : draw_way<way>(sh, row, rp, 0);
     int token = -1;
     if (d.any) {
         const uint32_t mag = (d.bits & 0x7FFFu) - kMagLo;
         int vb = 0, ve = row.nvec, q = -1;
         uint32_t left = d.ordinal;
         if constexpr (way == kQuarters)
-            if (mag < kBinsHalf) {
+            if (d.counted && mag < kBinsHalf) {
                 const uint32_t bin = (d.bits >> 15) * kBinsHalf + mag, u = sh.h.bin[bin], v = sh.bin2[bin];
                 for (q = 0; q < 3; ++q) {
                     const uint32_t x = q & 2 ? v : u, n = q & 1 ? x >> 16 : x & 0xFFFFu;
@@ -800,6 +859,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8, 8))
     }
 }
 
+// The rows that sample_row_kernel marked.
 __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *__restrict__ logits, int64_t ld, Params par,
                                                                int32_t *__restrict__ tokens, float *__restrict__ logprobs,
                                                                int64_t M, int V) {
@@ -808,11 +868,11 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
         const bool mine = tokens[m] == kLongWay;
         __syncthreads();  // every thread has read the mark, and the row before is done with
         if (!mine) continue;
-        draw_clear(sh);
-        __syncthreads();
         const Row row = make_row(logits + m * ld, V);
         const RowParams rp = row_params(par, m);
-        const Drawn d = draw_way<kLong>(sh, row, rp, weight_of(rp), Own{}, 0);
+        draw_clear(sh);
+        __syncthreads();
+        const Drawn d = draw_way<kLong>(sh, row, rp, 0);
         int token = -1;
         if (d.any) token = locate(sh, row, 0, row.nvec, true, true, d.bits, d.ordinal);
         if (threadIdx.x == 0) {
@@ -843,7 +903,7 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     if (threadIdx.x == 0) entries = largest = 0;
     __syncthreads();
     const int vb = min(part * vpp, row.nvec), ve = min(vb + vpp, row.nvec);
-    hist_count(h, h.bin, 1, row, vb, ve, part == 0, part == C - 1);
+    hist_count<false>(h, nullptr, row, vb, ve, part == 0, part == C - 1);
     __syncthreads();
     // occurring bins in descending order, but none behind which top_k tokens of this
     // part already stand; (bins << 18 | tokens) are scanned in one word
@@ -935,8 +995,6 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     const int first = C < kWaves ? wave % C : wave, sub = C < kWaves ? wave / C : 0;
     const uint32_t lane0 = sub * 64 + lane, step = shared * 64;
     uint32_t kept[kTwo][kAhead], entries[kTwo] = {0, 0};
-    Weight wt;
-    Own own;
     uint32_t largest = 0;
     for (int c = lane; c < C; c += 64) largest = max(largest, src[(int64_t)c * kPartWords + 6]);
     for (int c0 = 0; c0 < C; c0 += kTwo * kWaves) {
@@ -951,8 +1009,11 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
             for (int i = 0; i < kAhead; ++i) kept[j][i] = p[kHeader + min(step * i + lane0, kBins - 1)];
         }
         if (c0 == 0) {  // beside the loads
-            wt = weight_of(rp);
-            own = own_bins(wt);
+            draw_ratios(sh, rp);
+#pragma unroll
+            for (int x = 1; x < 64; x <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, x));
+            largest = uniform(largest);
+            if (largest) draw_anchors(sh, Weight{value_of(bits_of(largest)), uniform(sh.inv_t)});
         }
 #pragma unroll
         for (int j = 0; j < kTwo; ++j) {
@@ -980,11 +1041,8 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     }
     for (int c = t; c < C; c += kThreads) in_part[c] = 0;
     draw_clear(sh);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, x));
     __syncthreads();
-    const Drawn d = h.odd || h.side_n > kSideMax ? draw_long(sh, row, rp, wt)
-                                                 : draw_way<kWhole>(sh, row, rp, wt, own, uniform(largest));
+    const Drawn d = h.odd || h.side_n > kSideMax ? draw_long(sh, row, rp) : draw_way<kWhole>(sh, row, rp, largest);
     int token = -1;
     if (d.any) {
         const uint32_t q = (d.bits & 0x7FFFu) - kMagLo;
@@ -1093,6 +1151,7 @@ SamplePlan plan_sample(int64_t M, int64_t V, int num_cus) {
     C = C < 4 ? 1 : std::min<int64_t>(C, 8);
     if (C > 1) C = std::max<int64_t>(C, (nvec + kMaxPartVectors - 1) / kMaxPartVectors);
     p.parts = (int)std::max<int64_t>(C, 1);
+    p.mark = M > num_cus;
     p.vectors_per_part = (int)((nvec + p.parts - 1) / p.parts);
     if (p.parts > 1) p.workspace_bytes = kCounterBytes + (size_t)M * p.parts * kPartWords * 4;
     return p;
@@ -1104,12 +1163,18 @@ hipError_t launch_sample(const SamplePlan &p, const void *logits, int64_t ld, co
     const Params par{u, temperature, top_p, min_p, top_k};
     const uint16_t *l = (const uint16_t *)logits;
     if (p.parts == 1) {
-        if (V / 8 + 1 <= 4 * kMaxQuarter)
-            hipLaunchKernelGGL(sample_row_kernel<kQuarters>, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,
-                               tokens, logprobs, (int)V);
-        else
-            hipLaunchKernelGGL(sample_row_kernel<kWhole>, dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,
-                               tokens, logprobs, (int)V);
+        const bool quarters = V / 8 + 1 <= 4 * kMaxQuarter;
+#define SVQ_ROW(WAY, MARK)                                                                                          \
+    hipLaunchKernelGGL((sample_row_kernel<WAY, MARK>), dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,    \
+                       tokens, logprobs, (int)V)
+        if (!p.mark) {
+            if (quarters) SVQ_ROW(kQuarters, false);
+            else SVQ_ROW(kWhole, false);
+            return hipGetLastError();
+        }
+        if (quarters) SVQ_ROW(kQuarters, true);
+        else SVQ_ROW(kWhole, true);
+#undef SVQ_ROW
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)std::min<int64_t>(M, 256)), dim3(kThreads), 0, stream, l, ld,

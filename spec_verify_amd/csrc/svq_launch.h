@@ -166,6 +166,7 @@ hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld
 // values and a second launch draws from their lists in the workspace.
 struct SamplePlan {
     int parts, vectors_per_part;
+    bool mark;  // one workgroup per row: rare rows are left to a second launch
     size_t workspace_bytes;
 };
 SamplePlan plan_sample(int64_t M, int64_t V, int num_cus);
