@@ -419,9 +419,31 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
         uint32_t n = h.bin[at];
         if constexpr (way == kQuarters) {
             const uint32_t n2 = second_table(sh)[at];
-            n = (n & 0xFFFFu) + (n >> 16) + (n2 & 0xFFFFu) + (n2 >> 16);
+            n = __builtin_amdgcn_sad_u16(n, 0, __builtin_amdgcn_sad_u16(n2, 0, 0));  // the four halves
         }
         return n;
+    };
+
+    // The thread's bins, in 16-byte reads (single words, eight apart from lane to lane, meet
+    // in the banks: 1 us more).
+    auto counts = [&](uint32_t (&n)[kOwn]) {
+        static_assert(kOwn == 8, "two vectors");
+        const bool flip = !longway && wave <= kSideWave;  // the positive bins stand ascending
+        const int first = flip ? (int)kBinsHalf - kOwn * (t + 1) : kOwn * t;
+        const uint4 *p = (const uint4 *)&h.bin[first];
+        uint4 a = p[0], b = p[1];
+        if constexpr (way == kQuarters) {
+            const uint4 *p2 = (const uint4 *)&second_table(sh)[first];
+            const uint4 a2 = p2[0], b2 = p2[1];
+            auto sum = [](uint32_t u, uint32_t v) {  // of the four 16-bit halves
+                return __builtin_amdgcn_sad_u16(u, 0, __builtin_amdgcn_sad_u16(v, 0, 0));
+            };
+            a = make_uint4(sum(a.x, a2.x), sum(a.y, a2.y), sum(a.z, a2.z), sum(a.w, a2.w));
+            b = make_uint4(sum(b.x, b2.x), sum(b.y, b2.y), sum(b.z, b2.z), sum(b.w, b2.w));
+        }
+        const uint32_t x[kOwn] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) n[j] = flip ? x[kOwn - 1 - j] : x[j];
     };
 
     auto analyse = [&](int win) {
@@ -453,8 +475,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
             own.ratio = exp((value_of(own.bits0 + own.dir) - value_of(own.bits0)) * wt.inv_t);
         }
         uint32_t cnt[kOwn];
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) cnt[j] = bin_at(t, j);
+        counts(cnt);
         c = 0;
         f = kOwn;
 #pragma unroll
@@ -741,10 +762,7 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
         uint4 q[kIter];
         uint32_t eq[kIter], sum = 0;
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const int v = w0 + i * 64 + lane;
-            q[i] = row_vec(r, min(v, ve - 1));
-        }
+        for (int i = 0; i < kIter; ++i) q[i] = row_vec(r, min(w0 + i * 64 + lane, ve - 1));
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
             eq[i] = w0 + i * 64 + lane < ve ? 8 - misses(q[i]) : 0;
