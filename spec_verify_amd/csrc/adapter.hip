@@ -27,7 +27,7 @@
 // is the bytes of A, B, base and out (or, for a few rows, latency).
 #include <algorithm>
 
-#include "svq_launch.h"
+#include "svq_requests.h"
 
 namespace svq {
 

@@ -27,7 +27,7 @@
 #include <cstddef>
 #include <type_traits>
 
-#include "svq_launch.h"
+#include "svq_requests.h"
 
 namespace svq {
 

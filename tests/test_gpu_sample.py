@@ -300,6 +300,45 @@ def test_long_vocabulary():
     _check(l, np.array([0.99], np.float32), "2^24 chat", T=[0.8], k=[50], p=[0.95])
 
 
+@pytest.mark.parametrize("M", [90, 300])
+def test_rows_longer_than_their_quarters_count(M):
+    """Vocabularies past 4 x 65512 tokens with a workgroup per row: the whole row is one
+    count, with fewer rows than compute units and with more."""
+    import spec_verify_amd as svq
+    _say("sample long rows", M)
+    rng = np.random.default_rng(M)
+    V = 262145 + 8
+    l = torch.randn(M, V, device="cuda", generator=torch.Generator("cuda").manual_seed(M)).mul_(2).bfloat16()
+    l[7] = 0.5                                   # one value: more than 16 bits of it
+    l[9] = _logits(rng, 1, V, "huge")[0]
+    pick = [0, 3, 7, 9, M - 1]
+    u = torch.rand(M, device="cuda")
+    par = _params(rng, M)
+    cast = lambda v, t: torch.tensor(v, dtype=t, device="cuda")
+    got = svq.sample(l, u, cast(par["T"], torch.float32), cast(par["k"], torch.int32), cast(par["p"], torch.float32),
+                     cast(par["mp"], torch.float32))
+    _check(l[pick], u[pick].cpu().numpy(), "long rows", got=(got[0][pick], got[1][pick]),
+           **{k: v[pick] for k, v in par.items()})
+    plain = svq.sample(l, u)
+    _check(l[pick], u[pick].cpu().numpy(), "long rows, plain", got=(plain[0][pick], plain[1][pick]))
+
+
+@pytest.mark.parametrize("M", [1, 30, 300])
+def test_heavy_values(M):
+    """A whole vocabulary of one value, and of one value but for a few tokens: counts past
+    16 bits, in every kernel."""
+    _say("sample heavy values", M)
+    rng = np.random.default_rng(M + 3)
+    rows = min(M, 6)
+    for value in (1.25, 0.0, -3e38, 1e-20, -10000.0):
+        l = torch.full((M, VOCAB), value, dtype=torch.bfloat16, device="cuda")
+        l[:, 100000:100003] = torch.tensor([value + 1, value, 0.25], dtype=torch.bfloat16, device="cuda")
+        import spec_verify_amd as svq
+        u = torch.rand(M, device="cuda")
+        got = svq.sample(l, u)
+        _check(l[:rows], u[:rows].cpu().numpy(), ("heavy", value), got=(got[0][:rows], got[1][:rows]))
+
+
 def test_graph_replays_and_streams():
     import spec_verify_amd as svq
     _say("sample graph")

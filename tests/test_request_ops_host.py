@@ -33,6 +33,7 @@ def _adapter(L, base=P[0], ldb=256, x=P[1], a=P[2], b=P[3], rows=P[4], scales=P[
     (1, dict(scales=None)), (1, dict(out=None)),
     (2, dict(M=0)), (2, dict(N=-16)), (2, dict(K=0)), (2, dict(R=0)), (2, dict(R=264)), (2, dict(slots=0)),
     (2, dict(ldb=240)), (2, dict(ldo=255)), (2, dict(M=1 << 20, K=1 << 11)), (2, dict(M=1 << 23, N=256)),
+    (2, dict(slots=(1 << 31) - 1, R=256, K=1 << 20)),
     (4, dict(N=250)), (4, dict(K=320)), (4, dict(R=12)), (4, dict(ldb=260)), (4, dict(ldo=257)),
     (6, dict(base=P[0] + 8)), (6, dict(x=P[1] + 8)), (6, dict(a=P[2] + 2)), (6, dict(b=P[3] + 4)),
     (6, dict(rows=P[4] + 2)), (6, dict(scales=P[5] + 1)), (6, dict(out=P[6] + 8)),
