@@ -1178,8 +1178,8 @@ SamplePlan plan_sample(int64_t M, int64_t V, int num_cus) {
     SamplePlan p{};
     const int64_t nvec = V / 8 + 1;
     // parts of a row: enough workgroups to fill the chip, at least one vector a thread, no
-    // more than 8 (M = 1: 23 us with 8, 25 with 16, 31 with 31: the lists grow), and one
-    // where there would be fewer than 4 (M = 100: 43 us with 3, 34 with one)
+    // more than 8 (M = 1, nothing filtered: 29 us with 8, 32 with 16, 39 with 31: the lists
+    // grow), and one where there would be fewer than 4 (M = 100: 43 us with 3, 34 with one)
     int64_t C = std::min<int64_t>((num_cus + M - 1) / M, (nvec + kThreads - 1) / kThreads);
     C = C < 4 ? 1 : std::min<int64_t>(C, 8);
     if (C > 1) C = std::max<int64_t>(C, (nvec + kMaxPartVectors - 1) / kMaxPartVectors);
