@@ -43,7 +43,9 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr uint32_t kBinsHalf = 4096;         // 32 exponents x 128 mantissas of one sign
-constexpr uint32_t kBins = 2 * kBinsHalf;    // of raw index sign << 12 | (magnitude - kMagLo)
+constexpr uint32_t kBins = 2 * kBinsHalf;    // of index sign << 12 | (magnitude - kMagLo)
+constexpr uint32_t kSignWords = kBinsHalf + 64;  // of a table in LDS: a sign's bins, and a word for each lane's other tokens
+constexpr uint32_t kTable = 2 * kSignWords;
 constexpr int kOwn = kBins / kThreads;       // bins of a thread
 constexpr uint32_t kMagLo = 111u << 7;       // pattern of 2^-16
 constexpr uint32_t kSideMax = 55;            // smaller magnitudes; with zero and a thread's bins they are one per lane
@@ -91,7 +93,9 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t key) { return (key & 0x8000
 // NaN and -inf are never drawn: finite values and +inf have keys in [0x80, 0xFF80].
 __device__ __forceinline__ bool key_valid(uint32_t key) { return key - 0x80u <= 0xFF00u; }
 __device__ __forceinline__ double value_of(uint32_t bits) { return (double)bits_f32(bits << 16); }
-// Raw bin index <-> place in descending order (an involution).
+// Where a bin stands in a table.
+__device__ __forceinline__ uint32_t bin_word(uint32_t bin) { return bin + (bin < kBinsHalf ? 0 : kSignWords - kBinsHalf); }
+// Bin index <-> place in descending order (an involution).
 __device__ __forceinline__ uint32_t bin_order(uint32_t bin) { return bin < kBinsHalf ? kBinsHalf - 1 - bin : bin; }
 
 // The pattern of a bf16 value.
@@ -137,15 +141,14 @@ __device__ __forceinline__ RowParams row_params(const Params &p, int64_t m) {
 // ---- histogram of a row or of a part of it -------------------------------------------
 
 struct Hist {
-    uint32_t bin[kBins];
-    uint32_t none[64];            // where a lane's pair goes that is not counted here
+    uint32_t bin[kTable];
     uint32_t side[kSideMax];
     uint32_t side_n, zeros, odd;  // odd: the row needs the long way
     uint32_t low_n, low_bits;     // tokens of the one pattern at or below -2^16
 };
 
 __device__ __forceinline__ void hist_clear(Hist &h) {
-    for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < (int)kTable / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) h.side_n = h.zeros = h.odd = h.low_n = h.low_bits = 0;
 }
 
@@ -157,30 +160,31 @@ __device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
 }
 
 // Counts vectors [vb, ve) of a row into h.bin, or (quarters) a whole row's four quarters
-// apart, 16 bits each, in h.bin and `bin2`. Two elements at a time: subtracting kMagLo
-// from both halves leaves the raw bin index with the sign in bit 15, and clear bits 12..14
-// say that the magnitude has a bin: ten vector instructions and two LDS additions for two
-// elements, without a branch (pairs that are not plain are counted in a word of the lane's
-// own, which nobody reads). A vector with such a pair is read again by a loop of its own,
-// but for pairs of -inf, which can be most of a row. Zeros and mask values are counted in
-// registers. A step's four loads (of the four quarters, in that case) are issued a step
-// ahead.
+// apart, 16 bits each, in h.bin and `bin2`. Two elements at a time, without a branch:
+// subtracting kMagLo from both magnitudes leaves the bins' places, and a minimum sends every
+// other token (-inf, NaN and what follows) to a word of the lane's own behind the bins, which
+// nobody reads: nine vector instructions and two LDS additions for two elements. A vector
+// with such tokens is looked at once more. Zeros and the thread's mask value, which like
+// -inf can be most of a row, are counted there in registers; a vector with anything else is
+// read again by a loop of its own, which keeps the code of the common case short. A step's
+// four loads (of the four quarters, in that case) are issued a step ahead.
 template <bool quarters>
 __device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r, int vb, int ve, bool head, bool tail) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    static_assert(offsetof(Hist, none) == kBins * 4 && offsetof(Hist, bin) == 0, "the lanes' own words follow the bins");
     constexpr uint32_t kNoBin = 0x70007000u, kPairOfInf = 0xFF80FF80u;
     constexpr int kUnroll = 4, kStep = quarters ? kThreads : kUnroll * kThreads;
     const int apart = quarters ? (ve - vb + 3) / 4 : kThreads;  // from one of a step's vectors to the next
     const int end = quarters ? vb + apart : ve;                 // of the first one
     uint32_t zeros = 0, low_n = 0, low_bits = 0;
-    const uint32_t none = (0x8000u + 4 * (threadIdx.x & 63)) * 0x10001u;
+    const uint16_t own = (uint16_t)(kBinsHalf + (threadIdx.x & 63));
+    const u16x2 other = {own, own};
     auto table = [&](int i) { return quarters && (i & 2) ? bin2 : h.bin; };
     auto unit = [](int i) { return quarters && (i & 1) ? 0x10000u : 1u; };
-    auto single = [&](uint32_t b, int i) {
+    // a token that is no pair's: of the row's ends (any), or without a bin (`odd`)
+    auto single = [&](uint32_t b, int i, bool odd) {
         const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
         if (q < kBinsHalf) {
-            atomicAdd(&table(i)[(b >> 15) * kBinsHalf + q], unit(i));
+            if (!odd) atomicAdd(&table(i)[(b >> 15) * kSignWords + q], unit(i));
         } else if (mag == 0) {
             ++zeros;
         } else if (mag < kMagLo) {
@@ -194,30 +198,37 @@ __device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r
             h.odd = 1;
         }
     };
-    auto plain = [](uint32_t w) {
-        const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo};
-        return __builtin_bit_cast(u16x2, w) - lo;
-    };
-    // counts the pair if both have bins; the bits that say it has not
+    // counts a pair; the bits that say that one of it has no bin
     auto pair = [&](uint32_t w, int i) -> uint32_t {
-        const u16x2 t = plain(w);
-        const uint32_t tt = __builtin_bit_cast(uint32_t, t), bad = tt & kNoBin;
-        uint32_t a = __builtin_bit_cast(uint32_t, (u16x2)(t << 2)) | ((tt >> 1) & 0x40004000u);
-        a = bad ? none : a;
+        const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo}, magnitude = {0x7FFF, 0x7FFF};
+        const u16x2 t = __builtin_bit_cast(u16x2, w) - lo;
+        const u16x2 a = (t >> 15) * (uint16_t)(4 * kSignWords) + (__builtin_elementwise_min(t & magnitude, other) << 2);
+        const uint32_t at = __builtin_bit_cast(uint32_t, a);
         char *base = (char *)table(i);
-        atomicAdd((uint32_t *)(base + (a & 0xFFFFu)), unit(i));
-        atomicAdd((uint32_t *)(base + (a >> 16)), unit(i));
-        return bad;
+        atomicAdd((uint32_t *)(base + (at & 0xFFFFu)), unit(i));
+        atomicAdd((uint32_t *)(base + (at >> 16)), unit(i));
+        return __builtin_bit_cast(uint32_t, t) & kNoBin;
     };
-    auto odd_word = [&](uint32_t w) { return (__builtin_bit_cast(uint32_t, plain(w)) & kNoBin) != 0 && w != kPairOfInf; };
-    auto rest = [&](int v, int i) {
+    // of a pair with tokens without a bin: counts zeros and mask values; whether others are left
+    auto look = [&](uint32_t w) -> bool {
+        bool left = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t b = half ? w >> 16 : w & 0xFFFFu, mag = b & 0x7FFFu;
+            const bool zero = mag == 0, low = b == low_bits && low_n != 0;
+            zeros += zero;
+            low_n += low;
+            // neither a bin nor -inf or NaN (patterns above 0x7F80 of either sign, and -inf)
+            left |= mag - kMagLo >= kBinsHalf && !zero && !low && mag <= 0x7F80u && b != 0xFF80u;
+        }
+        return left;
+    };
+    // the vector's tokens that `look` left over (zeros and the known mask value are counted)
+    auto rest = [&](int v, int i, uint32_t known_low) {
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t w = *(const uint32_t *)(r.p + r.head + (int64_t)v * 8 + 2 * j);
-            if (odd_word(w)) {
-                single(w & 0xFFFFu, i);
-                single(w >> 16, i);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = r.p[r.head + (int64_t)v * 8 + j];
+            if ((b & 0x7FFFu) != 0 && b != known_low) single(b, i, true);
         }
     };
     auto load = [&](uint4 (&q)[kUnroll], int v) {
@@ -235,18 +246,24 @@ __device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r
         for (int i = 0; i < kUnroll; ++i) q[i] = next[i];
         if (v0 + kStep < end) load(next, v + kStep);
         uint32_t todo = 0;
+        const uint32_t known_low = low_n ? low_bits : 0;  // as the looks below know it
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const uint32_t bad = pair(q[i].x, i) | pair(q[i].y, i) | pair(q[i].z, i) | pair(q[i].w, i);
-            if (bad && (odd_word(q[i].x) || odd_word(q[i].y) || odd_word(q[i].z) || odd_word(q[i].w))) todo |= 1u << i;
+            // (a vector of -inf alone, as there are many in a masked row and past a row's end,
+            // needs no look)
+            if (bad && ((q[i].x ^ kPairOfInf) | (q[i].y ^ kPairOfInf) | (q[i].z ^ kPairOfInf) | (q[i].w ^ kPairOfInf))) {
+                const uint32_t left = (uint32_t)look(q[i].x) | (uint32_t)look(q[i].y) | (uint32_t)look(q[i].z) | (uint32_t)look(q[i].w);
+                todo |= left << i;
+            }
         }
         for (; todo; todo &= todo - 1) {
             const int i = __builtin_ctz(todo);
-            rest(v + i * apart, i);
+            rest(v + i * apart, i, known_low);
         }
     }
     const int at = row_end(r, threadIdx.x, head, tail);
-    if (at >= 0) single(r.p[at], at < r.head ? 0 : 3);
+    if (at >= 0) single(r.p[at], at < r.head ? 0 : 3, false);
     if (zeros) atomicAdd(&h.zeros, zeros);
     if (low_n) hist_low(h, low_bits, low_n);
 }
@@ -311,7 +328,7 @@ struct Draw {
 
 // A row's quarters: the second of two tables, where a kernel has one.
 struct DrawQuarters : Draw {
-    uint32_t bin2[kBins + 64];  // the first and second quarter are in bin, the others here
+    uint32_t bin2[kTable];  // the first and second quarter are in bin, the others here
 };
 __device__ __forceinline__ uint32_t *second_table(Draw &sh) { return static_cast<DrawQuarters &>(sh).bin2; }
 
@@ -422,7 +439,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     int current = -1;
 
     auto bin_at = [&](int thread, int j) -> uint32_t {  // a thread's j-th bin
-        const int at = !longway && thread <= kLastPositive ? kBinsHalf - 1 - kOwn * thread - j : kOwn * thread + j;
+        const int at = longway ? kOwn * thread + j : (int)bin_word(bin_order(kOwn * thread + j));
         uint32_t n = h.bin[at];
         if constexpr (way == kQuarters) {
             const uint32_t n2 = second_table(sh)[at];
@@ -436,7 +453,7 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
     auto counts = [&](uint32_t (&n)[kOwn]) {
         static_assert(kOwn == 8, "two vectors");
         const bool flip = !longway && wave <= kSideWave;  // the positive bins stand ascending
-        const int first = flip ? (int)kBinsHalf - kOwn * (t + 1) : kOwn * t;
+        const int first = flip ? (int)kBinsHalf - kOwn * (t + 1) : (longway ? kOwn * t : (int)bin_word(kOwn * t));
         const uint4 *p = (const uint4 *)&h.bin[first];
         uint4 a = p[0], b = p[1];
         if constexpr (way == kQuarters) {
@@ -785,20 +802,18 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
             if (before <= left && left < before + sum) {  // in this wave's part
                 uint32_t skip = left - before;
 #pragma unroll
-                for (int i = 0; i < kIter; ++i)
-                    for (uint64_t mask = __ballot(eq[i] != 0); mask; mask &= mask - 1) {
-                        const int owner = __builtin_ctzll(mask);
-                        const uint32_t n = __builtin_amdgcn_readlane((int)eq[i], owner);
-                        if (skip < n) {
-                            const int v = w0 + i * 64 + owner;
-                            uint32_t in = matches(row_vec(r, v));
-                            for (; skip; --skip) in &= in - 1;
-                            if (lane == 0) sh.at = r.head + v * 8 + __builtin_ctz(in);
-                            skip = ~0u;  // found: no later vector has that many
-                            break;
-                        }
-                        skip -= n;
+                for (int i = 0; i < kIter; ++i) {
+                    const uint32_t inc = wave_scan(eq[i]), n = __builtin_amdgcn_readlane((int)inc, 63);
+                    const uint32_t first = inc - eq[i];
+                    if (first <= skip && skip < inc) {  // in this lane's vector
+                        const int v = w0 + i * 64 + lane;
+                        uint32_t in = matches(row_vec(r, v));
+                        for (uint32_t k = skip - first; k; --k) in &= in - 1;
+                        sh.at = r.head + v * 8 + __builtin_ctz(in);
                     }
+                    if (skip < n) break;
+                    skip -= n;
+                }
             }
             __syncthreads();
             return sh.at;
@@ -846,7 +861,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(mark ?
     hist_clear(sh.h);
     draw_clear(sh);
     if constexpr (way == kQuarters) {
-        for (int i = threadIdx.x; i < (int)kBins / 4; i += kThreads) ((uint4 *)sh.bin2)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < (int)kTable / 4; i += kThreads) ((uint4 *)sh.bin2)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         hist_count<true>(sh.h, sh.bin2, row, 0, row.nvec, true, true);
     } else {
@@ -868,7 +883,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(mark ?
         uint32_t left = d.ordinal;
         if constexpr (way == kQuarters)
             if (d.counted && mag < kBinsHalf) {
-                const uint32_t bin = (d.bits >> 15) * kBinsHalf + mag, u = sh.h.bin[bin], v = sh.bin2[bin];
+                const uint32_t at = (d.bits >> 15) * kSignWords + mag, u = sh.h.bin[at], v = sh.bin2[at];
                 for (q = 0; q < 3; ++q) {
                     const uint32_t x = q & 2 ? v : u, n = q & 1 ? x >> 16 : x & 0xFFFFu;
                     if (left < n) break;
@@ -938,7 +953,7 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(const uint16_t *
     // occurring bins in descending order, but none behind which top_k tokens of this
     // part already stand; (bins << 18 | tokens) are scanned in one word
     const int t = threadIdx.x, lane = t & 63, wave = wave_id();
-    const uint4 v0 = ((const uint4 *)h.bin)[kBinsHalf / 4 - 1 - t], v1 = ((const uint4 *)h.bin)[kBinsHalf / 4 + t];
+    const uint4 v0 = ((const uint4 *)h.bin)[kBinsHalf / 4 - 1 - t], v1 = ((const uint4 *)h.bin)[kSignWords / 4 + t];
     const uint32_t n[2][4] = {{v0.w, v0.z, v0.y, v0.x}, {v1.x, v1.y, v1.z, v1.w}};
     uint32_t own[2], inc[2];
 #pragma unroll
@@ -1016,7 +1031,7 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
     Hist &h = sh.h;
     hist_clear(h);
     __syncthreads();
-    auto add = [&](uint32_t e) { atomicAdd(&h.bin[bin_order(e >> kCountBits)], e & kCountMask); };
+    auto add = [&](uint32_t e) { atomicAdd(&h.bin[bin_word(bin_order(e >> kCountBits))], e & kCountMask); };
     // A wave takes two parts at once (or, of few parts, several waves share one), and keeps
     // the first kAhead entries of a lane for the search below (all there are, as a rule,
     // where top_k limits them).
@@ -1079,15 +1094,20 @@ __global__ __launch_bounds__(kThreads) void sample_select_kernel(const uint16_t 
         int vb = 0, ve = row.nvec;
         bool head = true, tail = true;
         uint32_t left = d.ordinal;
-        if (d.counted && q < kBinsHalf) {
-            // the value's count in each part tells which part holds the occurrence; a
-            // part's entries ascend by place: 64 samples, then the stretch between two.
-            // (Zero, smaller and low values and the long way have no counts by part.)
+        const uint32_t mag = d.bits & 0x7FFFu;
+        const bool binned = q < kBinsHalf, zero = mag == 0, low = d.bits == h.low_bits && h.low_n;
+        if (d.counted && (binned || zero || low)) {
+            // the value's count in each part tells which part holds the occurrence: zero's and
+            // the low value's in its header; a part's entries ascend by place: 64 samples,
+            // then the stretch between two. (Smaller values and the long way have no counts
+            // by part.)
             const uint32_t want = bin_order((d.bits >> 15) * kBinsHalf + q);
             for (int c = first, j = 0; c < C && sub < shared; c += kWaves, ++j) {
                 uint32_t n = 0;
                 const uint32_t count = C <= kTwo * kWaves ? (j ? entries[1] : entries[0]) : ~0u;
-                if (count <= step * kAhead) {
+                if (!binned) {
+                    if (sub == 0 && lane == 0) n = src[(int64_t)c * kPartWords + (zero ? 2 : 4)];
+                } else if (count <= step * kAhead) {
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) {
                         const uint32_t e = j ? kept[1][i] : kept[0][i];
