@@ -24,12 +24,15 @@
 // below -2^16 (a mask value) are items of their own. Any other row is counted the long
 // way: eight windows of 8192 patterns, one scan of the row per window and step.
 //
-// One workgroup takes a row from 86 rows on (and of short rows); of fewer, four to eight
+// One workgroup takes a row from 52 rows on (and of short rows); of fewer, five to eight
 // workgroups count a part of one row each and a second launch draws from their lists.
-// V = 248320, us a call on the GPU alone: M = 1 21, 5 22, 64 28, 128 33, 256 44, 1024 119
-// (508 MB read at 4.3 TB/s; a large copy moves 4.8 TB/s). Few rows are bound by latency
-// (two launches and their dependent steps), many by the counting: two LDS additions and
-// eleven vector instructions per two tokens keep the vector units 75% and LDS 54% busy.
+// V = 248320, us a call on the GPU alone, with top-k and top-p / nothing filtered: M = 1
+// 22 / 28, 5 23 / 29, 64 32 / 31, 128 33 / 31, 256 43 / 42, 1024 117 / 115 (508 MB read at
+// 4.4 TB/s; a large copy moves 4.8 TB/s). Few rows are bound by latency (two launches and
+// their dependent steps), many by the counting: two LDS additions and ten vector
+// instructions per two tokens keep the vector units 74% and LDS 53% busy. Masked rows (95% of
+// -inf, -1e9, -1e4): 43 to 44 at M = 128, 138 to 143 at 1024; rows counted the long way 300 at
+// M = 1, 480 at 128, 1400 at 1024.
 #include <algorithm>
 #include <cstddef>
 #include <type_traits>
@@ -138,136 +141,6 @@ __device__ __forceinline__ RowParams row_params(const Params &p, int64_t m) {
     return r;
 }
 
-// ---- histogram of a row or of a part of it -------------------------------------------
-
-struct Hist {
-    uint32_t bin[kTable];
-    uint32_t side[kSideMax];
-    uint32_t side_n, zeros, odd;  // odd: the row needs the long way
-    uint32_t low_n, low_bits;     // tokens of the one pattern at or below -2^16
-};
-
-__device__ __forceinline__ void hist_clear(Hist &h) {
-    for (int i = threadIdx.x; i < (int)kTable / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) h.side_n = h.zeros = h.odd = h.low_n = h.low_bits = 0;
-}
-
-// A token count for one pattern at or below -2^16; a second such pattern makes the row odd.
-__device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
-    const uint32_t was = atomicCAS(&h.low_bits, 0u, bits);
-    if (was != 0 && was != bits) h.odd = 1;
-    atomicAdd(&h.low_n, n);
-}
-
-// Counts vectors [vb, ve) of a row into h.bin, or (quarters) a whole row's four quarters
-// apart, 16 bits each, in h.bin and `bin2`. Two elements at a time, without a branch:
-// subtracting kMagLo from both magnitudes leaves the bins' places, and a minimum sends every
-// other token (-inf, NaN and what follows) to a word of the lane's own behind the bins, which
-// nobody reads: nine vector instructions and two LDS additions for two elements. A vector
-// with such tokens is looked at once more. Zeros and the thread's mask value, which like
-// -inf can be most of a row, are counted there in registers; a vector with anything else is
-// read again by a loop of its own, which keeps the code of the common case short. A step's
-// four loads (of the four quarters, in that case) are issued a step ahead.
-template <bool quarters>
-__device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r, int vb, int ve, bool head, bool tail) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    constexpr uint32_t kNoBin = 0x70007000u, kPairOfInf = 0xFF80FF80u;
-    constexpr int kUnroll = 4, kStep = quarters ? kThreads : kUnroll * kThreads;
-    const int apart = quarters ? (ve - vb + 3) / 4 : kThreads;  // from one of a step's vectors to the next
-    const int end = quarters ? vb + apart : ve;                 // of the first one
-    uint32_t zeros = 0, low_n = 0, low_bits = 0;
-    const uint16_t own = (uint16_t)(kBinsHalf + (threadIdx.x & 63));
-    const u16x2 other = {own, own};
-    auto table = [&](int i) { return quarters && (i & 2) ? bin2 : h.bin; };
-    auto unit = [](int i) { return quarters && (i & 1) ? 0x10000u : 1u; };
-    // a token that is no pair's: of the row's ends (any), or without a bin (`odd`)
-    auto single = [&](uint32_t b, int i, bool odd) {
-        const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
-        if (q < kBinsHalf) {
-            if (!odd) atomicAdd(&table(i)[(b >> 15) * kSignWords + q], unit(i));
-        } else if (mag == 0) {
-            ++zeros;
-        } else if (mag < kMagLo) {
-            const uint32_t at = atomicAdd(&h.side_n, 1u);
-            if (at < kSideMax) h.side[at] = b;
-        } else if (b > 0x8000u && b < 0xFF80u) {
-            if (low_n == 0) low_bits = b;
-            if (b == low_bits) ++low_n;
-            else h.odd = 1;
-        } else if (b <= 0x7F80u) {
-            h.odd = 1;
-        }
-    };
-    // counts a pair; the bits that say that one of it has no bin
-    auto pair = [&](uint32_t w, int i) -> uint32_t {
-        const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo}, magnitude = {0x7FFF, 0x7FFF};
-        const u16x2 t = __builtin_bit_cast(u16x2, w) - lo;
-        const u16x2 a = (t >> 15) * (uint16_t)(4 * kSignWords) + (__builtin_elementwise_min(t & magnitude, other) << 2);
-        const uint32_t at = __builtin_bit_cast(uint32_t, a);
-        char *base = (char *)table(i);
-        atomicAdd((uint32_t *)(base + (at & 0xFFFFu)), unit(i));
-        atomicAdd((uint32_t *)(base + (at >> 16)), unit(i));
-        return __builtin_bit_cast(uint32_t, t) & kNoBin;
-    };
-    // of a pair with tokens without a bin: counts zeros and mask values; whether others are left
-    auto look = [&](uint32_t w) -> bool {
-        bool left = false;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t b = half ? w >> 16 : w & 0xFFFFu, mag = b & 0x7FFFu;
-            const bool zero = mag == 0, low = b == low_bits && low_n != 0;
-            zeros += zero;
-            low_n += low;
-            // neither a bin nor -inf or NaN (patterns above 0x7F80 of either sign, and -inf)
-            left |= mag - kMagLo >= kBinsHalf && !zero && !low && mag <= 0x7F80u && b != 0xFF80u;
-        }
-        return left;
-    };
-    // the vector's tokens that `look` left over (zeros and the known mask value are counted)
-    auto rest = [&](int v, int i, uint32_t known_low) {
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = r.p[r.head + (int64_t)v * 8 + j];
-            if ((b & 0x7FFFu) != 0 && b != known_low) single(b, i, true);
-        }
-    };
-    auto load = [&](uint4 (&q)[kUnroll], int v) {
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            q[i] = v < end && v + i * apart < ve ? row_vec(r, v + i * apart)
-                                                 : make_uint4(kPairOfInf, kPairOfInf, kPairOfInf, kPairOfInf);
-    };
-    uint4 next[kUnroll];
-    int v = vb + (int)threadIdx.x;
-    if (vb < end) load(next, v);
-    for (int v0 = vb; v0 < end; v0 += kStep, v += kStep) {
-        uint4 q[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) q[i] = next[i];
-        if (v0 + kStep < end) load(next, v + kStep);
-        uint32_t todo = 0;
-        const uint32_t known_low = low_n ? low_bits : 0;  // as the looks below know it
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t bad = pair(q[i].x, i) | pair(q[i].y, i) | pair(q[i].z, i) | pair(q[i].w, i);
-            // (a vector of -inf alone, as there are many in a masked row and past a row's end,
-            // needs no look)
-            if (bad && ((q[i].x ^ kPairOfInf) | (q[i].y ^ kPairOfInf) | (q[i].z ^ kPairOfInf) | (q[i].w ^ kPairOfInf))) {
-                const uint32_t left = (uint32_t)look(q[i].x) | (uint32_t)look(q[i].y) | (uint32_t)look(q[i].z) | (uint32_t)look(q[i].w);
-                todo |= left << i;
-            }
-        }
-        for (; todo; todo &= todo - 1) {
-            const int i = __builtin_ctz(todo);
-            rest(v + i * apart, i, known_low);
-        }
-    }
-    const int at = row_end(r, threadIdx.x, head, tail);
-    if (at >= 0) single(r.p[at], at < r.head ? 0 : 3, false);
-    if (zeros) atomicAdd(&h.zeros, zeros);
-    if (low_n) hist_low(h, low_bits, low_n);
-}
-
 // ---- wave scans on the cross-lane data path -----------------------------------------------
 
 template <int CTRL, int ROWS>
@@ -305,6 +178,211 @@ __device__ __forceinline__ double uniform(double v) {
 // The value one lane down, 0 in lane 0. All lanes take part in these scans.
 template <typename T>
 __device__ __forceinline__ T wave_down(T v) { return dpp0<0x138, 0xF>(v); }
+
+// ---- histogram of a row or of a part of it -------------------------------------------
+
+struct Hist {
+    uint32_t bin[kTable];
+    uint32_t side[kSideMax];
+    uint32_t side_n, zeros, odd;  // odd: the row needs the long way
+    uint32_t low_n, low_bits;     // tokens of the one pattern at or below -2^16
+};
+
+__device__ __forceinline__ void hist_clear(Hist &h) {
+    for (int i = threadIdx.x; i < (int)kTable / 4; i += kThreads) ((uint4 *)h.bin)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) h.side_n = h.zeros = h.odd = h.low_n = h.low_bits = 0;
+}
+
+// A token count for one pattern at or below -2^16; a second such pattern makes the row odd.
+__device__ __forceinline__ void hist_low(Hist &h, uint32_t bits, uint32_t n) {
+    const uint32_t was = atomicCAS(&h.low_bits, 0u, bits);
+    if (was != 0 && was != bits) h.odd = 1;
+    atomicAdd(&h.low_n, n);
+}
+
+// Counts vectors [vb, ve) of a row into h.bin, or (quarters) a whole row's four quarters
+// apart, 16 bits each, in h.bin and `bin2`. Two elements at a time, without a branch:
+// subtracting kMagLo from both magnitudes leaves the bins' places, and a minimum sends every
+// other token (-inf, NaN and what follows) to a word of the lane's own behind the bins, which
+// nobody reads: ten vector instructions and two LDS additions for two elements. A step's
+// four loads (of the four quarters, in that case) are issued a step ahead.
+//
+// One value can be most of a row (a mask's, or zeros), and LDS additions to one address go
+// one after another. Such a value is the wave's `common` one: its tokens go to the lanes' own
+// words too and are counted in registers, for seven more instructions a pair. A wave takes
+// it up where a step's first token is the same in kManyEqual lanes, or tokens without a bin
+// turn up in kManyOdd, and drops it after a step without it. What else has no bin is
+// read again by a loop of its own, which keeps the code of the usual case short.
+template <bool quarters>
+__device__ __forceinline__ void hist_count(Hist &h, uint32_t *bin2, const Row &r, int vb, int ve, bool head, bool tail) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    constexpr uint32_t kNoBin = 0x70007000u, kPairOfInf = 0xFF80FF80u;
+    constexpr int kManyEqual = 16, kManyOdd = 4;
+    constexpr int kUnroll = 4, kStep = quarters ? kThreads : kUnroll * kThreads;
+    const int apart = quarters ? (ve - vb + 3) / 4 : kThreads;  // from one of a step's vectors to the next
+    const int end = quarters ? vb + apart : ve;                 // of the first one
+    const int lane = threadIdx.x & 63;
+    const uint16_t own = (uint16_t)(kBinsHalf + lane);
+    const u16x2 other = {own, own};
+    bool has_common = false;  // these two are the same in the whole wave
+    uint32_t common = 0;
+    uint32_t n_lo = 0, n_hi = 0;  // the lane's common tokens, as the two tables take them
+    auto table = [&](int i) { return quarters && (i & 2) ? bin2 : h.bin; };
+    auto unit = [](int i) { return quarters && (i & 1) ? 0x10000u : 1u; };
+    // a token that is no pair's: of the row's ends (any), or without a bin (`odd`)
+    auto single = [&](uint32_t b, int i, bool odd) {
+        const uint32_t mag = b & 0x7FFFu, q = mag - kMagLo;
+        if (q < kBinsHalf) {
+            if (!odd) atomicAdd(&table(i)[(b >> 15) * kSignWords + q], unit(i));
+        } else if (mag == 0) {
+            atomicAdd(&h.zeros, 1u);
+        } else if (mag < kMagLo) {
+            const uint32_t at = atomicAdd(&h.side_n, 1u);
+            if (at < kSideMax) h.side[at] = b;
+        } else if (b > 0x8000u && b < 0xFF80u) {
+            hist_low(h, b, 1);
+        } else if (b <= 0x7F80u) {
+            h.odd = 1;
+        }
+    };
+    // whether a value can be the common one: one that has a bin, zero, below -2^16, -inf or NaN
+    auto countable = [](uint32_t b) { return (b & 0x7FFFu) == 0 || ((b & 0x7FFFu) >= kMagLo && b - 0x4780u > 0x3800u); };
+    // a pair's places in a table, in bytes
+    auto places = [&](u16x2 index, u16x2 t) -> uint32_t {
+        return __builtin_bit_cast(uint32_t, (u16x2)((t >> 15) * (uint16_t)(4 * kSignWords) + (index << 2)));
+    };
+    auto add = [&](uint32_t at, int i) {
+        char *base = (char *)table(i);
+        atomicAdd((uint32_t *)(base + (at & 0xFFFFu)), unit(i));
+        atomicAdd((uint32_t *)(base + (at >> 16)), unit(i));
+    };
+    const u16x2 lo = {(uint16_t)kMagLo, (uint16_t)kMagLo}, magnitude = {0x7FFF, 0x7FFF};
+    // counts a pair; the bits that say that one of it has no bin
+    auto pair = [&](uint32_t w, int i) -> uint32_t {
+        const u16x2 t = __builtin_bit_cast(u16x2, w) - lo;
+        add(places(__builtin_elementwise_min(t & magnitude, other), t), i);
+        return __builtin_bit_cast(uint32_t, t) & kNoBin;
+    };
+    // of a pair's halves, all ones where it is the common value
+    auto equal = [&](uint32_t w) -> u16x2 {
+        const u16x2 one = {1, 1};
+        return __builtin_elementwise_min(__builtin_bit_cast(u16x2, w ^ common), one) - one;
+    };
+    // `pair` where there is a common value: `n` counts it
+    auto pair_common = [&](uint32_t w, int i, u16x2 &n) -> uint32_t {
+        asm("" : "+v"(w));  // apart from `pair`, whose terms would be held across the branch between the two
+        const u16x2 t = __builtin_bit_cast(u16x2, w) - lo, e = equal(w);
+        add(places(__builtin_elementwise_max(__builtin_elementwise_min(t & magnitude, other), e & other), t), i);
+        n -= e;
+        return __builtin_bit_cast(uint32_t, t) & kNoBin & ~__builtin_bit_cast(uint32_t, e);
+    };
+    auto count_common = [&](u16x2 n, int i) {
+        const uint32_t sum = __builtin_amdgcn_sad_u16(__builtin_bit_cast(uint32_t, n), 0, 0);
+        (quarters && (i & 2) ? n_hi : n_lo) += sum * unit(i);
+    };
+    // the wave's common tokens into the tables
+    auto flush = [&]() {
+        const uint32_t at_lo = wave_scan(n_lo), at_hi = quarters ? wave_scan(n_hi) : 0;
+        n_lo = n_hi = 0;
+        has_common = false;
+        if (lane != 63) return;
+        const uint32_t b = common & 0xFFFFu, mag = b & 0x7FFFu;
+        const uint32_t sum = quarters ? __builtin_amdgcn_sad_u16(at_lo, 0, __builtin_amdgcn_sad_u16(at_hi, 0, 0)) : at_lo;
+        if (mag - kMagLo < kBinsHalf) {
+            const uint32_t at = (b >> 15) * kSignWords + mag - kMagLo;
+            atomicAdd(&h.bin[at], at_lo);
+            if constexpr (quarters) atomicAdd(&bin2[at], at_hi);
+        } else if (mag == 0) {
+            atomicAdd(&h.zeros, sum);
+        } else if (b > 0x8000u && b < 0xFF80u) {
+            hist_low(h, b, sum);
+        }
+    };
+    auto load = [&](uint4 (&q)[kUnroll], int v) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            q[i] = v < end && v + i * apart < ve ? row_vec(r, v + i * apart)
+                                                 : make_uint4(kPairOfInf, kPairOfInf, kPairOfInf, kPairOfInf);
+    };
+    uint4 next[kUnroll];
+    int v = vb + (int)threadIdx.x;
+    load(next, v);
+    // a wave's steps: nothing within waits for another wave
+    for (int v0 = vb + 64 * wave_id(); v0 < end; v0 += kStep, v += kStep) {
+        uint4 q[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) q[i] = next[i];
+        if (v0 + kStep < end) load(next, v + kStep);
+        if (!has_common) {
+            const uint32_t b = q[0].x & 0xFFFFu, b0 = uniform(b);
+            if (__popcll(__ballot(b == b0)) >= kManyEqual && countable(b0)) has_common = true, common = b0 << 16 | b0;
+        }
+        uint64_t lanes[kUnroll];  // with tokens that have no bin
+        if (!has_common) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                lanes[i] = __ballot((pair(q[i].x, i) | pair(q[i].y, i) | pair(q[i].z, i) | pair(q[i].w, i)) != 0);
+        } else {
+            const uint32_t was_lo = n_lo, was_hi = n_hi;
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                u16x2 n = {0, 0};
+                lanes[i] = __ballot((pair_common(q[i].x, i, n) | pair_common(q[i].y, i, n) | pair_common(q[i].z, i, n) |
+                                     pair_common(q[i].w, i, n)) != 0);
+                count_common(n, i);
+            }
+            if (!__ballot(n_lo != was_lo || n_hi != was_hi)) flush();
+        }
+        if (!(lanes[0] | lanes[1] | lanes[2] | lanes[3])) continue;
+        bool taken = false;  // the common value, here
+#pragma unroll 1
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint64_t some = i == 0 ? lanes[0] : i == 1 ? lanes[1] : i == 2 ? lanes[2] : lanes[3];
+            const bool within = v < end && v + i * apart < ve;
+            if (!(some & __ballot(within)) && !taken) continue;
+            const uint4 x = within ? row_vec(r, v + i * apart) : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, left = 0;
+            auto look = [&]() {
+                u16x2 n = {0, 0};
+                left = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const u16x2 e = has_common ? equal(w[j]) : n - n;
+                    left |= __builtin_bit_cast(uint32_t, __builtin_bit_cast(u16x2, w[j]) - lo) & kNoBin & ~__builtin_bit_cast(uint32_t, e);
+                    n -= e;
+                }
+                if (taken) count_common(n, i);
+            };
+            look();
+            const uint64_t odd = __ballot(left != 0);
+            if (!has_common && __popcll(odd) >= kManyOdd) {
+                const int from = __builtin_ctzll(odd);
+                uint32_t b = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t two = (uint32_t)__builtin_amdgcn_readlane((int)w[j >> 1], from);
+                    const uint32_t of = j & 1 ? two >> 16 : two & 0xFFFFu;
+                    if ((of & 0x7FFFu) - kMagLo >= kBinsHalf) b = of;
+                }
+                if (countable(b)) {
+                    has_common = taken = true, common = b << 16 | b;
+                    look();
+                }
+            }
+            if (!left) continue;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = w[0] & 0xFFFFu;
+                if (!(has_common && b == (common & 0xFFFFu))) single(b, i, true);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = __builtin_amdgcn_alignbit(k < 3 ? w[k + 1] : 0, w[k], 16);
+            }
+        }
+    }
+    if (has_common) flush();
+    const int at = row_end(r, threadIdx.x, head, tail);
+    if (at >= 0) single(r.p[at], at < r.head ? 0 : 3, false);
+}
 
 // ---- the draw ---------------------------------------------------------------------------
 
@@ -835,16 +913,16 @@ __device__ __forceinline__ int locate(Draw &sh, const Row &r, int vb, int ve, bo
 
 // ---- kernels ------------------------------------------------------------------------------
 
-// One workgroup per row: count, draw, find. M = 1024, V = 248320: 115 us (4.4 TB/s), of a
-// workgroup's 55 us 37 are the counting and 5 the search. The row's quarters are counted apart, which
+// One workgroup per row: count, draw, find. M = 1024, V = 248320: 110 us (4.6 TB/s), of a
+// workgroup's 53 us 35 are the counting and 5 the search. The row's quarters are counted apart, which
 // tells where to look for the occurrence: reading half a row again, as a search from its
 // beginning does on average, took a third of the time.
 //
 // With more rows than compute units two workgroups share one (64 registers), so that one's
 // draw runs beside the other's reading. A call of the long way, never taken, would cost
-// them its stack and spilled registers (M = 1024, V = 248320: 134 us instead of 115), so
+// them its stack and spilled registers (M = 1024, V = 248320: a sixth more time), so
 // rows that need it are marked and left to a launch of their own, whose workgroups
-// otherwise end at once (3 us). With fewer rows the call is the cheaper one (M = 1: 13 us
+// otherwise end at once (4 us). With fewer rows the call is the cheaper one (M = 1: 13 us
 // instead of 15).
 constexpr int64_t kMaxQuarter = 65535 / 8 - 2;  // vectors: a quarter's tokens fit 16 bits
 constexpr int kLongWay = -2;
@@ -923,9 +1001,9 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
     }
 }
 
-// Few rows: a workgroup per part of a row counts it (7.9 us at M = 1, V = 248320, 8 parts:
+// Few rows: a workgroup per part of a row counts it (8.2 us at M = 1, V = 248320, 8 parts:
 // 0.7 clearing, 2.6 reading and adding, 2.7 for the list), and one per row draws from the
-// lists (13.4 us: 2.5 reading them, 1.8 weighing, 1.2 a seek, 3.5 finding the token).
+// lists (13.8 us: 2.5 reading them, 1.8 weighing, 1.2 a seek, 3.5 finding the token).
 //
 // Workspace of one (row, part): header, then the occurring bins in descending order
 // (place in that order << 18 | count), then the smaller magnitudes.
@@ -1197,11 +1275,12 @@ __global__ __launch_bounds__(256) void accept_kernel(const int32_t *__restrict__
 SamplePlan plan_sample(int64_t M, int64_t V, int num_cus) {
     SamplePlan p{};
     const int64_t nvec = V / 8 + 1;
-    // parts of a row: enough workgroups to fill the chip, at least one vector a thread, no
-    // more than 8 (M = 1, nothing filtered: 29 us with 8, 32 with 16, 39 with 31: the lists
-    // grow), and one where there would be fewer than 4 (M = 100: 43 us with 3, 34 with one)
-    int64_t C = std::min<int64_t>((num_cus + M - 1) / M, (nvec + kThreads - 1) / kThreads);
-    C = C < 4 ? 1 : std::min<int64_t>(C, 8);
+    // parts of a row: as many workgroups as the chip holds at once (44 rows: 28.6 us with 5,
+    // 31.3 with 6), at least one vector a thread, no more than 8 (M = 1, nothing filtered: 29 us
+    // with 8, 32 with 16, 39 with 31: the lists grow), and one where there would be fewer than 5
+    // (64 rows: with 4 parts 34.2 us, filtered 29.7; with one 30.6 and 32.1)
+    int64_t C = std::min<int64_t>(num_cus / M, (nvec + kThreads - 1) / kThreads);
+    C = C < 5 ? 1 : std::min<int64_t>(C, 8);
     if (C > 1) C = std::max<int64_t>(C, (nvec + kMaxPartVectors - 1) / kMaxPartVectors);
     p.parts = (int)std::max<int64_t>(C, 1);
     p.mark = M > num_cus;

@@ -339,6 +339,37 @@ def test_heavy_values(M):
         _check(l[:rows], u[:rows].cpu().numpy(), ("heavy", value), got=(got[0][:rows], got[1][:rows]))
 
 
+@pytest.mark.parametrize("M,V", [(1, VOCAB), (3, 30011), (30, 60000), (100, VOCAB), (100, 601), (260, 50021), (2, 700003), (300, 280001)])
+def test_changing_common_values(M, V):
+    """Blocks of a row, each with one or two values in a share of it: masks, zeros, likely
+    tokens, NaN; one row of two values below every bin, which is counted another way."""
+    import spec_verify_amd as svq
+    _say("sample common values", M, V)
+    rng = np.random.default_rng(M * 7 + V)
+    inf, nan = float("inf"), float("nan")
+    kinds = [((-inf,), 0.95), ((-1e4,), 0.5), ((0.0,), 0.8), ((0.0, -0.0), 0.9), ((-3e38,), 0.3), ((7.5,), 0.6),
+             ((nan,), 0.4), ((0.0, -inf), 0.7), ((-1e4, 0.0), 0.9), ((6.0,), 1.0), ((-inf,), 0.1), ((-3e38, -inf), 0.5),
+             ((1.0,), 0.0)]
+    rows = min(M, 5)
+    l = rng.normal(size=(rows, V)) * 2.2
+    for m in range(rows):
+        at = 0
+        while at < V:
+            n = int(np.exp(rng.uniform(np.log(8), np.log(max(V // 3, 9)))))
+            values, share = kinds[rng.integers(len(kinds))]
+            here = l[m, at:at + n]
+            chosen = rng.random(len(here)) < share
+            here[chosen] = np.asarray(values)[rng.integers(0, len(values), int(chosen.sum()))]
+            at += n
+    l[rows - 1, rng.integers(0, V, 5)] = -2.5e38
+    l = torch.tensor(l, dtype=torch.bfloat16, device="cuda").repeat((M + rows - 1) // rows, 1)[:M].contiguous()
+    for draw in range(3):
+        u = rng.random(M).astype(np.float32)
+        T = np.where(rng.random(M) < 0.3, 4.0, 1.0)
+        got = svq.sample(l, torch.tensor(u, device="cuda"), torch.tensor(T, dtype=torch.float32, device="cuda"))
+        _check(l[:rows], u[:rows], ("common", M, V, draw), T=T[:rows], got=(got[0][:rows], got[1][:rows]))
+
+
 def test_graph_replays_and_streams():
     import spec_verify_amd as svq
     _say("sample graph")
