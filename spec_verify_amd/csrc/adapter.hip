@@ -7,7 +7,7 @@
 //
 // Rows are worked on in items: up to 16 rows of one adapter, out of 256 consecutive rows
 // wherever they stand among them. An adapter that several requests share is then read
-// once per 16 of their rows. Two launches:
+// once per 16 of their rows. Two launches (or one, where little is to be read):
 //
 // 1. down: t, split over K. A workgroup finds its item (each row's rank among the rows of
 //    its adapter, by ballots on the bits of the index; one writes the item down for the
@@ -21,8 +21,9 @@
 // An output element depends on its own row of x and on its own adapter only, so one
 // request's infinities or NaN never reach another.
 //
-// Measured (us on the GPU, both launches; bytes of x, A, B, base and out once):
+// Measured (us on the GPU, all launches; bytes of x, A, B, base and out once):
 //   M = 1, K = N = 5120, R = 16: 8.1 (latency: each launch waits for memory twice)
+//   M = 37, K = 640, N = 1040, R = 24, 5 adapters: 5.6 (one launch)
 //   M = 128, K = 5120, N = 17408, R = 32, 32 adapters: 17.0 (52 MB: 3.1 TB/s)
 //   M = 128, K = 17408, N = 5120, R = 64, 6 adapters: 18.9 (25 MB: 1.3 TB/s)
 //   M = 2001, K = 5120, N = 6144, R = 16, 3 adapters: 26.0 (70 MB: 2.7 TB/s)
@@ -357,6 +358,139 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
     }
 }
 
+// Both products in one launch, for a short K and few items: a workgroup takes 512 columns
+// of an item and computes the item's whole t itself. That reads A once per workgroup, and a
+// compute unit gets about 30 GB/s of it (5 us for 160 KB); against that stands a launch with its
+// waits for memory (M = 37, K = 640, N = 1040, R = 24: 5.5 us instead of 8.0). RT rank tiles.
+constexpr int kOneWaves = 16;
+constexpr int kOneColumns = 32 * kOneWaves;
+template <int RT>
+__global__ __launch_bounds__(64 * kOneWaves) __attribute__((amdgpu_waves_per_eu(4))) void adapter_one_kernel(
+    const uint16_t *base, const uint16_t *__restrict__ x, const uint16_t *__restrict__ a,
+    const uint16_t *__restrict__ b, const int32_t *__restrict__ rows, const float *__restrict__ scales, uint16_t *out,
+    int64_t M, int N, int K, int R, int slots, int64_t ld_base, int64_t ld_out, int col_blocks) {
+    constexpr int NS = (RT + 1) / 2;     // 32-rank steps
+    constexpr int kPitch = 32 * NS + 8;
+    constexpr int kAhead = RT == 1 ? 2 : 1;  // K tiles in flight
+    static_assert(256 * RT <= 64 * kOneWaves, "one thread sums one element of t");
+    __shared__ float red[kOneWaves][RT * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
+    __shared__ __attribute__((aligned(16))) int ids[16], item_slot;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r = lane & 15, g = lane >> 4;
+    const int cb = blockIdx.x % col_blocks, item = blockIdx.x / col_blocks;
+    const int blocks = (int)((M + kBlockRows - 1) / kBlockRows);
+    const int64_t row0 = (int64_t)(item % blocks) * kBlockRows;
+    if (wave == 0) {
+        Items items;
+        items.find(rows, row0, M, slots, lane);
+        if (lane < 16) ids[lane] = -1;
+        __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses are done in order
+        const int found = items.get(item / blocks, lane, ids);
+        if (lane == 0) item_slot = found;
+    }
+    __syncthreads();
+    const int s = __builtin_amdgcn_readfirstlane(item_slot);
+    if (s < 0) return;
+    // MFMA row 4 g' + i of product q is column 8 g' + 4 q + i: a lane ends up with 8
+    // consecutive columns of one row
+    const int col0 = (cb * kOneWaves + wave) * 32;
+    const int col = col0 + 8 * g, id = ids[r];
+    const int64_t m = row0 + id;
+    const bool mine = id >= 0 && col < N;
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (mine) y = *(const uint4 *)(base + m * ld_base + col);
+    if (s == slots) {  // rows without an adapter
+        if (mine && (const uint16_t *)out != base) *(uint4 *)(out + m * ld_out + col) = y;
+        return;
+    }
+    uint4 bv[NS][2];
+    const int brow = col0 + 8 * (r >> 2) + (r & 3);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            bv[st][q] = make_uint4(0, 0, 0, 0);
+            if (brow + 4 * q < N && 32 * st + 8 * g < R)
+                bv[st][q] = *(const uint4 *)(b + ((int64_t)s * N + brow + 4 * q) * R + 32 * st + 8 * g);
+        }
+    const float scale = scales[s];
+    const uint16_t *xp = x + (row0 + max(id, ids[0])) * K + 8 * g;  // past the last: the first again
+    const uint16_t *ap[RT];
+    bool in[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        in[i] = 16 * i + r < R;  // ranks past R: no load, a zero operand
+        ap[i] = a + ((int64_t)s * R + min(16 * i + r, R - 1)) * K + 8 * g;
+    }
+    f32x4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int KT = K >> 7;
+    for (int k0 = wave; k0 < KT; k0 += kAhead * kOneWaves) {
+        uint4 xv[kAhead][4], av[kAhead][RT][4];
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+            const int kt = k0 + h * kOneWaves;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                xv[h][j] = kt < KT && id >= 0 ? *(const uint4 *)(xp + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    av[h][i][j] = kt < KT && in[i] ? *(const uint4 *)(ap[i] + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i] = mfma16x16x32(xv[h][j], av[h][i][j], acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *(f32x4 *)&red[wave][256 * i + 4 * lane] = acc[i];
+    __syncthreads();
+    const int at = threadIdx.x;
+    if (at < 256 * RT) {  // element i of lane l of tile j: row 4 (l / 16) + i, rank 16 j + l % 16
+        float t = red[0][at];
+#pragma unroll
+        for (int w = 1; w < kOneWaves; ++w) t += red[w][at];
+        // scale * t, rounded in two halves
+        const float f = scale * t;
+        const uint32_t hi = f32_to_bf16_rne(f);
+        const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
+        const int row = 4 * (at >> 6 & 3) + (at & 3), rank = 16 * (at >> 8) + (at >> 2 & 15);
+        thi[row][rank] = (uint16_t)hi;
+        tlo[row][rank] = (uint16_t)lo;
+    } else if (RT == 1 && at < 512) {  // of a step of 32 ranks, those past the tile
+        thi[at >> 4 & 15][16 + (at & 15)] = 0;
+        tlo[at >> 4 & 15][16 + (at & 15)] = 0;
+    }
+    __syncthreads();
+    f32x4 o[2];
+    o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+        const uint4 hi = *(const uint4 *)&thi[r][32 * st + 8 * g];
+        const uint4 lo = *(const uint4 *)&tlo[r][32 * st + 8 * g];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            o[q] = mfma16x16x32(bv[st][q], hi, o[q]);
+            o[q] = mfma16x16x32(bv[st][q], lo, o[q]);
+        }
+    }
+    if (mine) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (&y.x)[j];
+            w[j] = (uint32_t)f32_to_bf16_rne(bits_f32(v << 16) + o[j >> 1][2 * (j & 1)]) |
+                   (uint32_t)f32_to_bf16_rne(bits_f32(v & 0xFFFF0000u) + o[j >> 1][2 * (j & 1) + 1]) << 16;
+        }
+        *(uint4 *)(out + m * ld_out + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 }  // namespace
 
 AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slots) {
@@ -381,6 +515,12 @@ AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slo
     p.range_blocks = (int)blocks;
     p.col_blocks = (int)((N + 64 * kUpWaves - 1) / (64 * kUpWaves));
     if (p.col_blocks > 4) p.col_blocks = (p.col_blocks + 7) / 8 * 8;
+    // One launch: while A's part is 80 KB at most (N = 2560, one row, us: R = 16, K = 2560 6.6, two
+    // launches 8.1; K = 5120, N = 5120 9.4 and 8.0; R = 32, K = 1280 6.6 and 8.5, K = 2560 8.9 and
+    // 8.9) and the chip holds the workgroups at once (R = 16, K = 640, N = 5120: 16 adapters 5.2
+    // and 8.1, 32 adapters, which are 320 workgroups, 9.6 and 8.8).
+    p.one_launch = R <= 32 && 16 * p.rank_tiles * K <= 40960 &&
+                   p.row_blocks * p.items * ((N + kOneColumns - 1) / kOneColumns) <= 256;
     p.workspace_bytes = kCounterBytes + (size_t)p.row_blocks * p.items * sizeof(Item) + (size_t)p.splits * M * R * 4;
     return p;
 }
@@ -389,6 +529,18 @@ hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld
                               const void *b, const int32_t *rows, const float *scales, void *out, int64_t ld_out,
                               int64_t M, int64_t N, int64_t K, int R, int slots, void *workspace,
                               hipStream_t stream) {
+    if (p.one_launch) {
+        const int cols = (int)((N + kOneColumns - 1) / kOneColumns);
+        const dim3 grid((uint32_t)(p.row_blocks * p.items * cols));
+#define SVQ_ONE(RT)                                                                                                  \
+    hipLaunchKernelGGL((adapter_one_kernel<RT>), grid, dim3(64 * kOneWaves), 0, stream, (const uint16_t *)base,      \
+                       (const uint16_t *)x, (const uint16_t *)a, (const uint16_t *)b, rows, scales, (uint16_t *)out, \
+                       M, (int)N, (int)K, R, slots, ld_base, ld_out, cols)
+        if (R <= 16) SVQ_ONE(1);
+        else SVQ_ONE(2);
+#undef SVQ_ONE
+        return hipGetLastError();
+    }
     Item *table = (Item *)ws_partials(workspace);
     float *part = (float *)(table + p.row_blocks * p.items);
     const dim3 down((uint32_t)(p.row_blocks * p.items * p.rank_chunks * p.range_blocks));

@@ -11,11 +11,13 @@ int device_cus();  // compute units of the current device (svq_api.cpp)
 // Low-rank adapters: blocks of 256 rows, in each at most `items` groups of up to 16 rows
 // of one adapter. First launch: an item, rank_tiles x 16 ranks and one of `splits` K
 // ranges (of tiles_per_split 128-element tiles; range_blocks block indexes) per workgroup.
-// Second: an item and 256 columns (col_blocks block indexes).
+// Second: an item and 256 columns (col_blocks block indexes). Or one launch for both; the
+// workspace is the same for either.
 struct AdapterPlan {
     int64_t row_blocks;
     int items, rank_tiles, rank_chunks, splits, tiles_per_split, range_blocks;
     int col_blocks;
+    bool one_launch;
     size_t workspace_bytes;
 };
 AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slots);

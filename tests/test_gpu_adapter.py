@@ -119,6 +119,31 @@ def test_against_the_formula(M, K, N, R, slots, pattern):
     _check(p, _call(_dev(p)), (M, K, N, R, slots, pattern))
 
 
+# few items and a short K (one launch), and either bound passed
+@pytest.mark.parametrize("M,K,N,R,slots,pattern", [
+    (1, 2560, 512, 16, 1, "one"),
+    (1, 2688, 512, 16, 1, "one"),
+    (3, 1280, 528, 32, 2, "each"),
+    (3, 1408, 528, 32, 2, "each"),
+    (31, 128, 1552, 24, 5, "random"),
+    (256, 2560, 48, 16, 9, "random"),
+    (300, 640, 1040, 24, 3, "chunks"),
+    (600, 2688, 96, 16, 5, "random"),
+    (129, 1280, 6160, 32, 40, "each"),
+    (1000, 256, 1040, 8, 30, "random"),
+    (2001, 640, 80, 8, 3, "chunks"),
+    (17, 2560, 7680, 8, 16, "each"),
+    (17, 2560, 7696, 8, 16, "each"),
+])
+def test_one_launch_and_two(M, K, N, R, slots, pattern):
+    _say("adapter launches", M, K, N, R, slots, pattern)
+    p = _problem(M * 5 + K, M, K, N, R, slots, pattern)
+    d = _dev(p)
+    out = _call(d)
+    _check(p, out, (M, K, N, R, slots, pattern))
+    assert torch.equal(_call(d, out=d["base"]), out)
+
+
 @pytest.mark.parametrize("M,R", [(5, 16), (37, 40), (130, 136)])
 def test_exact_on_integers(M, R):
     """Small whole numbers: every sum is exact in fp32 and every result in bf16
