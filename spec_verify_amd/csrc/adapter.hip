@@ -23,7 +23,7 @@
 //
 // Measured (us on the GPU, all launches; bytes of x, A, B, base and out once):
 //   M = 1, K = N = 5120, R = 16: 8.1 (latency: each launch waits for memory twice)
-//   M = 37, K = 640, N = 1040, R = 24, 5 adapters: 5.6 (one launch)
+//   M = 37, K = 640, N = 1040, R = 24, 5 adapters: 5.5 (one launch)
 //   M = 128, K = 5120, N = 17408, R = 32, 32 adapters: 17.0 (52 MB: 3.1 TB/s)
 //   M = 128, K = 17408, N = 5120, R = 64, 6 adapters: 18.9 (25 MB: 1.3 TB/s)
 //   M = 2001, K = 5120, N = 6144, R = 16, 3 adapters: 26.0 (70 MB: 2.7 TB/s)
