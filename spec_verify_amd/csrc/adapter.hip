@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * kOneWaves) __attribute__((amdgpu_waves_per_eu(
             const int kt = k0 + h * kOneWaves;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                xv[h][j] = kt < KT && id >= 0 ? *(const uint4 *)(xp + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
+                xv[h][j] = kt < KT ? *(const uint4 *)(xp + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
                     av[h][i][j] = kt < KT && in[i] ? *(const uint4 *)(ap[i] + kt * 128 + 32 * j) : make_uint4(0, 0, 0, 0);
