@@ -455,11 +455,12 @@ __global__ __launch_bounds__(64 * kOneWaves) __attribute__((amdgpu_waves_per_eu(
         float t = red[0][at];
 #pragma unroll
         for (int w = 1; w < kOneWaves; ++w) t += red[w][at];
-        // scale * t, rounded in two halves
-        const float f = scale * t;
+        const int row = 4 * (at >> 6 & 3) + (at & 3), rank = 16 * (at >> 8) + (at >> 2 & 15);
+        // scale * t, rounded in two halves. Ranks past R are zero whatever their sum of zero
+        // products: it is NaN where x holds an infinity.
+        const float f = rank < R ? scale * t : 0.f;
         const uint32_t hi = f32_to_bf16_rne(f);
         const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
-        const int row = 4 * (at >> 6 & 3) + (at & 3), rank = 16 * (at >> 8) + (at >> 2 & 15);
         thi[row][rank] = (uint16_t)hi;
         tlo[row][rank] = (uint16_t)lo;
     } else if (RT == 1 && at < 512) {  // of a step of 32 ranks, those past the tile
