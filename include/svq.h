@@ -363,10 +363,10 @@ size_t svq_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R, i
  * every row adds its own adapter's product,
  *     out[m] = base[m] + scales[s] * B_s (A_s x[m]),   s = rows[m].
  * A row whose index is outside [0, slots) has no adapter: out[m] = base[m].
- * Products and sums are fp32 (the rank-R intermediate enters the second product
- * with 16 significant bits), out is rounded to bf16 (nearest even) once. Rows
- * are independent: no row's result depends on another row or on an adapter that
- * is not its own.
+ * Products and sums are fp32, the rank-R intermediate too (all 24 bits of it enter
+ * the second product), out is rounded to bf16 (nearest even) once. Rows are
+ * independent: no row's result depends on another row or on an adapter that is
+ * not its own.
  *   base     bf16 [M][ld_base], the first N columns of each row; 16-byte aligned
  *   x        bf16 [M][K], 16-byte aligned
  *   a        bf16 [slots][R][K], 16-byte aligned, finite (any size: 64-bit offsets)

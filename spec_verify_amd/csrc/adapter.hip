@@ -28,10 +28,11 @@
 //   M = 128, K = 17408, N = 5120, R = 64, 6 adapters: 18.9 (25 MB: 1.3 TB/s)
 //   M = 2001, K = 5120, N = 6144, R = 16, 3 adapters: 26.0 (70 MB: 2.7 TB/s)
 //
-// t stays fp32 up to the second product, whose bf16 operand is scale * t split in two
-// (high and low halves, 16 significant bits): rounding it to one bf16 would put an error
-// of the size of the output's own rounding on the sum. MFMA time is idle here: the bound
-// is the bytes of A, B, base and out (or, for a few rows, latency).
+// t stays fp32 in the second product too: its bf16 operand is scale * t cut into three parts
+// of 8 significant bits, which together are all 24. (Two parts rounded to nearest keep 16:
+// where base and the product cancel, the median element's error then is 1.9 times as large,
+// and a value past the largest bf16 becomes an infinity.) MFMA time is idle here: the bound is
+// the bytes of A, B, base and out (or, for a few rows, latency).
 #include <algorithm>
 
 #include "svq_requests.h"
@@ -122,6 +123,25 @@ struct Items {
             if (slot[j] == s && rank[j] >> 4 == q) ids[rank[j] & 15] = 64 * j + lane;
         }
         return s;
+    }
+};
+
+// An fp32 value as the exact sum of three bf16 patterns, each cut off the rest (below 2^-110
+// what falls under the smallest bf16 is lost). Infinities and NaN are the first part.
+struct Parts {
+    uint32_t part[3];
+    __device__ __forceinline__ explicit Parts(float f) {
+        const uint32_t u = f32_bits(f);
+        if ((u & 0x7F800000u) == 0x7F800000u) {
+            part[0] = u >> 16 | ((u & 0x7FFFFFu) ? 0x40u : 0);
+            part[1] = part[2] = 0;
+        } else {
+            const float r = f - bits_f32(u & 0xFFFF0000u);
+            const uint32_t v = f32_bits(r);
+            part[0] = u >> 16;
+            part[1] = v >> 16;
+            part[2] = f32_bits(r - bits_f32(v & 0xFFFF0000u)) >> 16;
+        }
     }
 };
 
@@ -235,7 +255,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
     constexpr int kEach = 2 * NS;            // ranks of a thread where t is put together
     constexpr int kVec = kEach < 4 ? kEach : 4;
     constexpr int kAhead = NS <= 2 ? 8 : (NS == 4 ? 4 : 2);  // K ranges of t in flight
-    __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
+    __shared__ __attribute__((aligned(16))) uint16_t ts[3][16][kPitch];  // scale * t in three parts
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
     const int cg = blockIdx.x % col_blocks;
@@ -315,35 +335,24 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(
     }
     add();
     const float scale = scales[s];
-    // scale * t, rounded in two halves
 #pragma unroll
     for (int i = 0; i < kEach; i += 2) {
-        uint32_t hi2 = 0, lo2 = 0;
+        const Parts even(scale * t[i]), odd(scale * t[i + 1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float f = scale * t[i + e];
-            const uint32_t hi = f32_to_bf16_rne(f);
-            const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
-            hi2 |= hi << (16 * e);
-            lo2 |= lo << (16 * e);
-        }
-        *(uint32_t *)&thi[trow][rank0 + i] = hi2;
-        *(uint32_t *)&tlo[trow][rank0 + i] = lo2;
+        for (int h = 0; h < 3; ++h) *(uint32_t *)&ts[h][trow][rank0 + i] = even.part[h] | odd.part[h] << 16;
     }
     lds_barrier();
     f32x4 acc[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
-        const uint4 hi = *(const uint4 *)&thi[r][32 * st + 8 * g];
-        const uint4 lo = *(const uint4 *)&tlo[r][32 * st + 8 * g];
+    for (int st = 0; st < NS; ++st)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            acc[q] = mfma16x16x32(bv[st][q], hi, acc[q]);
-            acc[q] = mfma16x16x32(bv[st][q], lo, acc[q]);
+        for (int h = 0; h < 3; ++h) {
+            const uint4 tv = *(const uint4 *)&ts[h][r][32 * st + 8 * g];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = mfma16x16x32(bv[st][q], tv, acc[q]);
         }
-    }
     if (mine) {
         uint32_t o[8];
 #pragma unroll
@@ -374,7 +383,7 @@ __global__ __launch_bounds__(64 * kOneWaves) __attribute__((amdgpu_waves_per_eu(
     constexpr int kAhead = RT == 1 ? 2 : 1;  // K tiles in flight
     static_assert(256 * RT <= 64 * kOneWaves, "one thread sums one element of t");
     __shared__ float red[kOneWaves][RT * 256];
-    __shared__ __attribute__((aligned(16))) uint16_t thi[16][kPitch], tlo[16][kPitch];
+    __shared__ __attribute__((aligned(16))) uint16_t ts[3][16][kPitch];  // scale * t in three parts
     __shared__ __attribute__((aligned(16))) int ids[16], item_slot;
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
@@ -456,30 +465,26 @@ __global__ __launch_bounds__(64 * kOneWaves) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
         for (int w = 1; w < kOneWaves; ++w) t += red[w][at];
         const int row = 4 * (at >> 6 & 3) + (at & 3), rank = 16 * (at >> 8) + (at >> 2 & 15);
-        // scale * t, rounded in two halves. Ranks past R are zero whatever their sum of zero
-        // products: it is NaN where x holds an infinity.
-        const float f = rank < R ? scale * t : 0.f;
-        const uint32_t hi = f32_to_bf16_rne(f);
-        const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16_rne(f - bits_f32(hi << 16));
-        thi[row][rank] = (uint16_t)hi;
-        tlo[row][rank] = (uint16_t)lo;
+        // Ranks past R are zero whatever their sum of zero products: it is NaN where x holds
+        // an infinity.
+        const Parts v(rank < R ? scale * t : 0.f);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) ts[h][row][rank] = (uint16_t)v.part[h];
     } else if (RT == 1 && at < 512) {  // of a step of 32 ranks, those past the tile
-        thi[at >> 4 & 15][16 + (at & 15)] = 0;
-        tlo[at >> 4 & 15][16 + (at & 15)] = 0;
+#pragma unroll
+        for (int h = 0; h < 3; ++h) ts[h][at >> 4 & 15][16 + (at & 15)] = 0;
     }
     __syncthreads();
     f32x4 o[2];
     o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
-        const uint4 hi = *(const uint4 *)&thi[r][32 * st + 8 * g];
-        const uint4 lo = *(const uint4 *)&tlo[r][32 * st + 8 * g];
+    for (int st = 0; st < NS; ++st)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            o[q] = mfma16x16x32(bv[st][q], hi, o[q]);
-            o[q] = mfma16x16x32(bv[st][q], lo, o[q]);
+        for (int h = 0; h < 3; ++h) {
+            const uint4 tv = *(const uint4 *)&ts[h][r][32 * st + 8 * g];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) o[q] = mfma16x16x32(bv[st][q], tv, o[q]);
         }
-    }
     if (mine) {
         uint32_t w[4];
 #pragma unroll

@@ -52,3 +52,57 @@ def test_an_infinity_is_a_rows_own_whatever_the_rank(K, R):
     got = _call(p)
     assert bool((got[2] == float("inf")).all()) and bool((got[4] == -float("inf")).all())
     assert torch.equal(got[[0, 1, 3]], clean[[0, 1, 3]])
+
+
+def _one_hot_pairs(slots, N, R):
+    """B that takes the difference of two neighbouring ranks, another pair in each column."""
+    b = torch.zeros(slots, N, R)
+    n = torch.arange(N)
+    first = 2 * (n % (R // 2))
+    b[:, n, first], b[:, n, first + 1] = 1.0, -1.0
+    return b.bfloat16(), first
+
+
+@pytest.mark.parametrize("K,R,M", [(256, 8, 3), (640, 24, 37), (1280, 32, 5), (1408, 32, 5), (512, 64, 19), (384, 136, 40)])
+def test_all_24_bits_of_the_intermediate_reach_the_output(K, R, M):
+    """t is a whole number of 24 bits, put together from three exact parts; an output is the
+    difference of two such numbers, below 2^7: every product and sum is exact in fp32, so the
+    output is too."""
+    _say("adapter 24 bits", K, R, M)
+    g = torch.Generator().manual_seed(K + R)
+    slots, N = 3, 80
+    pairs = R // 2
+    t = torch.randint(1 << 23, 1 << 24, (slots, pairs), generator=g)
+    t = torch.stack([t, t ^ torch.randint(0, 1 << 7, (slots, pairs), generator=g)], 2).view(slots, R)
+    a = torch.zeros(slots, R, K)
+    at = torch.randperm(K, generator=g)[:3]
+    for part in range(3):
+        a[:, :, at[part]] = (t >> (8 * part) & 255).float() * 2.0 ** (8 * part)
+    x = torch.zeros(M, K)
+    x[:, at] = 1.0
+    b, first = _one_hot_pairs(slots, N, R)
+    rows = torch.randint(-1, slots, (M,), generator=g)
+    p = dict(base=torch.zeros(M, N).bfloat16(), x=x.bfloat16(), a=a.bfloat16(), b=b, rows=rows.int(),
+             scales=torch.tensor([1.0, 0.5, 4.0]))
+    assert torch.equal(p["a"].float(), a)
+    want = (t[:, first] - t[:, first + 1]).double() * p["scales"].double()[:, None]
+    want = torch.cat([want, torch.zeros(1, N)])[rows]
+    assert torch.equal(_call(p).double(), want)
+
+
+@pytest.mark.parametrize("K,R", [(256, 8), (1280, 32), (1408, 32), (256, 64)])
+def test_an_intermediate_next_to_the_largest_float(K, R):
+    """t = 2^128 - 2^118, finite in fp32 and past the largest bf16: times 2^-10 it is
+    2^118 - 2^108 and no infinity."""
+    _say("adapter large intermediate", K, R)
+    M, N = 4, 32
+    x, a, b = torch.zeros(M, K), torch.zeros(1, R, K), torch.zeros(1, N, R)
+    x[:, 5] = x[:, 9] = 1.0
+    a[0, 3, 5], a[0, 3, 9] = 2.0 ** 128 - 2.0 ** 120, 0.75 * 2.0 ** 120
+    b[0, :, 3] = 2.0 ** -10
+    p = dict(base=torch.zeros(M, N).bfloat16(), x=x.bfloat16(), a=a.bfloat16(), b=b.bfloat16(),
+             rows=torch.tensor([0, 0, -1, 0], dtype=torch.int32), scales=torch.ones(1))
+    got = _call(p).double()
+    want = 2.0 ** 118 - 2.0 ** 108   # 10 bits: half a bf16 step off at most
+    assert bool((got[2] == 0).all())
+    assert bool(((got[[0, 1, 3]] - want).abs() <= 2.0 ** -8 * want).all())
