@@ -1289,32 +1289,50 @@ SamplePlan plan_sample(int64_t M, int64_t V, int num_cus) {
     return p;
 }
 
+namespace {
+
+// A workgroup per row, of rows that one launch takes.
+hipError_t launch_rows(const SamplePlan &p, const uint16_t *l, int64_t ld, const Params &par, int32_t *tokens,
+                       float *logprobs, int64_t M, int64_t V, hipStream_t stream) {
+    // Short rows are searched whole in one step, and one table is sooner cleared and read (V =
+    // 100, us: M = 100 12.4 instead of 13.2, M = 1000 32.1 instead of 34.4; V = 8000, M = 1000
+    // 38.2 and 36.7).
+    const bool quarters = V / 8 + 1 > kThreads / 2 && V / 8 + 1 <= 4 * kMaxQuarter;
+#define SVQ_ROW(WAY, MARK)                                                                                          \
+    hipLaunchKernelGGL((sample_row_kernel<WAY, MARK>), dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,    \
+                   tokens, logprobs, (int)V)
+    if (!p.mark) {
+        if (quarters) SVQ_ROW(kQuarters, false);
+        else SVQ_ROW(kWhole, false);
+        return hipGetLastError();
+    }
+    if (quarters) SVQ_ROW(kQuarters, true);
+    else SVQ_ROW(kWhole, true);
+#undef SVQ_ROW
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)std::min<int64_t>(M, 256)), dim3(kThreads), 0, stream, l, ld,
+                       par, tokens, logprobs, M, (int)V);
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_sample(const SamplePlan &p, const void *logits, int64_t ld, const float *u, const float *temperature,
                          const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                          float *logprobs, int64_t M, int64_t V, void *workspace, hipStream_t stream) {
     const Params par{u, temperature, top_p, min_p, top_k};
     const uint16_t *l = (const uint16_t *)logits;
     if (p.parts == 1) {
-        // Short rows are searched whole in one step, and one table is sooner cleared and read (V =
-        // 100, us: M = 100 12.4 instead of 13.2, M = 1000 32.1 instead of 34.4; V = 8000, M = 1000
-        // 38.2 and 36.7).
-        const bool quarters = V / 8 + 1 > kThreads / 2 && V / 8 + 1 <= 4 * kMaxQuarter;
-#define SVQ_ROW(WAY, MARK)                                                                                          \
-    hipLaunchKernelGGL((sample_row_kernel<WAY, MARK>), dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,    \
-                       tokens, logprobs, (int)V)
-        if (!p.mark) {
-            if (quarters) SVQ_ROW(kQuarters, false);
-            else SVQ_ROW(kWhole, false);
-            return hipGetLastError();
+        // a launch has fewer than 2^32 threads
+        constexpr int64_t kMost = (int64_t(1) << 31) / kThreads;
+        for (int64_t m = 0; m < M; m += kMost) {
+            auto from = [&](auto *q) { return q ? q + m : q; };
+            const Params at{from(u), from(temperature), from(top_p), from(min_p), from(top_k)};
+            const hipError_t e = launch_rows(p, l + m * ld, ld, at, tokens + m, from(logprobs), std::min(M - m, kMost), V, stream);
+            if (e != hipSuccess) return e;
         }
-        if (quarters) SVQ_ROW(kQuarters, true);
-        else SVQ_ROW(kWhole, true);
-#undef SVQ_ROW
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(sample_long_kernel, dim3((uint32_t)std::min<int64_t>(M, 256)), dim3(kThreads), 0, stream, l, ld,
-                           par, tokens, logprobs, M, (int)V);
-        return hipGetLastError();
+        return hipSuccess;
     }
     uint32_t *parts = (uint32_t *)ws_partials(workspace);
     hipLaunchKernelGGL(sample_count_kernel, dim3((uint32_t)(M * p.parts)), dim3(kThreads), 0, stream, l, ld, par, parts,
