@@ -531,6 +531,42 @@ AdapterPlan plan_adapter(int64_t M, int64_t N, int64_t K, int64_t R, int64_t slo
     return p;
 }
 
+namespace {
+
+// Both launches for blocks of rows that they take: the two are in stream order, so every
+// stretch of rows may use the same workspace.
+hipError_t launch_two(const AdapterPlan &p, const void *base, int64_t ld_base, const void *x, const void *a,
+                      const void *b, const int32_t *rows, const float *scales, void *out, int64_t ld_out, int64_t M,
+                      int64_t N, int64_t K, int R, int slots, void *workspace, hipStream_t stream) {
+    const int64_t row_blocks = (M + kBlockRows - 1) / kBlockRows;
+    Item *table = (Item *)ws_partials(workspace);
+    float *part = (float *)(table + row_blocks * p.items);
+    const dim3 down((uint32_t)(row_blocks * p.items * p.rank_chunks * p.range_blocks));
+#define SVQ_DOWN(RT)                                                                                                 \
+    hipLaunchKernelGGL((adapter_down_kernel<RT>), down, dim3(64 * kDownWaves), 0, stream, (const uint16_t *)x,       \
+                       (const uint16_t *)a, rows, table, part, M, (int)K, R, slots, p.rank_chunks, p.range_blocks,   \
+                       p.tiles_per_split)
+    if (p.rank_tiles == 1) SVQ_DOWN(1);
+    else if (p.rank_tiles == 2) SVQ_DOWN(2);
+    else SVQ_DOWN(4);
+#undef SVQ_DOWN
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const dim3 up((uint32_t)(row_blocks * p.items * p.col_blocks));
+#define SVQ_UP(NS)                                                                                                  \
+    hipLaunchKernelGGL((adapter_up_kernel<NS>), up, dim3(64 * kUpWaves), 0, stream, (const uint16_t *)base, part,   \
+                       (const uint16_t *)b, table, scales, (uint16_t *)out, M, (int)N, R, slots, ld_base, ld_out,    \
+                       p.col_blocks, p.splits)
+    if (R <= 32) SVQ_UP(1);
+    else if (R <= 64) SVQ_UP(2);
+    else if (R <= 128) SVQ_UP(4);
+    else SVQ_UP(8);
+#undef SVQ_UP
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld_base, const void *x, const void *a,
                               const void *b, const int32_t *rows, const float *scales, void *out, int64_t ld_out,
                               int64_t M, int64_t N, int64_t K, int R, int slots, void *workspace,
@@ -547,30 +583,17 @@ hipError_t launch_adapter_add(const AdapterPlan &p, const void *base, int64_t ld
 #undef SVQ_ONE
         return hipGetLastError();
     }
-    Item *table = (Item *)ws_partials(workspace);
-    float *part = (float *)(table + p.row_blocks * p.items);
-    const dim3 down((uint32_t)(p.row_blocks * p.items * p.rank_chunks * p.range_blocks));
-#define SVQ_DOWN(RT)                                                                                                 \
-    hipLaunchKernelGGL((adapter_down_kernel<RT>), down, dim3(64 * kDownWaves), 0, stream, (const uint16_t *)x,       \
-                       (const uint16_t *)a, rows, table, part, M, (int)K, R, slots, p.rank_chunks, p.range_blocks,   \
-                       p.tiles_per_split)
-    if (p.rank_tiles == 1) SVQ_DOWN(1);
-    else if (p.rank_tiles == 2) SVQ_DOWN(2);
-    else SVQ_DOWN(4);
-#undef SVQ_DOWN
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 up((uint32_t)(p.row_blocks * p.items * p.col_blocks));
-#define SVQ_UP(NS)                                                                                                  \
-    hipLaunchKernelGGL((adapter_up_kernel<NS>), up, dim3(64 * kUpWaves), 0, stream, (const uint16_t *)base, part,   \
-                       (const uint16_t *)b, table, scales, (uint16_t *)out, M, (int)N, R, slots, ld_base, ld_out,    \
-                       p.col_blocks, p.splits)
-    if (R <= 32) SVQ_UP(1);
-    else if (R <= 64) SVQ_UP(2);
-    else if (R <= 128) SVQ_UP(4);
-    else SVQ_UP(8);
-#undef SVQ_UP
-    return hipGetLastError();
+    // a launch has fewer than 2^32 threads: the first is kept to half of that, and the second is
+    // never as large (M N < 2^30)
+    const int64_t most = std::max<int64_t>(1, (int64_t(1) << 31) / (64 * kDownWaves) /
+                                                  ((int64_t)p.items * p.rank_chunks * p.range_blocks)) * kBlockRows;
+    for (int64_t m = 0; m < M; m += most) {
+        const hipError_t e = launch_two(p, (const uint16_t *)base + m * ld_base, ld_base, (const uint16_t *)x + m * K, a, b,
+                                        rows + m, scales, (uint16_t *)out + m * ld_out, ld_out, std::min(M - m, most), N,
+                                        K, R, slots, workspace, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace svq

@@ -106,3 +106,29 @@ def test_an_intermediate_next_to_the_largest_float(K, R):
     want = 2.0 ** 118 - 2.0 ** 108   # 10 bits: half a bf16 step off at most
     assert bool((got[2] == 0).all())
     assert bool(((got[[0, 1, 3]] - want).abs() <= 2.0 ** -8 * want).all())
+
+
+def test_more_items_than_one_launch_takes():
+    """2^21 rows, each of 256 consecutive ones on an adapter of its own, at rank 256: 2^23
+    workgroups of 512 threads are 2^32, which no launch may have.
+
+    Bound: t passes at most 128 + 8 roundings of one fp32 step (a tile of K, the waves), the
+    scale half a step, the second sum 3 * 256 + 2 terms, the output half a bf16 step."""
+    import spec_verify_amd as svq
+    _say("adapter 2^21 rows")
+    M, K, N, R, slots = (1 << 21) + 700, 128, 16, 256, 256
+    g = torch.Generator("cuda").manual_seed(3)
+    n = lambda *s, std=1.0: (torch.randn(*s, device="cuda", generator=g) * std).bfloat16()
+    base, x, a, b = n(M, N, std=3.0), n(M, K), n(slots, R, K, std=K ** -0.5), n(slots, N, R, std=R ** -0.5)
+    scales = torch.rand(slots, device="cuda", generator=g) + 0.5
+    rows = torch.arange(M, device="cuda", dtype=torch.int32) % slots
+    out = svq.adapter_add(base, x, a, b, rows, scales)
+    for s in range(slots):
+        xs, bs, sc = x[s::slots].double(), base[s::slots].double(), scales[s].double()
+        at, bt = a[s].double().t().contiguous(), b[s].double().t().contiguous()
+        t = xs @ at
+        t_err = 136 * 2.0 ** -23 * (xs.abs() @ at.abs()) + 2.0 ** -24 * t.abs()
+        want = bs + sc * (t @ bt)
+        bound = sc * (t_err @ bt.abs()) + 770 * 2.0 ** -23 * (bs.abs() + sc * ((t.abs() + t_err) @ bt.abs()))
+        bound = bound + 2.0 ** -8 * (want.abs() + bound)
+        assert bool(((out[s::slots].double() - want).abs() <= bound).all()), s
