@@ -720,18 +720,22 @@ __device__ __forceinline__ Drawn draw_way(Draw &sh, const Row &row, const RowPar
         if (waves && 63 - __builtin_clzll(waves) == wave) {  // every wave finds the same one
             const uint64_t mask = __ballot(c && within(ec, ew, head));
             const int ol = mask ? 63 - __builtin_clzll(mask) : 0, owner = wave * 64 + ol;
-            // its wave looks at its values, one a lane: the bins, then the items behind them
+            // its wave looks at its values, one a lane: the bins, then the items behind them.
+            // (What the owner has is read here, where every lane is on: within the choice below
+            // the owner may be off, and what it holds may be stale.)
             const uint32_t first = __builtin_amdgcn_readlane((int)ec, ol);
-            const double start = lane_value(ew, ol), r1 = lane_value(own.ratio, ol);
+            const double start = lane_value(ew, ol), r1 = lane_value(own.ratio, ol), w1 = lane_value(wf, ol);
             const int of = __builtin_amdgcn_readlane(f, ol);
+            const uint32_t bits0 = (uint32_t)__builtin_amdgcn_readlane((int)own.bits0, ol);
+            const int dir = __builtin_amdgcn_readlane(own.dir, ol);
             uint32_t k = 0, bits = 0;
             double v = 0.0;
             if (lane < kOwn) {
                 k = bin_at(owner, lane);
-                bits = __builtin_amdgcn_readlane((int)own.bits0, ol) + __builtin_amdgcn_readlane(own.dir, ol) * lane;
+                bits = bits0 + dir * lane;
                 const int d = max(lane - of, 0);
                 const double r2 = r1 * r1;
-                v = lane_value(wf, ol) * (d & 1 ? r1 : 1.0) * (d & 2 ? r2 : 1.0) * (d & 4 ? r2 * r2 : 1.0);
+                v = w1 * (d & 1 ? r1 : 1.0) * (d & 2 ? r2 : 1.0) * (d & 4 ? r2 * r2 : 1.0);
             } else if (!longway) {
                 const int i = lane - kOwn;
                 if (owner == kLastPositive && i < sides) {

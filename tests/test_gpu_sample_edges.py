@@ -50,3 +50,38 @@ def test_more_rows_than_one_launch_takes():
     want = torch.where(other, torch.log(w), 0.0) - torch.log1p(w)
     # half a step of fp32, and what two fp64 values differ
     assert bool(((logprobs.double() - want).abs() <= 2.0 ** -24 * want.abs() + 1e-12).all())
+
+
+def _every_bin(copies, keep):
+    """(logits, order): `copies` tokens of each of the first `keep` patterns of the magnitudes
+    from 2^-16 to 2^16, both signs, shuffled within each copy; order[i, c] is copy c of the i-th
+    largest value."""
+    rng = np.random.default_rng(copies)
+    mags = np.arange(111 << 7, (111 << 7) + 4096)
+    bits = np.concatenate([mags[::-1], mags | 0x8000])[:keep]   # descending
+    place = np.stack([rng.permutation(keep) + c * keep for c in range(copies)], 1)
+    row = np.empty(copies * keep, np.uint16)
+    row[place] = bits[:, None]
+    return torch.from_numpy(row.view(np.int16)).view(torch.bfloat16), place
+
+
+@pytest.mark.parametrize("copies,keep,M", [(1, 8192, 8192), (1, 4000, 250), (1, 8192, 100), (5, 8192, 48)])
+def test_every_bin_is_reached_by_every_seek(copies, keep, M):
+    """One row that holds every value with a bin; each position of its order in turn is the last
+    of top-k, the last of top-p and the draw. At T = 2^20 the weights are between 0.88 and 1, so
+    a position's share of the mass is far wider than the steps of fp32."""
+    import spec_verify_amd as svq
+    _say("sample every bin", copies, keep, M)
+    row, place = _every_bin(copies, keep)
+    l = row.cuda().repeat(M, 1)
+    v = np.sort(row.float().numpy().astype(np.float64))[::-1]
+    cum = np.cumsum(np.exp((v - v[0]) / 2 ** 20))
+    dev = lambda a, t=torch.float32: torch.tensor(a, dtype=t, device="cuda")
+    T, last = dev(np.full(M, 2.0 ** 20)), dev(np.full(M, 1 - 2.0 ** -24))
+    for i0 in range(0, keep, M):
+        i = np.minimum(np.arange(i0, i0 + M), keep - 1)
+        at, want = i * copies + i % copies, torch.from_numpy(place[i, i % copies]).int()
+        middle = dev((cum[at] - 0.5) / cum[-1])
+        assert torch.equal(svq.sample(l, middle, T)[0].cpu(), want), i0
+        assert torch.equal(svq.sample(l, last, T, top_k=dev(at + 1, torch.int32))[0].cpu(), want), i0
+        assert torch.equal(svq.sample(l, last, T, top_p=middle)[0].cpu(), want), i0
