@@ -1012,7 +1012,8 @@ __global__ __launch_bounds__(kThreads) void sample_long_kernel(const uint16_t *_
 // Workspace of one (row, part): header, then the occurring bins in descending order
 // (place in that order << 18 | count), then the smaller magnitudes.
 constexpr uint32_t kHeader = 8;
-constexpr uint32_t kPartWords = kHeader + kBins + kSideMax;
+constexpr uint32_t kPartWords = (kHeader + kBins + kSideMax + 31) / 32 * 32;  // whole lines of 128 bytes
+static_assert(kHeader == 8 && kPartWords % 4 == 0, "a header is two 16-byte vectors at 16-byte addresses");
 constexpr uint32_t kCountBits = 18;
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
 constexpr int64_t kMaxPartVectors = ((1 << kCountBits) - 16) / 8;  // a part's tokens fit the count
