@@ -375,7 +375,9 @@ size_t svq_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R, i
  *   scales   fp32 [slots]
  *   out      bf16 [M][ld_out], 16-byte aligned; its first N columns are written,
  *            the rest of each row is left as it was. May be base itself (same
- *            pointer, ld_out == ld_base); otherwise the two must not overlap.
+ *            pointer, ld_out == ld_base) or other columns of the same matrix
+ *            (ld_out == ld_base); otherwise the memory from the first to the last
+ *            element of the one must not overlap the other's.
  *   ld_base, ld_out >= N, multiples of 8: the columns of one projection inside a
  *            fused output are addressed by their first column and the fused width
  * Requires N % 16 == 0, K % 128 == 0, R % 8 == 0, R <= SVQ_MAX_ADAPTER_RANK.

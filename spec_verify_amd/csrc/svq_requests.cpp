@@ -38,6 +38,14 @@ int check_sample_shape(int64_t M, int64_t V) {
     return M > 0 && V > 0 && M <= kMaxDim && V <= kMaxDim ? SVQ_OK : SVQ_ERR_DIM;
 }
 
+// Whether N columns from `a` on and N columns from `b` on, of a matrix of 2-byte elements with
+// row stride ld that holds both, share none (both are 16-byte aligned).
+bool columns_apart(const void *a, const void *b, int64_t ld, int64_t N) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    const int64_t q = (int64_t)((pa < pb ? pb - pa : pa - pb) / 2 % (uintptr_t)ld);
+    return q >= N && q + N <= ld;
+}
+
 struct Span {
     const void *p;
     size_t bytes;
@@ -85,8 +93,11 @@ int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void
                         {rows, (size_t)M * 4},
                         {scales, (size_t)slots * 4}};
     if (any_overlap(outs, 2, ins, 5) || overlap(workspace, plan.workspace_bytes, base, base_bytes)) return SVQ_ERR_OVERLAP;
-    // in place is the same rows in the same places; anything else between base and out must be apart
-    if (!(out == base && ld_out == ld_base) && overlap(out, outs[0].bytes, base, base_bytes)) return SVQ_ERR_OVERLAP;
+    // in place is the same rows in the same places, or other columns of the same matrix; anything
+    // else between base and out must be apart
+    if (!(out == base && ld_out == ld_base) && !(ld_out == ld_base && columns_apart(base, out, ld_base, N)) &&
+        overlap(out, outs[0].bytes, base, base_bytes))
+        return SVQ_ERR_OVERLAP;
     return launch_adapter_add(plan, base, ld_base, x, a, b, rows, scales, out, ld_out, M, N, K, R, slots, workspace,
                               (hipStream_t)stream) == hipSuccess
                ? SVQ_OK

@@ -132,3 +132,26 @@ def test_more_items_than_one_launch_takes():
         bound = sc * (t_err @ bt.abs()) + 770 * 2.0 ** -23 * (bs.abs() + sc * ((t.abs() + t_err) @ bt.abs()))
         bound = bound + 2.0 ** -8 * (want.abs() + bound)
         assert bool(((out[s::slots].double() - want).abs() <= bound).all()), s
+
+
+@pytest.mark.parametrize("K", [512, 5120])
+@pytest.mark.parametrize("width,first,second", [(192, 0, 96), (192, 96, 0), (320, 200, 8), (320, 0, 224)])
+def test_from_one_column_slice_into_another(K, width, first, second):
+    """base and out are different columns of one matrix: their rows alternate in memory and
+    share no element."""
+    import spec_verify_amd as svq
+    _say("adapter slice to slice", K, width, first, second)
+    g = torch.Generator("cuda").manual_seed(K)
+    M, N, R, slots = 21, 96, 16, 4
+    n = lambda *s, std=1.0: (torch.randn(*s, device="cuda", generator=g) * std).bfloat16()
+    base, x, a, b = n(M, N, std=3.0), n(M, K), n(slots, R, K, std=K ** -0.5), n(slots, N, R, std=R ** -0.5)
+    rows = torch.randint(-1, slots, (M,), device="cuda", generator=g, dtype=torch.int32)
+    scales = torch.rand(slots, device="cuda", generator=g) + 0.5
+    plain = svq.adapter_add(base, x, a, b, rows, scales)
+    wide = torch.full((M, width), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, first:first + N] = base
+    svq.adapter_add(wide[:, first:first + N], x, a, b, rows, scales, out=wide[:, second:second + N])
+    assert torch.equal(wide[:, second:second + N], plain)
+    assert torch.equal(wide[:, first:first + N], base)
+    wide[:, first:first + N] = wide[:, second:second + N] = 7.0
+    assert bool((wide == 7.0).all())
