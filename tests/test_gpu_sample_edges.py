@@ -85,3 +85,27 @@ def test_every_bin_is_reached_by_every_seek(copies, keep, M):
         assert torch.equal(svq.sample(l, middle, T)[0].cpu(), want), i0
         assert torch.equal(svq.sample(l, last, T, top_k=dev(at + 1, torch.int32))[0].cpu(), want), i0
         assert torch.equal(svq.sample(l, last, T, top_p=middle)[0].cpu(), want), i0
+
+
+@pytest.mark.parametrize("M,V", [(1, 248320), (7, 50021), (51, 248320)])
+def test_a_workspace_need_not_be_cleared(M, V):
+    """The caller's workspace, exactly as large as it has to be, full of anything, used by one
+    call after another; its neighbours stay as they were."""
+    import spec_verify_amd as svq
+    _say("sample workspace", M, V)
+    g = torch.Generator("cuda").manual_seed(V + M)
+    l = (torch.randn(M, V, device="cuda", generator=g) * 2.2).bfloat16()
+    l[M - 1, ::3] = -1e9
+    u = torch.rand(M, device="cuda", generator=g)
+    k = torch.randint(0, 90, (M,), device="cuda", generator=g, dtype=torch.int32)
+    want = [svq.sample(l, u), svq.sample(l, u, top_k=k)]
+    n = svq.sample_workspace_bytes(M, V)
+    assert n > 0
+    memory = torch.empty(n + 512, dtype=torch.uint8, device="cuda")
+    for fill in (0, 0xFF, 0x7F):
+        memory.fill_(fill)
+        ws = memory[256:256 + n]
+        for w, kw in zip(want, ({}, dict(top_k=k))):
+            got = svq.sample(l, u, workspace=ws, **kw)
+            assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+        assert bool((memory[:256] == fill).all()) and bool((memory[256 + n:] == fill).all())
