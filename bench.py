@@ -13,19 +13,21 @@ exactly `--steps` decode steps for the headline) after untimed warm-up, timed
 with HIP events on the replay stream. Parity against the oracle is checked on
 the first and last weight copies of every workload before and after timing.
 
-Also reported (stderr table and the JSON line's "workloads" list): per-kernel
-time, GB/s, TFLOP/s and roofline fraction for every named workload (decode,
-M=3/5 verify chunks, M=128 batched verify, MXFP8 at M=1/5/128, the vocabulary
-heads, G=32/64 variants), each beside a read-only stream probe of the same bytes
-in the kernel's own launch shape and in the best of a fixed sweep of shapes
-("probe"), a stream probe of >1 GiB ("chip_stream"), the run record (versions,
-device, host CPU, input SHA-256 digests), the CPU oracle on every workload
-(``cpu_oracle``, bounded column samples scaled to the full width) and on whole
-decode steps (``cpu_baseline``), the fused K/V/Q and gate/up projections against
-the same projections launched one by one (``fusion``), and the setup-time steps
-(``quantizer``, ``ct_ingest``, ``mxfp8_quantizer``).
+Also reported (stderr table; whole rows in the ``--details`` file, times and
+rates in the JSON line's "workloads"): per-kernel time, GB/s, TFLOP/s and
+roofline fraction for every named workload (decode, M=3/5 verify chunks, M=128
+batched verify, MXFP8 at M=1/5/128, the vocabulary heads, G=32/64 variants),
+each beside a read-only stream probe of the same bytes in the kernel's own
+launch shape and in the best of a fixed sweep of shapes ("probe"), a stream
+probe of >1 GiB ("chip_stream"), the run record (versions, device, host CPU,
+input SHA-256 digests), the CPU oracle on every workload (``cpu_oracle`` of the
+details, bounded column samples scaled to the full width) and on whole decode
+steps (``cpu_baseline``), the fused K/V/Q and gate/up projections against the
+same projections launched one by one (``fusion``), and the setup-time steps
+(``quantizer``, ``ct_ingest``, ``mxfp8_quantizer``). The JSON line itself stays
+short: who keeps only the last few kilobytes of the output still has it whole.
 
-    python bench.py [--steps K] [--warmup W] [--gpus 1] [--quick] [--no-cpu]
+    python bench.py [--steps K] [--warmup W] [--gpus 1] [--quick] [--no-cpu] [--details FILE]
     python bench.py --only decode_n6144,mxfp8_m128   # a few workloads, for profiling runs
     python bench.py --copy-probe    # a plain 1 GiB device copy, to calibrate HBM counters
 """
@@ -719,12 +721,25 @@ def copy_probe(nbytes=1 << 30, reps=5):
         f"{2 * nbytes / dt / 1e9:.1f} GB/s")
 
 
+def printed_line(line):
+    """The record as it is printed: of each workload its time and rates alone, the chip's
+    ceilings without their sweeps, and no rows of the CPU oracle (the table on stderr has both)."""
+    short = {k: v for k, v in line.items() if k != "cpu_oracle"}
+    short["workloads"] = {r["workload"]: {k: r[k] for k in ("us", "GBps", "TFLOPs")} for r in line["workloads"]}
+    if line["chip_stream"]:
+        short["chip_stream"] = {k: v for k, v in line["chip_stream"].items() if k != "shapes"}
+    return short
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=300)
     ap.add_argument("--warmup", type=int, default=30)
     ap.add_argument("--quick", action="store_true", help="decode step only, no per-workload table")
+    ap.add_argument("--details", metavar="FILE",
+                    help="also write everything measured (each workload's trials, launch shape and probes, the CPU "
+                         "oracle's rows) to this file, as JSON")
     ap.add_argument("--no-cpu", action="store_true", help="skip the CPU oracle legs")
     ap.add_argument("--no-probe", action="store_true", help="skip the stream probes")
     ap.add_argument("--only", default="",
@@ -896,7 +911,10 @@ def main():
         "ct_ingest": ct,
         "mxfp8_quantizer": mxq,
     }
-    print(json.dumps(line), flush=True)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(line, f)
+    print(json.dumps(printed_line(line)), flush=True)
 
 
 # sources the dominant kernel is built from: traffic counters taken on other
