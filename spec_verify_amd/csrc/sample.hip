@@ -19,7 +19,10 @@
 // Values are binned by their bf16 pattern: magnitudes in [2^-16, 2^16) of either sign are
 // 8192 bins, 8 consecutive ones per thread. A binade's patterns are equally far apart, so
 // its weights are a geometric series: 32 ratios and 64 largest weights, one exponential
-// each by one wave, give all 8192 in multiplications (at most 134 roundings of 2^-53 each).
+// each by one wave, give all 8192 in multiplications. A weight's relative error: at most 134
+// multiplications round (2^-53 each); its ratio enters up to 127 times, and with it the
+// exponential's own error (2^-52); the exponents' roundings add 2^-51 of the exponent, which is
+// below 37 where a weight is above 1e-16 of the largest. All together less than 6e-14.
 // Zero, up to kSideMax smaller magnitudes (a logit or two in a vocabulary) and one pattern
 // below -2^16 (a mask value) are items of their own. Any other row is counted the long
 // way: eight windows of 8192 patterns, one scan of the row per window and step.
@@ -1299,9 +1302,9 @@ namespace {
 // A workgroup per row, of rows that one launch takes.
 hipError_t launch_rows(const SamplePlan &p, const uint16_t *l, int64_t ld, const Params &par, int32_t *tokens,
                        float *logprobs, int64_t M, int64_t V, hipStream_t stream) {
-    // Short rows are searched whole in one step, and one table is sooner cleared and read (V =
-    // 100, us: M = 100 12.4 instead of 13.2, M = 1000 32.1 instead of 34.4; V = 8000, M = 1000
-    // 38.2 and 36.7).
+    // One table is sooner cleared and read, two leave a quarter of the row to search. They meet
+    // between 4000 and 6000 tokens (M = 1000, us, one / two: V = 100 32.1 / 34.3, 3000 33.6 / 34.5,
+    // 4200 35.1 / 35.3, 8000 37.1 / 36.3) and stay within 2% of each other up to 32000.
     const bool quarters = V / 8 + 1 > kThreads / 2 && V / 8 + 1 <= 4 * kMaxQuarter;
 #define SVQ_ROW(WAY, MARK)                                                                                          \
     hipLaunchKernelGGL((sample_row_kernel<WAY, MARK>), dim3((uint32_t)M), dim3(kThreads), 0, stream, l, ld, par,    \
