@@ -449,6 +449,139 @@ int svq_sample(const void *logits, int64_t ld, const float *u, const float *temp
 int svq_accept_drafts(const int32_t *tokens, const int32_t *inputs, const int32_t *starts, int32_t *accepted,
                       int32_t *next, int32_t *committed, int64_t M, int64_t S, void *stream);
 
+/* ---- a tree of drafted tokens over a cache ---------------------------------------- */
+
+/*
+ * A verify chunk may branch: the rows of a sequence are the nodes of a tree. Its first
+ * row is the root (the last committed token) and every other row's input is a draft
+ * that follows its parent. The operators below share these arguments:
+ *   starts   int32 [S + 1], ascending, in [0, M] (values outside are clamped to it):
+ *            sequence s owns rows starts[s] .. starts[s+1] - 1; it may be empty
+ *   parents  int32 [M]: the parent of each row, counted from the sequence's first row
+ *            and smaller than the row's own number; anything else is no parent. NULL
+ *            (where allowed): a chain, every row's parent is the row before it
+ *   lengths  int32 [S]: committed tokens before the sequence's first row
+ * The path of a row is its ancestors and itself; its depth is the number of ancestors,
+ * its position lengths[s] + depth.
+ */
+
+/* Types of cached keys and values. */
+#define SVQ_CACHE_BF16 0
+#define SVQ_CACHE_E4M3 1 /* OCP E4M3FN codes */
+
+/* Keys and values of committed tokens, in pages that sequences hold by table. */
+typedef struct svq_kv_cache {
+    const void *k, *v;     /* token t, head h of page p at element
+                              p*strides[0] + t*strides[1] + h*strides[2]; D contiguous
+                              elements, 16-byte aligned (pointers and strides) */
+    int64_t k_strides[3];  /* page, token, head; in elements */
+    int64_t v_strides[3];
+    int64_t pages;         /* pages in the pool; with none k and v may be NULL */
+    int32_t page_size;     /* tokens in a page, 1 .. 2^20 */
+    int32_t type;          /* SVQ_CACHE_* */
+    const float *k_scale;  /* E4M3: fp32 [KVH], a cached value is code * scale; NULL for 1. */
+    const float *v_scale;  /* BF16: both NULL */
+    const int32_t *page_table; /* int32 [S][ld_table], the first max_pages of each row: the
+                              pages of a sequence in order. Tokens of an entry outside
+                              [0, pages) are not seen */
+    int64_t ld_table;
+    int32_t max_pages;     /* with none page_table may be NULL */
+    const int32_t *lengths; /* int32 [S], clamped to [0, max_pages * page_size] */
+} svq_kv_cache;
+
+/* Workspace bytes needed by svq_tree_attention (never 0); (size_t)-1 if the arguments
+ * are invalid. */
+size_t svq_tree_attention_workspace_bytes(int64_t M, int64_t S, int32_t H, int32_t KVH, int32_t D);
+
+/*
+ * Attention of every row of a chunk to its sequence's cache and to its own path:
+ *     out[m][h] = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q[m][h] . k_j)
+ * over the tokens j that row m sees, heads h of group h / (H / KVH) sharing one key and
+ * value head. A row at position p sees of the cache and of its path the tokens at
+ * positions > p - window and those < sinks; window <= 0 is no limit. The chunk's own
+ * keys and values are rows beside q, not in the cache: what is accepted is written to
+ * the cache afterwards. A score of -inf has weight zero; a row that sees nothing, or
+ * only such scores, is zero. Rows outside every sequence are left as they were. What a
+ * row does not see, infinities and NaN too, does not change its result.
+ * Scores, weights' sums and products are fp32; weights enter the second product as bf16;
+ * out is rounded to bf16 (nearest even).
+ *   q        bf16 [M][ld_q], the first H*D of each row: H heads of D elements
+ *   k, v     bf16 [M][ld_k], [M][ld_v], the first KVH*D of each row
+ *   cache    host struct, read during the call only
+ *   starts, parents (or NULL): above
+ *   out      bf16 [M][ld_out], the first H*D of each row are written
+ *   q, k, v, out 16-byte aligned, their row strides multiples of 8 and at least the
+ *   columns used. D is 64, 128 or 256, H a multiple of KVH, H <= 65536.
+ *   workspace  at least svq_tree_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ *              not cleared; as for svq_adapter_add.
+ * out and the workspace must not overlap any input or each other.
+ */
+int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                       const svq_kv_cache *cache, const int32_t *starts, const int32_t *parents, float scale,
+                       int32_t window, int32_t sinks, void *out, int64_t ld_out, int64_t M, int64_t S, int32_t H,
+                       int32_t KVH, int32_t D, void *workspace, size_t workspace_bytes, void *stream);
+
+/* What svq_adjust_logits changes; a NULL pointer leaves its part out. */
+typedef struct svq_adjustments {
+    const int32_t *history;        /* int32 [S][ld_history]: committed tokens before a chunk */
+    int64_t ld_history;
+    int32_t max_history;           /* lengths are clamped to [0, max_history] */
+    const int32_t *lengths;        /* int32 [S] */
+    const int32_t *prompt_lengths; /* int32 [S]: that many of them are the prompt's; NULL for 0 */
+    const int32_t *inputs;         /* int32 [M]: the input of each row */
+    const int32_t *parents;        /* int32 [M], or NULL for chains */
+    const float *repetition;       /* fp32 [S], positive; NULL for 1 */
+    const float *presence;         /* fp32 [S]; NULL for 0 */
+    const float *frequency;        /* fp32 [S]; NULL for 0 */
+    const int32_t *bias_starts;    /* int32 [S + 1], ascending, clamped to [0, biases] */
+    const int32_t *bias_tokens;    /* int32 [biases] */
+    const float *bias_values;      /* fp32 [biases] */
+    int64_t biases;
+    const int32_t *allowed;        /* int32 [masks][ld_allowed]: bit v % 32 of word v / 32 is 1 if
+                                      token v may follow */
+    int64_t ld_allowed, masks;
+    const int32_t *mask_rows;      /* int32 [M]: the mask of each row; outside [0, masks): none */
+} svq_adjustments;
+
+/*
+ * Logits as the sampler takes them, from those of the vocabulary head, by what stands
+ * before each row: the sequence's history and the inputs of the row's path. For token v
+ * of row m of sequence s, with c its number of occurrences in the history after the
+ * prompt and on the path:
+ *     x = logit;  if v occurs in the history or on the path: x = x > 0 ? x / r : x * r
+ *     x = x - frequency * c - (c > 0 ? presence : 0)
+ *     x = x + the biases of v in s, in their order
+ *     x = -inf if the row's mask has v's bit clear
+ * in fp32, rounded to bf16 (nearest even) once; r is applied as a product with r or with
+ * 1 / r, rounded to fp32. A logit that nothing applies to keeps its bits. Tokens outside
+ * [0, V) are passed over. Rows outside every sequence are left as they were.
+ *   logits   bf16 [M][ld], the first V of each row; 2-byte aligned
+ *   out      bf16 [M][ld_out]; may be logits itself (same pointer and stride), and must
+ *            otherwise not overlap any input
+ */
+int svq_adjust_logits(const void *logits, int64_t ld, const int32_t *starts, const svq_adjustments *adjustments,
+                      void *out, int64_t ld_out, int64_t M, int64_t S, int64_t V, void *stream);
+
+/*
+ * Acceptance along a tree (svq_accept_drafts for chunks that branch): from the
+ * sequence's first row on, while a child's input is the token sampled at the current
+ * node, the first such child (the lowest row) is accepted and becomes the current node.
+ *   tokens, inputs  int32 [M]: the sample and the input of each row; a negative token
+ *                   accepts nothing
+ *   parents, starts as above
+ *   accepted, next  int32 [S]: the number n of accepted drafts and the token sampled at
+ *                   the last of them; an empty sequence gets 0 and -1
+ *   committed       int32 [M]: the accepted drafts and then next at the first n + 1 rows
+ *                   of each sequence, -1 elsewhere
+ *   path            int32 [M]: at the same places the nodes whose samples these are,
+ *                   counted from the sequence's first row (0 first), -1 elsewhere: the
+ *                   rows whose keys and values belong into the cache
+ * Outputs must not overlap the inputs or each other.
+ */
+int svq_accept_tree(const int32_t *tokens, const int32_t *inputs, const int32_t *parents, const int32_t *starts,
+                    int32_t *accepted, int32_t *next, int32_t *committed, int32_t *path, int64_t M, int64_t S,
+                    void *stream);
+
 /* ---- format-generic queries ---------------------------------------------------- */
 
 /* Workspace bytes the GEMM of `op` (an svq_op) needs with its automatic kernel

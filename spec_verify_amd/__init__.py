@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -25,7 +26,8 @@ __all__ = [
     "fuse_projections", "fuse_or_keep", "ct_to_gptq", "MAX_FUSED_PARTS", "mxfp8_quantize",
     "OP_W4A16", "OP_MXFP8", "OP_W8A16", "workspace_bytes", "kernel_name",
     "launch_geometry", "stream_probe", "adapter_add", "adapter_workspace_bytes", "sample",
-    "sample_workspace_bytes", "accept_drafts", "MAX_ADAPTER_RANK",
+    "sample_workspace_bytes", "accept_drafts", "MAX_ADAPTER_RANK", "tree_attention",
+    "tree_attention_workspace_bytes", "adjust_logits", "accept_tree",
 ]
 
 KERNEL_AUTO, KERNEL_DOT2, KERNEL_MFMA_SKINNY, KERNEL_MFMA_WIDE = 0, 1, 2, 3
@@ -42,7 +44,8 @@ EXPORTED_SYMBOLS = (
     "svq_fuse_projections", "svq_ct_to_gptq", "svq_mxfp8_quantize", "svq_workspace_bytes",
     "svq_kernel_name", "svq_launch_geometry", "svq_stream_probe", "svq_mfma_probe", "svq_mxfp8_repack",
     "svq_w4a16_gemm_noalloc", "svq_adapter_workspace_bytes", "svq_adapter_add",
-    "svq_sample_workspace_bytes", "svq_sample", "svq_accept_drafts",
+    "svq_sample_workspace_bytes", "svq_sample", "svq_accept_drafts", "svq_tree_attention_workspace_bytes",
+    "svq_tree_attention", "svq_adjust_logits", "svq_accept_tree",
 )
 
 OP_W4A16, OP_MXFP8, OP_W8A16 = 1, 2, 3
@@ -137,6 +140,15 @@ def lib():
         L.svq_sample.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _p, _sz, _p]
         L.svq_accept_drafts.restype = ctypes.c_int
         L.svq_accept_drafts.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _p]
+        L.svq_tree_attention_workspace_bytes.restype = _sz
+        L.svq_tree_attention_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32, _i32]
+        L.svq_tree_attention.restype = ctypes.c_int
+        L.svq_tree_attention.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, ctypes.c_float, _i32, _i32, _p, _i64,
+                                         _i64, _i64, _i32, _i32, _i32, _p, _sz, _p]
+        L.svq_adjust_logits.restype = ctypes.c_int
+        L.svq_adjust_logits.argtypes = [_p, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _p]
+        L.svq_accept_tree.restype = ctypes.c_int
+        L.svq_accept_tree.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _p]
         _lib = L
         return L
 
@@ -542,6 +554,7 @@ class _Kinds:
         self.uint8, self.bfloat16, self.float32, self.int32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
         self.bf16 = (torch.bfloat16, torch.int16, torch.uint16)
         self.f32, self.i32 = (torch.float32,), (torch.int32,)
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
         # the stream's handle alone where PyTorch offers it: a Stream object takes 2.7 us to make
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -729,3 +742,214 @@ def accept_drafts(tokens, inputs, starts):
     _enqueue(dev, "svq_accept_drafts", lib().svq_accept_drafts, t_ptr, i_ptr, s_ptr, accepted.data_ptr(),
              following.data_ptr(), committed.data_ptr(), M, S)
     return accepted, following, committed
+
+
+# ---- a tree of drafted tokens over a cache --------------------------------------------
+# svq_kv_cache and svq_adjustments, field by field
+_CACHE = struct.Struct("@PPqqqqqqqiiPPPqiP")
+_ADJUSTMENTS = struct.Struct("@PqiPPPPPPPPPPqPqqP")
+
+
+def _heads_of(t, name, dtypes, heads, dim, device):
+    """(address, row stride) of a tensor [rows, heads, dim] whose rows are contiguous and apart."""
+    if not isinstance(t, _kinds().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    rows = t.shape[0]
+    if t.dim() != 3 or t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must have shape {('M', heads, dim)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    by_row, by_head, by_elem = t.stride()
+    if by_elem != 1 or (heads > 1 and by_head != dim):
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return t.data_ptr(), heads * dim
+    if by_row < heads * dim:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.data_ptr(), by_row
+
+
+def _table_of(t, name, dtypes, rows, device):
+    """(address, row stride, columns) of a matrix of `rows` rows (any number for None), which may share memory."""
+    if not isinstance(t, _kinds().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape {(rows, 'any')}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    rows, cols = t.shape
+    by_row, by_col = t.stride()
+    if cols > 1 and by_col != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows > 1 and by_row < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.data_ptr(), by_row if rows > 1 else cols, cols
+
+
+def tree_attention_workspace_bytes(M, S, H, KVH, D) -> int:
+    v = lib().svq_tree_attention_workspace_bytes(M, S, H, KVH, D)
+    if v == ctypes.c_size_t(-1).value:
+        raise SvqError(2, "svq_tree_attention_workspace_bytes")
+    return v
+
+
+def tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, starts, parents=None, scale=None, window=0, sinks=0,
+                   k_scale=None, v_scale=None, out=None, workspace=None):
+    """Attention of every row of a verify chunk to its sequence's paged cache and to its own path.
+
+    q [M, H, D] and the chunk's k, v [M, KVH, D], bf16, may be column slices of a fused
+    projection's output. k_cache, v_cache [pages, page_size, KVH, D], bf16 or float8_e4m3fn
+    (or its codes in uint8) with k_scale, v_scale float32 [KVH] or None, in any order of the
+    first three dimensions; page_table int32 [S, max_pages] and lengths int32 [S]: the pages and the
+    number of each sequence's cached tokens. starts int32 [S + 1]: sequence s owns rows
+    starts[s] .. starts[s + 1] - 1; parents int32 [M]: each row's parent, counted from its
+    sequence's first row, or None for a chain. scale: 1 / sqrt(D) if None. window > 0: only the
+    `window` last positions, the row's own among them, and the first `sinks` are seen. Returns
+    [M, H, D]; rows outside every sequence are not written.
+    """
+    kd = _kinds()
+    bf16, i32 = kd.bf16, kd.i32
+    if not isinstance(q, kd.Tensor) or q.dim() != 3 or not isinstance(k, kd.Tensor) or k.dim() != 3:
+        raise ValueError("q must be [M, H, D] and k [M, KVH, D]")
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError(f"q must be a device tensor, got {dev}")
+    M, H, D = q.shape
+    KVH = k.shape[1]
+    q_ptr, ld_q = _heads_of(q, "q", bf16, H, D, dev)
+    k_ptr, ld_k = _heads_of(k, "k", bf16, KVH, D, dev)
+    v_ptr, ld_v = _heads_of(v, "v", bf16, KVH, D, dev)
+    if k.shape[0] != M or v.shape[0] != M:
+        raise ValueError(f"k and v must have {M} rows")
+    e4m3 = k_cache.dtype in kd.e4m3
+    kinds = kd.e4m3 if e4m3 else bf16
+    if k_cache.dim() != 4 or k_cache.shape[2:] != (KVH, D) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must have shape {('pages', 'page_size', KVH, D)}, got "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype not in kinds:
+            raise TypeError(f"{name} must be {' or '.join(str(d) for d in kinds)}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must have contiguous heads")
+    pages, page_size = k_cache.shape[:2]
+    S = lengths.shape[0]
+    table_ptr, ld_table, max_pages = _table_of(page_table, "page_table", i32, S, dev)
+    lengths_ptr = _ptr(lengths, "lengths", i32, (S,), dev)
+    starts_ptr = _ptr(starts, "starts", i32, (S + 1,), dev)
+    parents_ptr = None if parents is None else _ptr(parents, "parents", i32, (M,), dev)
+    per_head = (KVH,)
+    ks_ptr = 0 if k_scale is None else _ptr(k_scale, "k_scale", kd.f32, per_head, dev)
+    vs_ptr = 0 if v_scale is None else _ptr(v_scale, "v_scale", kd.f32, per_head, dev)
+    if out is None:
+        out = kd.empty((M, H, D), dtype=kd.bfloat16, device=dev)
+        out_ptr, ld_out = out.data_ptr(), H * D
+    else:
+        out_ptr, ld_out = _heads_of(out, "out", bf16, H, D, dev)
+        if out.shape[0] != M:
+            raise ValueError(f"out must have {M} rows")
+    if not max(pages, page_size, max_pages) < 1 << 31:
+        raise ValueError("the cache has too many pages")
+    cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3], *v_cache.stride()[:3], pages,
+                        page_size, 1 if e4m3 else 0, ks_ptr, vs_ptr, table_ptr, ld_table, max_pages, lengths_ptr)
+    keep, ws, ws_bytes = _scratch(tree_attention_workspace_bytes, (M, S, H, KVH, D), workspace, dev)
+    _enqueue(dev, "svq_tree_attention", lib().svq_tree_attention, q_ptr, ld_q, k_ptr, ld_k, v_ptr, ld_v, cache, starts_ptr,
+             parents_ptr, D ** -0.5 if scale is None else scale, window, sinks, out_ptr, ld_out, M, S, H, KVH, D, ws,
+             ws_bytes)
+    return out
+
+
+def adjust_logits(logits, history, lengths, inputs, starts, parents=None, prompt_lengths=None, repetition=None,
+                  presence=None, frequency=None, bias=None, allowed=None, mask_rows=None, out=None):
+    """Logits [M, V] bf16 as the sampler takes them, by what stands before each row.
+
+    history int32 [S, max_history], its first lengths[s] tokens committed before sequence s's
+    rows (the first prompt_lengths[s] of them its prompt); inputs int32 [M]: the input of each row;
+    starts and parents as for tree_attention. A token that occurs in the history or on a row's path is
+    divided (if positive) or multiplied by repetition[s]; frequency[s] per occurrence after
+    the prompt and presence[s] once are subtracted; bias = (starts int32 [S + 1], tokens int32,
+    values float32) adds values to the tokens of each sequence; allowed int32 [masks, words]
+    holds a bit per token and mask_rows int32 [M] each row's mask (outside [0, masks):
+    none), a clear bit makes -inf. out may be logits itself; logits and out may be column
+    slices of wider matrices. Rows outside every sequence are not written.
+    """
+    kd = _kinds()
+    i32, f32 = kd.i32, kd.f32
+    ptr, ld = _rows_of(logits, "logits", kd.bf16)
+    dev = logits.device
+    M, V = logits.shape
+    S = lengths.shape[0]
+    per_seq, per_row = (S,), (M,)
+    history_ptr, ld_history, max_history = _table_of(history, "history", i32, S, dev)
+    lengths_ptr = _ptr(lengths, "lengths", i32, per_seq, dev)
+    inputs_ptr = _ptr(inputs, "inputs", i32, per_row, dev)
+    starts_ptr = _ptr(starts, "starts", i32, (S + 1,), dev)
+    parents_ptr = 0 if parents is None else _ptr(parents, "parents", i32, per_row, dev)
+    prompt_ptr = 0 if prompt_lengths is None else _ptr(prompt_lengths, "prompt_lengths", i32, per_seq, dev)
+    rep_ptr = 0 if repetition is None else _ptr(repetition, "repetition", f32, per_seq, dev)
+    pres_ptr = 0 if presence is None else _ptr(presence, "presence", f32, per_seq, dev)
+    freq_ptr = 0 if frequency is None else _ptr(frequency, "frequency", f32, per_seq, dev)
+    bs_ptr = bt_ptr = bv_ptr = biases = 0
+    if bias is not None:
+        first, tokens, values = bias
+        biases = tokens.shape[0]
+        bs_ptr = _ptr(first, "bias starts", i32, (S + 1,), dev)
+        bt_ptr = _ptr(tokens, "bias tokens", i32, (biases,), dev)
+        bv_ptr = _ptr(values, "bias values", f32, (biases,), dev)
+    al_ptr = ld_allowed = masks = mr_ptr = 0
+    if allowed is not None or mask_rows is not None:
+        if allowed is None or mask_rows is None:
+            raise ValueError("allowed and mask_rows come together")
+        al_ptr, ld_allowed, words = _table_of(allowed, "allowed", i32, None, dev)
+        masks = allowed.shape[0]
+        if words < (V + 31) // 32:
+            raise ValueError(f"allowed must have {(V + 31) // 32} words a row, got {words}")
+        mr_ptr = _ptr(mask_rows, "mask_rows", i32, per_row, dev)
+    if out is None:
+        out = kd.empty((M, V), dtype=kd.bfloat16, device=dev)
+        out_ptr, ld_out = out.data_ptr(), V
+    else:
+        out_ptr, ld_out = _rows_of(out, "out", kd.bf16)
+        if out.shape != (M, V) or out.device != dev:
+            raise ValueError(f"out must have shape {(M, V)} on {dev}")
+    if not max_history < 1 << 31:
+        raise ValueError("the history is too long")
+    adjustments = _ADJUSTMENTS.pack(history_ptr, ld_history, max_history, lengths_ptr, prompt_ptr, inputs_ptr, parents_ptr,
+                                    rep_ptr, pres_ptr, freq_ptr, bs_ptr, bt_ptr, bv_ptr, biases, al_ptr, ld_allowed,
+                                    masks, mr_ptr)
+    _enqueue(dev, "svq_adjust_logits", lib().svq_adjust_logits, ptr, ld, starts_ptr, adjustments, out_ptr, ld_out, M, S,
+             V)
+    return out
+
+
+def accept_tree(tokens, inputs, parents, starts):
+    """Accepts drafted tokens of trees against the main model's samples.
+
+    tokens, inputs int32 [M]: the sample and the input of each row; parents int32 [M] and
+    starts int32 [S + 1] as for tree_attention. Returns (accepted [S], next [S], committed [M], path
+    [M]), int32: as accept_drafts, and the accepted nodes in place (the first row, 0, first),
+    -1 elsewhere.
+    """
+    kd = _kinds()
+    i32 = kd.i32
+    if tokens.dim() != 1 or starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("tokens must be [M] and starts [S + 1] with S >= 1")
+    dev, M, S = tokens.device, tokens.shape[0], starts.shape[0] - 1
+    t_ptr = _ptr(tokens, "tokens", i32, (M,), dev)
+    i_ptr = _ptr(inputs, "inputs", i32, (M,), dev)
+    p_ptr = _ptr(parents, "parents", i32, (M,), dev)
+    s_ptr = _ptr(starts, "starts", i32, (S + 1,), dev)
+    if not tokens.is_cuda:
+        raise ValueError(f"tokens must be a device tensor, got {dev}")
+    accepted = kd.empty(S, dtype=kd.int32, device=dev)
+    following = kd.empty(S, dtype=kd.int32, device=dev)
+    committed = kd.empty(M, dtype=kd.int32, device=dev)
+    path = kd.empty(M, dtype=kd.int32, device=dev)
+    _enqueue(dev, "svq_accept_tree", lib().svq_accept_tree, t_ptr, i_ptr, p_ptr, s_ptr, accepted.data_ptr(),
+             following.data_ptr(), committed.data_ptr(), path.data_ptr(), M, S)
+    return accepted, following, committed, path
