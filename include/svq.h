@@ -474,7 +474,8 @@ typedef struct svq_kv_cache {
     const void *k, *v;     /* token t, head h of page p at element
                               p*strides[0] + t*strides[1] + h*strides[2]; D contiguous
                               elements, 16-byte aligned (pointers and strides) */
-    int64_t k_strides[3];  /* page, token, head; in elements */
+    int64_t k_strides[3];  /* page, token, head; in elements. Pages and tokens lie less than
+                              4 GiB apart (if there are several) */
     int64_t v_strides[3];
     int64_t pages;         /* pages in the pool; with none k and v may be NULL */
     int32_t page_size;     /* tokens in a page, 1 .. 2^20 */

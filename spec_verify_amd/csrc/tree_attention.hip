@@ -22,7 +22,9 @@
 // different lengths keep the chip equally busy. A block of rows that ends up in several
 // workgroups is joined by a second launch from its parts' maxima, sums and fp32 values.
 #include <algorithm>
+#include <type_traits>
 
+#include "svq_dma.h"
 #include "svq_tree.h"
 
 namespace svq {
@@ -31,12 +33,15 @@ namespace {
 
 constexpr int kTile = 64;          // tokens in a tile
 constexpr int kStaged = 1024;      // parents kept in LDS; of wider trees the rest is read where it lies
+constexpr int kEntries = 2048;     // page table entries kept in LDS
+constexpr float kSlack = 8.f;      // how far (in powers of two) scores may pass the maximum that weights refer to
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 struct Side {
     const char *cache;            // keys or values of the cache
-    int64_t page, token, head;    // its strides in bytes
+    uint32_t page, token;         // its strides in bytes
+    int64_t head;
     const float *scale;
     const uint16_t *rows;         // of the chunk
     int64_t ld;
@@ -72,6 +77,7 @@ struct Sequence {
     int len;           // cached tokens
     int sinks, from;   // tokens 0 .. sinks - 1 of the cache come first, then those from `from` on
     int cached;        // how many that are
+    int sink_pages, from_page;  // pages of the first ones, and the page that holds token `from`
     int cache_tiles;   // E4M3: tiles of cached tokens; the chunk's follow in tiles of their own
     int tiles;
     int blocks;
@@ -91,21 +97,49 @@ struct Sequence {
             if (from > len) from = len;
         }
         cached = sinks + len - from;
+        sink_pages = sinks > 0 ? (int)page_of(p, sinks - 1) + 1 : 0;
+        from_page = (int)page_of(p, from);
         cache_tiles = (int)(((int64_t)cached + kTile - 1) / kTile);
         tiles = E4M3 ? cache_tiles + (int)(((int64_t)n + kTile - 1) / kTile)
                      : (int)(((int64_t)cached + n + kTile - 1) / kTile);
         blocks = (int)(((int64_t)n * p.group + block_rows - 1) / block_rows);
     }
+    // place in the table of the cached token numbered u
+    __device__ __forceinline__ int position(int u) const { return u < sinks ? u : u - sinks + from; }
+    // its page, of the pages in use counted without a gap
+    __device__ __forceinline__ int page(const Params &p, int u) const {
+        return u < sinks ? (int)page_of(p, u) : sink_pages + (int)page_of(p, u - sinks + from) - from_page;
+    }
     __device__ __forceinline__ int64_t steps(const Params &p) const { return (int64_t)p.heads * blocks * tiles; }
 };
 
-// Chunks of 16 bytes of a tile's row change places by the row's number, so that the 16
-// rows that a read takes at one column lie in different banks, and so do the 8 rows of
-// half a transposed read (which takes pairs of chunks).
-template <int D>
+// In LDS the 16-byte chunks of a tile's row stand at other places, by the row's number, so
+// that what is read at once lies in different banks: the 16 rows of a score's operand at one
+// column; of a transposed read of bf16, 8 rows and two neighbouring chunks; of codes, one
+// chunk of rows 0 .. 7 and 16 .. 23. The row's lowest bits are in the address already where a
+// row is shorter than the 16 chunks that the banks hold.
+template <int CHUNKS, bool CODES>
 __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (D == 64) return ((row >> 1) & 3) << 1 | ((row >> 3) & 1);
-    else return (row & 7) << 1 | ((row >> 3) & 1);
+    if constexpr (!CODES && CHUNKS >= 16) return (row & 7) << 1 | ((row >> 3) & 1);
+    else if constexpr (!CODES) return ((row >> 1) & 3) << 1 | ((row >> 3) & 1);
+    else if constexpr (CHUNKS >= 16) return (row & 7) | ((row >> 3 ^ row >> 4) & 1) << 3;
+    else if constexpr (CHUNKS == 8) return ((row >> 1) & 3) | ((row >> 3 ^ row >> 4) & 1) << 2;
+    else return ((row >> 2) & 1) | ((row >> 3 ^ row >> 4) & 1) << 1;
+}
+
+// What absent tokens are loaded from.
+__device__ __attribute__((aligned(16))) const uint4 kZeros[32] = {};
+
+// 16 bytes a lane from memory into LDS, lane i's at lds + 16 i. (Not counted by the compiler,
+// which would wait for all loads in flight before each read of LDS: the waits are explicit.)
+__device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(lds) : "memory", "m0");
+}
+
+// Eight E4M3 codes as bf16 (exact).
+__device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b) {
+    return make_uint4(e4m3_pair_scaled<false>(a, 1.f), e4m3_pair_scaled<true>(a, 1.f), e4m3_pair_scaled<false>(b, 1.f),
+                      e4m3_pair_scaled<true>(b, 1.f));
 }
 
 __device__ __forceinline__ f32x4 mfma16x16x16(s16x4 a, s16x4 b, f32x4 c) {
@@ -132,15 +166,23 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // exp2(m - top) for a maximum m <= top; no weight has been seen below -inf
 __device__ __forceinline__ float decay(float m, float top) { return exp2_fast(m - (top == -INFINITY ? 0.f : top)); }
 
+// A value that all lanes hold, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // D elements a head; RT 16-row tiles a wave, WR waves over rows, WK waves over tokens.
 template <int D, bool E4M3, int RT, int WR, int WK>
 struct Shape {
     static constexpr int kWaves = WR * WK, kThreads = 64 * kWaves;
     static constexpr int kRows = 16 * RT * WR;
     static constexpr int kBlocks = kTile / 16 / WK;   // 16-token blocks of a tile that a wave takes
-    static constexpr int kRowBytes = D * 2;
-    static constexpr int kTileBytes = kTile * kRowBytes;
-    static constexpr int kLds = 2 * kTileBytes + kRows * 8 + kStaged * 4 + 256;
+    static constexpr int kPart = kTile * D * (E4M3 ? 1 : 2);  // bytes of a tile's keys, or values
+    static constexpr int kJoin = WK / 2 * kRows * D * 4;      // of half the waves' sums
+    static constexpr int kArea = 4 * kPart > kJoin ? 4 * kPart : kJoin;
+    static constexpr int kOdd = 3 * kRows * D / 8;            // a bit each: infinities and NaN that rows see
+    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + 256 + kOdd;
 };
 
 template <int D, bool E4M3, int RT, int WR, int WK>
@@ -148,10 +190,13 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
     using Z = Shape<D, E4M3, RT, WR, WK>;
     constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16;
     __shared__ __attribute__((aligned(256))) char lds[Z::kLds];
-    char *const lds_k = lds, *const lds_v = lds + Z::kTileBytes;
-    uint64_t *const masks = (uint64_t *)(lds + 2 * Z::kTileBytes);
+    // keys of two tiles, values of two; or one tile of bf16 beside an 8-bit cache; or sums
+    uint64_t *const masks = (uint64_t *)(lds + Z::kArea);
     int *const staged = (int *)(masks + Z::kRows);
-    int64_t *const scratch = (int64_t *)(staged + kStaged);
+    int *const entries = staged + kStaged;
+    int64_t *const scratch = (int64_t *)(entries + kEntries);
+    uint32_t *const odd = (uint32_t *)(scratch + 32);  // [kind][row][D / 32]
+    const uint32_t area = lds_addr(lds);
 
     const int lane = threadIdx.x & 63, wave = wave_id(), tid = threadIdx.x;
     const int wr = wave / WK, wk = wave % WK;
@@ -160,14 +205,16 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
     // ---- this workgroup's steps, of all sequences' in order ----
     const int w = xcd_contiguous(blockIdx.x, p.grid);
     Sequence sq;
-    int64_t total, mine, seq_at;  // all steps, those before this thread's sequences, those before sq
+    int64_t total, seq_at;  // all steps, and those before sq
+    int parts;
     {
         const int per = (p.S + Z::kThreads - 1) / Z::kThreads;
         const int s0 = min(tid * per, p.S), s1 = min(s0 + per, p.S);
+        Sequence each;
         int64_t sum = 0;
         for (int s = s0; s < s1; ++s) {
-            sq.load<E4M3>(p, s, Z::kRows);
-            sum += sq.steps(p);
+            each.load<E4M3>(p, s, Z::kRows);
+            sum += each.steps(p);
         }
         int64_t run = sum;
         for (int d = 1; d < 64; d <<= 1) {
@@ -176,36 +223,34 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         }
         if (lane == 63) scratch[wave] = run;
         __syncthreads();
-        mine = run - sum;
-        total = 0;
+        int64_t before = run - sum, all = 0;
         for (int i = 0; i < Z::kWaves; ++i) {
-            if (i < wave) mine += scratch[i];
-            total += scratch[i];
+            if (i < wave) before += scratch[i];
+            all += scratch[i];
         }
-        __syncthreads();
-        const int parts = (int)min((int64_t)p.grid, total);
+        total = uniform(all);
+        parts = (int)min((int64_t)p.grid, total);
         if (w >= parts) {
             if (tid == 0) p.joins[w] = make_int4(0, 0, 0, 0);
             return;
         }
+        __syncthreads();
         const int64_t x0 = total * w / parts;
-        if (mine <= x0 && x0 < mine + sum) {
-            int64_t at = mine;
+        if (before <= x0 && x0 < before + sum) {
             int s = s0;
             for (;; ++s) {
-                sq.load<E4M3>(p, s, Z::kRows);
-                const int64_t st = sq.steps(p);
-                if (x0 < at + st) break;
-                at += st;
+                each.load<E4M3>(p, s, Z::kRows);
+                const int64_t st = each.steps(p);
+                if (x0 < before + st) break;
+                before += st;
             }
             scratch[0] = s;
-            scratch[1] = at;
+            scratch[1] = before;
         }
         __syncthreads();
-        sq.load<E4M3>(p, (int)scratch[0], Z::kRows);
-        seq_at = scratch[1];
+        sq.load<E4M3>(p, (int)uniform(scratch[0]), Z::kRows);
+        seq_at = uniform(scratch[1]);
     }
-    const int parts = (int)min((int64_t)p.grid, total);
     const int64_t end = total * (w + 1) / parts;
     int64_t x = total * w / parts;
     int4 join = make_int4(0, 0, 0, 0);
@@ -228,9 +273,11 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         for (int rt = 0; rt < RT; ++rt) {
             const int r = row0 + (wr * RT + rt) * 16 + col;
             const int node = r / p.group, head = h * p.group + r % p.group;
-            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head * D) + quad;
+            // elements that a lane's keys hold: 8 of every 32, or 16 codes of every 64
+            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head * D);
 #pragma unroll
-            for (int c = 0; c < C; ++c) qf[rt][c] = r < rows ? src[4 * c] : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < C; ++c)
+                qf[rt][c] = r < rows ? src[E4M3 ? 8 * (c / 2) + 2 * quad + c % 2 : 4 * c + quad] : make_uint4(0, 0, 0, 0);
         }
         float ks = p.scale, vs = 1.f;
         if (E4M3) {
@@ -256,128 +303,155 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             for (int dt = 0; dt < DT; ++dt) acc[rt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        for (int t = t0; t < t1; ++t) {
-            const bool own = E4M3 && t >= sq.cache_tiles;  // a tile of the chunk's rows alone
-            if (E4M3 && t == sq.cache_tiles)
-                // what stands so far is in units of the cache's scale
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
+        const int cut = E4M3 ? min(t1, sq.cache_tiles) : t1;  // tiles past it hold the chunk's rows alone
+        int entry0 = 0, entry1 = 0;                            // pages whose table entries LDS holds
 
-            // ---- where the tile's tokens lie: lane i finds token i ----
-            const int base = own ? sq.cached + (t - sq.cache_tiles) * kTile : t * kTile;
-            const int limit = own ? sq.cached + sq.n : E4M3 ? sq.cached : sq.cached + sq.n;
-            const char *ka = nullptr, *va = nullptr;
-            {
-                const int64_t u = (int64_t)base + lane;
-                if (u < limit) {
-                    if (u < sq.cached) {
-                        const int pos = u < sq.sinks ? (int)u : (int)u - sq.sinks + sq.from;
-                        const uint32_t at = page_of(p, pos);
-                        const uint32_t page = (uint32_t)p.table[(int64_t)sq.s * p.ld_table + at];
-                        const int in = pos - (int)(at * p.page_size);
-                        if (page < p.pages) {
-                            ka = p.k.cache + page * p.k.page + in * p.k.token + h * p.k.head;
-                            va = p.v.cache + page * p.v.page + in * p.v.token + h * p.v.head;
-                        }
+        // Where the tokens of a tile lie: lane i finds token base + i; kZeros for none. Returns
+        // the bits of those that are there.
+        uint64_t ka = 0, va = 0;
+        const uint64_t k_cache = (uint64_t)(p.k.cache + h * p.k.head), v_cache = (uint64_t)(p.v.cache + h * p.v.head);
+        auto locate = [&](int base, int limit) {
+            const int u = base + lane;
+            ka = va = (uint64_t)kZeros;
+            bool there = false;
+            if (u < limit) {
+                if (u < sq.cached) {
+                    const int pos = sq.position(u);
+                    const uint32_t page = (uint32_t)entries[sq.page(p, u) - entry0];
+                    const uint32_t in = (uint32_t)pos - page_of(p, pos) * p.page_size;
+                    if (page < p.pages) {
+                        ka = k_cache + (uint64_t)page * p.k.page + (uint64_t)in * p.k.token;
+                        va = v_cache + (uint64_t)page * p.v.page + (uint64_t)in * p.v.token;
+                        there = true;
+                    }
+                } else {
+                    const int64_t m = sq.first + (u - sq.cached);
+                    ka = (uint64_t)(p.k.rows + m * p.k.ld + (int64_t)h * D);
+                    va = (uint64_t)(p.v.rows + m * p.v.ld + (int64_t)h * D);
+                    there = true;
+                }
+            }
+            return __ballot(there);
+        };
+        // The table's entries for a tile, if they are not in LDS (for as many more as it holds).
+        auto look_up = [&](int base) {
+            if (base >= sq.cached) return;
+            const int last = sq.page(p, min(base + kTile, sq.cached) - 1);
+            if (last < entry1) return;
+            lds_barrier();
+            entry0 = sq.page(p, base);
+            entry1 = min(entry0 + kEntries, sq.page(p, min(cut * kTile, sq.cached) - 1) + 1);
+            const int32_t *table = p.table + (int64_t)sq.s * p.ld_table;
+            for (int i = tid; i < entry1 - entry0; i += Z::kThreads) {
+                const int c = entry0 + i;
+                entries[i] = table[c < sq.sink_pages ? c : c - sq.sink_pages + sq.from_page];
+            }
+            __syncthreads();
+        };
+        // A tile's rows of BYTES bytes into LDS, in pieces of 1 KiB that the waves share.
+        auto fill = [&](auto row_bytes, uint64_t from, uint32_t to) {
+            constexpr int BYTES = decltype(row_bytes)::value, CHUNKS = BYTES / 16, kPieces = kTile * BYTES / 1024;
+            constexpr int kMine = kPieces > Z::kWaves ? kPieces / Z::kWaves : 1;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int piece = wave * kMine + i;
+                if (kPieces < Z::kWaves && piece >= kPieces) break;
+                const int row = piece * (64 / CHUNKS) + lane / CHUNKS;
+                const int chunk = lane % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
+                const uint64_t a = (uint64_t)__shfl((long long)from, row);
+                load_to_lds(a + chunk * 16, to + piece * 1024);
+            }
+        };
+        constexpr int kMine = Z::kPart / 1024 > Z::kWaves ? Z::kPart / 1024 / Z::kWaves : 1;  // pieces a wave loads at once
+        constexpr std::integral_constant<int, D * (E4M3 ? 1 : 2)> cache_row{};
+        constexpr std::integral_constant<int, 2 * D> bf16_row{};
+
+        // tiles that every row sees whole need no mask
+        auto needs_mask = [&](int base, uint64_t there) {
+            if (~there != 0 || base + kTile > sq.cached) return true;
+            return p.window > 0 && base < (int64_t)sq.sinks + sq.n - 1 && base + kTile > sq.sinks;
+        };
+        auto make_masks = [&](int base, uint64_t there) {
+            for (int i = tid; i < Z::kRows; i += Z::kThreads) {
+                const int r = row0 + i, node = r / p.group;
+                uint64_t bits = 0;
+                if (r < rows) {
+                    auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
+                    int depth = node;
+                    if (parents && p.window > 0) {
+                        depth = 0;
+                        for (int i = parent_of(node); i >= 0; i = parent_of(i)) ++depth;
+                    }
+                    const int64_t at = (int64_t)sq.len + depth;
+                    bits = below((int64_t)sq.cached - base);
+                    if (p.window > 0) {
+                        const int64_t old = sq.sinks + max(at - p.window + 1 - sq.from, (int64_t)0);
+                        bits &= ~below(old - base) | below((int64_t)sq.sinks - base);
+                    }
+                    const int far = p.window > 0 ? p.window : INT32_MAX;            // ancestors nearer than that
+                    const int64_t sunk = p.window > 0 ? (int64_t)p.sinks - sq.len : 0;  // depths below are sinks
+                    const int64_t off = (int64_t)sq.cached - base;                  // bit of the sequence's first row
+                    if (!parents) {
+                        const uint64_t line = below(off + node + 1) & ~below(off);
+                        bits |= line & (~below(off + (int64_t)node - far + 1) | below(off + sunk));
                     } else {
-                        const int64_t m = sq.first + (u - sq.cached);
-                        ka = (const char *)(p.k.rows + m * p.k.ld + (int64_t)h * D);
-                        va = (const char *)(p.v.rows + m * p.v.ld + (int64_t)h * D);
+                        int d = 0;
+                        for (int i = node; i >= 0 && off + i >= 0; i = parent_of(i), ++d)
+                            if (off + i < 64 && (d < far || depth - d < sunk)) bits |= 1ull << (off + i);
                     }
+                    bits &= there;
                 }
+                masks[i] = bits;
             }
-            const uint64_t there = __ballot(ka != nullptr);
-            // tiles that every row sees whole need no mask
-            bool masked = ~there != 0 || base + kTile > sq.cached;
-            if (p.window > 0 && (int64_t)base < (int64_t)sq.sinks + sq.n - 1 && base + kTile > sq.sinks) masked = true;
+        };
 
-            // ---- the tile into LDS ----
-            __syncthreads();
-            auto fill = [&](const char *addr, char *to) {
-                constexpr int kChunks = Z::kRowBytes / 16;             // 16-byte chunks of a row in LDS
-                constexpr int kRowsAtOnce = 64 / kChunks > 0 ? 64 / kChunks : 1;
-                constexpr int kSteps = kTile / kRowsAtOnce / Z::kWaves;
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int row = (wave * kSteps + i) * kRowsAtOnce + lane / kChunks;
-                    const int chunk = (lane % kChunks) ^ swizzle<D>(row);
-                    const uint64_t a = (uint64_t)__shfl((long long)(uint64_t)addr, row);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (a) {
-                        if (E4M3 && !own) {
-                            const uint2 c = *(const uint2 *)(a + chunk * 8);
-                            v = make_uint4(e4m3_pair_scaled<false>(c.x, 1.f), e4m3_pair_scaled<true>(c.x, 1.f),
-                                           e4m3_pair_scaled<false>(c.y, 1.f), e4m3_pair_scaled<true>(c.y, 1.f));
-                        } else {
-                            v = *(const uint4 *)(a + chunk * 16);
-                        }
-                    }
-                    *(uint4 *)(to + row * Z::kRowBytes + (lane % kChunks) * 16) = v;
-                }
+        f32x4 sc[RT][NB];
+        uint2 wt[RT][NB];  // bf16 weights of tokens 4 quad .. 4 quad + 3 of each block
+        // scores of this wave's blocks of tokens, from keys in LDS
+        auto scores = [&](auto codes, uint32_t keys) {
+            constexpr bool CODES = decltype(codes)::value;
+            constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16;
+            // chunk c of a row is at c ^ swizzle: the lane's own bits are in the address from the
+            // start, those of an operand are changed or added to it
+            constexpr bool WIDE = CODES || E4M3;  // a lane's two operands are neighbours
+            const int row = wk * NB * 16 + col;
+            const lds_u8 *const from = lds_opaque(keys + row * BYTES + ((WIDE && !CODES ? 2 * quad : quad) ^ swizzle<CHUNKS, CODES>(row)) * 16);
+            auto chunk_at = [&](int b, int chunk) {
+                constexpr int kMixed = CHUNKS < 16 ? CHUNKS - 1 : 15;
+                return lds_ld16((const lds_u8 *)((uint32_t)(uintptr_t)from ^ (chunk & kMixed) * 16) +
+                                (chunk & ~kMixed) * 16 + b * 16 * BYTES);
             };
-            fill(ka, lds_k);
-            fill(va, lds_v);
-            if (masked) {
-                for (int i = tid; i < Z::kRows; i += Z::kThreads) {
-                    const int r = row0 + i, node = r / p.group;
-                    uint64_t bits = 0;
-                    if (r < rows) {
-                        auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
-                        // positions of the row, and the distance a path's token may have
-                        int depth = node;
-                        if (parents && p.window > 0) {
-                            depth = 0;
-                            for (int i = parent_of(node); i >= 0; i = parent_of(i)) ++depth;
-                        }
-                        const int64_t at = (int64_t)sq.len + depth;
-                        bits = below((int64_t)sq.cached - base);
-                        if (p.window > 0) {
-                            const int64_t old = sq.sinks + max(at - p.window + 1 - sq.from, (int64_t)0);
-                            bits &= ~below(old - base) | below((int64_t)sq.sinks - base);
-                        }
-                        const int far = p.window > 0 ? p.window : INT32_MAX;
-                        const int64_t sunk = p.window > 0 ? (int64_t)p.sinks - sq.len : 0;  // depths below are sinks
-                        const int64_t off = (int64_t)sq.cached - base;  // bit of the sequence's first row
-                        if (!parents) {
-                            // nodes 0 .. node, those nearer than `far` or of depths that are sinks
-                            const uint64_t line = below(off + node + 1) & ~below(off);
-                            bits |= line & (~below(off + (int64_t)node - far + 1) | below(off + sunk));
-                        } else {
-                            int d = 0;
-                            for (int i = node; i >= 0 && off + i >= 0; i = parent_of(i), ++d)
-                                if (off + i < 64 && (d < far || depth - d < sunk)) bits |= 1ull << (off + i);
-                        }
-                        bits &= there;
-                    }
-                    masks[i] = bits;
-                }
-            }
-            __syncthreads();
-
-            // ---- scores of this wave's blocks of tokens ----
-            f32x4 sc[RT][NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const int row = (wk * NB + b) * 16 + col;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) sc[rt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const uint4 kf = *(const uint4 *)(lds_k + row * Z::kRowBytes + (((4 * c + quad) ^ swizzle<D>(row)) * 16));
+                for (int c = 0; c < C; c += 2) {
+                    uint4 kf[2];
+                    if constexpr (CODES) {
+                        // (the next block's swizzle differs in its highest bit)
+                        const uint4 x = chunk_at(b, 2 * c ^ (b % 2 ? (CHUNKS < 16 ? CHUNKS / 2 : 8) : 0));
+                        kf[0] = decode8(x.x, x.y);
+                        kf[1] = decode8(x.z, x.w);
+                    } else {
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) sc[rt][b] = mfma16x16x32(kf, qf[rt][c], sc[rt][b]);
+                        for (int e = 0; e < 2; ++e) kf[e] = chunk_at(b, WIDE ? 4 * c + e : 4 * (c + e));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) sc[rt][b] = mfma16x16x32(kf[e], qf[rt][c + e], sc[rt][b]);
                 }
             }
-            // ---- weights ----
-            const float to2 = own ? p.scale : ks;
-            uint2 wt[RT][NB];  // bf16 weights of tokens 4 quad .. 4 quad + 3 of each block
+        };
+        // their weights, relative to a maximum that follows the scores' once these pass it by
+        // kSlack: 2^kSlack is nothing to fp32 sums, and sums are rarely rescaled
+        auto weigh = [&](float to2, bool masked) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 uint64_t bits = ~0ull;
                 if (masked) bits = masks[(wr * RT + rt) * 16 + col] >> (wk * NB * 16 + 4 * quad);
-                float high = top[rt];
+                float high = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -388,9 +462,15 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                         high = fmaxf(high, s);
                     }
                 high = rows4_max(high);
-                const float safe = high == -INFINITY ? 0.f : high;
-                const float down = exp2_fast(top[rt] - safe);
-                top[rt] = high;
+                if (__any(high > top[rt] + kSlack)) {
+                    high = fmaxf(high, top[rt]);
+                    const float down = decay(top[rt], high);
+                    top[rt] = high;
+                    sum[rt] *= down;
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= down;
+                }
+                const float safe = top[rt] == -INFINITY ? 0.f : top[rt];
                 float add = 0.f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -399,99 +479,167 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                     for (int i = 0; i < 4; ++i) add += e[i] = exp2_fast(sc[rt][b][i] - safe);
                     wt[rt][b] = make_uint2(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]));
                 }
-                sum[rt] = sum[rt] * down + add;
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= down;
+                sum[rt] += add;
             }
-            // ---- weighted values ----
-            auto value = [&](int b, int dt) {
-                const int row = (wk * NB + b) * 16 + 4 * quad + (col >> 2);
-                const int chunk = (2 * dt + ((col >> 1) & 1)) ^ swizzle<D>(row);
-                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4 *)(lds_v + row * Z::kRowBytes + chunk * 16 + (col & 1) * 8));
+        };
+        // The weighted values of a tile in LDS. A transposed read gives a lane 4 tokens of its
+        // column (4 quad .. 4 quad + 3 of a block), of codes 8: of two blocks of tokens, or (a wave
+        // with one) of two blocks of columns.
+        auto add_values = [&](auto codes, uint32_t values) {
+            constexpr bool CODES = decltype(codes)::value;
+            constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16, kMixed = CHUNKS < 16 ? CHUNKS - 1 : 15;
+            const int row = wk * NB * 16 + 4 * quad + (CODES ? col >> 1 & 3 : col >> 2) + (CODES && NB > 1 ? col >> 3 << 4 : 0);
+            const int chunk = CODES ? (NB == 1 ? col >> 3 : 0) : col >> 1 & 1;
+            const uint32_t from = (uint32_t)(uintptr_t)lds_opaque(values + row * BYTES + (chunk ^ swizzle<CHUNKS, CODES>(row)) * 16 +
+                                                                  (col & 1) * 8);
+            typedef int i32x2 __attribute__((ext_vector_type(2)));
+            auto read = [&](int b, int chunk) {
+                const lds_u8 *at = (const lds_u8 *)(from ^ (chunk & kMixed) * 16) + (chunk & ~kMixed) * 16 + b * 16 * BYTES;
+                if constexpr (CODES)
+                    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2 *)at);
+                else
+                    return __builtin_bit_cast(
+                        i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at));
             };
-            bool rough = false;  // a value that some row does not see is infinite or NaN
-            if (masked) {
-                bool bad = false;
-                for (int i = tid; i < Z::kTileBytes / 16; i += Z::kThreads) {
-                    const uint4 v = ((const uint4 *)lds_v)[i];
-                    for (uint32_t x : {v.x, v.y, v.z, v.w})
-                        bad |= (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
-                }
-                rough = __syncthreads_or(bad);
-            }
-            auto finite = [](s16x4 v) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = (v[i] & 0x7F80) == 0x7F80 ? (short)0 : v[i];
-                return v;
-            };
-            auto add_values = [&](auto take) {
-                if constexpr (NB == 1) {
+            for (int b = 0; b < NB; b += 2)
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        const s16x4 a = take(value(0, dt));
+                for (int dt = 0; dt < DT; dt += 2) {
+                    uint4 a[2];  // of columns 16 dt and 16 dt + 16: a block's tokens, and the next one's
+                    if constexpr (CODES && NB == 1) {
+                        const i32x2 x = read(0, dt);
+                        const uint4 d = decode8(x[0], x[1]);
+                        a[0] = d;
+                        a[1] = make_uint4(d.z, d.w, 0, 0);
+                    } else if constexpr (CODES) {
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            acc[rt][dt] = mfma16x16x16(a, __builtin_bit_cast(s16x4, wt[rt][0]), acc[rt][dt]);
+                        for (int e = 0; e < 2; ++e) {
+                            const i32x2 x = read(b, dt + e);
+                            a[e] = decode8(x[0], x[1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const i32x2 x = read(b, 2 * (dt + e));
+                            i32x2 y = {};
+                            if (NB > 1) y = read(b + 1, 2 * (dt + e));
+                            a[e] = make_uint4(x[0], x[1], y[0], y[1]);
+                        }
                     }
-                } else {
 #pragma unroll
-                    for (int b = 0; b < NB; b += 2)
-#pragma unroll
-                        for (int dt = 0; dt < DT; ++dt) {
-                            const uint2 a = __builtin_bit_cast(uint2, take(value(b, dt)));
-                            const uint2 c = __builtin_bit_cast(uint2, take(value(b + 1, dt)));
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-                                acc[rt][dt] = mfma16x16x32(make_uint4(a.x, a.y, c.x, c.y),
-                                                           make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x,
-                                                                      wt[rt][b + 1].y),
-                                                           acc[rt][dt]);
-                        }
-                }
-            };
-            if (!rough) {
-                add_values([](s16x4 v) { return v; });
-            } else {
-                // finite values as ever (0 * infinity would reach the rows that do not see it); of the
-                // others, how many of each kind every row sees
-                add_values(finite);
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        const s16x4 v = value(b, dt);
-                        s16x4 up, down, none;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            up[i] = v[i] == (short)0x7F80 ? (short)0x3F80 : (short)0;
-                            down[i] = v[i] == (short)0xFF80 ? (short)0x3F80 : (short)0;
-                            none[i] = (v[i] & 0x7FFF) > 0x7F80 ? (short)0x3F80 : (short)0;
-                        }
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
-                            const uint64_t bits = masks[(wr * RT + rt) * 16 + col] >> ((wk * NB + b) * 16 + 4 * quad);
-                            s16x4 seen;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) seen[i] = bits >> i & 1 ? (short)0x3F80 : (short)0;
-                            const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-                            const f32x4 nu = mfma16x16x16(up, seen, zero), nd = mfma16x16x16(down, seen, zero),
-                                        nn = mfma16x16x16(none, seen, zero);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (nu[i] > 0.f) acc[rt][dt][i] += INFINITY;
-                                if (nd[i] > 0.f) acc[rt][dt][i] -= INFINITY;
-                                if (nn[i] > 0.f) acc[rt][dt][i] = NAN;
-                            }
+                            if constexpr (NB == 1)
+                                acc[rt][dt + e] = mfma16x16x16(__builtin_bit_cast(s16x4, make_uint2(a[e].x, a[e].y)),
+                                                               __builtin_bit_cast(s16x4, wt[rt][0]), acc[rt][dt + e]);
+                            else
+                                acc[rt][dt + e] = mfma16x16x32(
+                                    a[e], make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x, wt[rt][b + 1].y),
+                                    acc[rt][dt + e]);
                         }
+                }
+        };
+        // In a tile that some row does not see whole, 0 * infinity must not reach the rows that do
+        // not see it: infinities and NaN become zeros there, and the rows that see one get it when
+        // their sums are done.
+        bool any_odd = false;
+        auto set_apart = [&](auto codes, char *values) {
+            constexpr bool CODES = decltype(codes)::value;
+            constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16;
+            auto each = [&](auto found) {
+                for (int i = tid; i < kTile * CHUNKS; i += Z::kThreads) {
+                    const uint4 v = ((const uint4 *)values)[i];
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    for (int e = 0; e < (CODES ? 16 : 8); ++e) {
+                        const uint32_t y = CODES ? x[e / 4] >> (8 * (e % 4)) & 0xFF : x[e / 2] >> (16 * (e % 2)) & 0xFFFF;
+                        if (CODES ? (y & 0x7F) == 0x7F : (y & 0x7F80) == 0x7F80) found(i, e, y);
                     }
+                }
+            };
+            bool here = false;
+            each([&](int, int, uint32_t) { here = true; });
+            if (!__syncthreads_or(here)) return;
+            if (!any_odd)
+                for (int i = tid; i < Z::kOdd / 4; i += Z::kThreads) odd[i] = 0;
+            any_odd = true;
+            __syncthreads();
+            each([&](int i, int e, uint32_t y) {
+                const int row = i / CHUNKS, d = ((i % CHUNKS) ^ swizzle<CHUNKS, CODES>(row)) * (CODES ? 16 : 8) + e;
+                const int kind = CODES || (y & 0x7F) ? 2 : y >> 15;  // 0 inf, 1 -inf, 2 NaN
+                for (int r = 0; r < Z::kRows; ++r)
+                    if (masks[r] >> row & 1) atomicOr(&odd[((kind * Z::kRows + r) * D + d) / 32], 1u << (d & 31));
+                if (CODES) values[i * 16 + e] = 0;
+                else ((uint16_t *)values)[i * 8 + e] = 0;
+            });
+            __syncthreads();
+        };
+
+        // ---- the cache's tiles (bf16: and the chunk's rows) ----
+        // Keys and values have two places each. At the first barrier of a step its keys are
+        // there and the last step's values are done with: their place takes the next tile's.
+        // At the second its values are there and the keys' place takes those after the next.
+        if (t0 < cut) {
+            const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
+            look_up(t0 * kTile);
+            uint64_t there = locate(t0 * kTile, limit), next = 0, after = 0;
+            fill(cache_row, ka, area);
+            fill(cache_row, va, area + 2 * Z::kPart);
+            if (t0 + 1 < cut) {
+                look_up((t0 + 1) * kTile);
+                next = locate((t0 + 1) * kTile, limit);
+                fill(cache_row, ka, area + Z::kPart);
             }
+            for (int t = t0; t < cut; ++t) {
+                const int at = (t - t0) & 1;
+                const uint32_t keys = area + at * Z::kPart, values = area + (2 + at) * Z::kPart;
+                const bool more = t + 1 < cut;
+                if (more) wait_vmcnt<2 * kMine>();
+                else wait_vmcnt<kMine>();
+                lds_barrier();
+                if (more) fill(cache_row, va, area + (3 - at) * Z::kPart);
+                const bool masked = needs_mask(t * kTile, there);
+                if (masked) {
+                    make_masks(t * kTile, there);
+                    lds_barrier();
+                }
+                scores(std::bool_constant<E4M3>{}, keys);
+                weigh(ks, masked);
+                if (more) wait_vmcnt<2 * kMine>();
+                else wait_vmcnt<0>();
+                lds_barrier();
+                if (t + 2 < cut) {
+                    look_up((t + 2) * kTile);
+                    after = locate((t + 2) * kTile, limit);
+                    fill(cache_row, ka, area + at * Z::kPart);
+                }
+                if (masked) set_apart(std::bool_constant<E4M3>{}, lds + (2 + at) * Z::kPart);
+                add_values(std::bool_constant<E4M3>{}, values);
+                there = next;
+                next = after;
+            }
+            if (E4M3)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
         }
-        if (E4M3 && t1 <= sq.cache_tiles)
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
+        // ---- beside an 8-bit cache, the chunk's rows ----
+        if constexpr (E4M3)
+            for (int t = max(t0, sq.cache_tiles); t < t1; ++t) {
+                const int base = sq.cached + (t - sq.cache_tiles) * kTile;
+                const uint64_t there = locate(base, sq.cached + sq.n);
+                lds_barrier();
+                fill(bf16_row, ka, area);
+                fill(bf16_row, va, area + 2 * Z::kPart);
+                make_masks(base, there);
+                wait_vmcnt<0>();
+                lds_barrier();
+                scores(std::false_type{}, area);
+                weigh(p.scale, true);
+                set_apart(std::false_type{}, lds + 2 * Z::kPart);
+                add_values(std::false_type{}, area + 2 * Z::kPart);
+            }
 
         // ---- the sums of the four 16-lane rows, then of the waves over tokens ----
 #pragma unroll
@@ -501,7 +649,6 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             __syncthreads();
             float *const at = (float *)lds;
             float2 *const st = (float2 *)masks;  // [waves over rows][half][16 RT], in place of masks and parents
-            static_assert(WK / 2 * Z::kRows * 4 * D <= 2 * Z::kTileBytes, "parts fit the tiles");
             static_assert(WK / 2 <= 2, "statistics fit the masks and the parents");
             if (wk >= half && wk < 2 * half) {
                 const int slot = wr * half + wk - half;
@@ -554,6 +701,24 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                 }
             }
         }
+        if (any_odd) {
+            // infinities and NaN that rows see
+            __threadfence_block();
+            __syncthreads();
+            for (int i = tid; i < Z::kRows * D; i += Z::kThreads) {
+                const int at = i / D, d = i % D, r = row0 + at;
+                auto is = [&](int kind) { return odd[(kind * Z::kRows * D + i) / 32] >> (d & 31) & 1; };
+                const bool up = is(0), down = is(1);
+                if (r >= rows || !(up || down || is(2))) continue;
+                const float add = is(2) || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+                if (whole) {
+                    uint16_t *o = p.out + (int64_t)(sq.first + r / p.group) * p.ld_out + (int64_t)(h * p.group + r % p.group) * D + d;
+                    *o = f32_to_bf16_rne(bits_f32((uint32_t)*o << 16) + add);
+                } else {
+                    p.parts[((2 * (int64_t)w + (t0 == 0)) * Z::kRows + at) * D + d] += add;
+                }
+            }
+        }
         if (t0 == 0 && t1 < sq.tiles) {
             // the parts that follow: one a workgroup, up to the one with this unit's last step
             const int64_t last = x + sq.tiles - 1;
@@ -565,48 +730,72 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
     if (tid == 0) p.joins[w] = join;
 }
 
-// Joins a block of rows whose first part is workgroup x's: one row of it a workgroup.
-template <int D>
-__global__ __launch_bounds__(256) void join_kernel(const Params p, int block_rows) {
+// Joins a block of rows whose first part is workgroup x's: a sixteenth of the rows a
+// workgroup, RW waves a row (few rows have many parts).
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void join_kernel(const Params p) {
     const int w = blockIdx.x;
     const int4 j = p.joins[w];
     if (j.w == 0) return;
+    constexpr int RW = ROWS >= 64 ? 1 : 64 / ROWS, E = D / 64, kAtOnce = 4 / RW;
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int first = min(max(p.starts[j.x], 0), p.M);
     const int n = max(min(p.starts[j.x + 1], p.M) - first, 0);
-    const int i = blockIdx.y, r = j.z * block_rows + i;
-    if (r >= n * p.group) return;
     __shared__ float2 stat[4];
     __shared__ float vals[4][D];
-    constexpr int E = D / 64;
-    // wave v takes parts v, v + 4, ...
-    float top = -INFINITY, sum = 0.f, acc[E];
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    auto slot = [&](int part) { return part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part); };
-    for (int part = wave; part <= j.w; part += 4) {
-        const int64_t at = slot(part) * block_rows + i;
-        const float2 st = p.stats[at];
-        const float high = fmaxf(top, st.x), a = decay(top, high), b = decay(st.x, high);
-        top = high;
-        sum = sum * a + st.y * b;
-        const float *src = p.parts + at * D + lane * E;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + src[e] * b;
+    typedef float row_t __attribute__((ext_vector_type(E)));
+    for (int i0 = 0; i0 < ROWS / 16; i0 += kAtOnce) {
+        const int i = blockIdx.y * (ROWS / 16) + i0 + wave / RW, r = j.z * ROWS + i;
+        const bool here = r < n * p.group;
+        float top = -INFINITY, sum = 0.f;
+        row_t acc = 0.f;
+        auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part)) * ROWS + i; };
+        if (here)
+            // 64 parts at a time: lane l's statistics, then the values by their weights
+            for (int p0 = wave % RW; p0 <= j.w; p0 += 64 * RW) {
+                const int part = p0 + lane * RW;
+                float2 st = make_float2(-INFINITY, 0.f);
+                if (part <= j.w) st = p.stats[slot(part)];
+                float high = fmaxf(top, st.x);
+                for (int d = 1; d < 64; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
+                const float b = decay(st.x, high), a = decay(top, high);
+                float add = st.y * b;
+                for (int d = 1; d < 64; d <<= 1) add += __shfl_xor(add, d);
+                sum = sum * a + add;
+                top = high;
+                acc *= a;
+                const int count = min(64, (j.w - p0) / RW + 1);
+#pragma unroll 8
+                for (int k = 0; k < count; ++k) {
+                    const row_t v = *(const row_t *)(p.parts + slot(p0 + k * RW) * D + lane * E);
+                    acc += v * bits_f32(__builtin_amdgcn_readlane(f32_bits(b), k));
+                }
+            }
+        if constexpr (RW > 1) {
+            if (lane == 0) stat[wave] = make_float2(top, sum);
+            *(row_t *)&vals[wave][lane * E] = acc;
+            __syncthreads();
+            float high = -INFINITY;
+            for (int v = 0; v < RW; ++v) high = fmaxf(high, stat[wave / RW * RW + v].x);
+            sum = 0.f;
+            acc = 0.f;
+            for (int v = 0; v < RW; ++v) {
+                const float2 st = stat[wave / RW * RW + v];
+                const float b = decay(st.x, high);
+                sum += st.y * b;
+                acc += *(row_t *)&vals[wave / RW * RW + v][lane * E] * b;
+            }
+        }
+        if (here && wave % RW == 0) {
+            const row_t o = acc * (sum == 0.f ? 0.f : 1.f / sum);
+            uint16_t *to = p.out + (int64_t)(first + r / p.group) * p.ld_out + (int64_t)(j.y * p.group + r % p.group) * D;
+            if constexpr (E == 1) to[lane] = f32_to_bf16_rne(o[0]);
+            else {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) ((uint32_t *)to)[(lane * E + e) / 2] = pack_bf16(o[e], o[e + 1]);
+            }
+        }
     }
-    if (lane == 0) stat[wave] = make_float2(top, sum);
-    for (int e = 0; e < E; ++e) vals[wave][lane * E + e] = acc[e];
-    __syncthreads();
-    if (wave) return;
-    float high = -INFINITY, all = 0.f, o[E];
-    for (int v = 0; v < 4; ++v) high = fmaxf(high, stat[v].x);
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int v = 0; v < 4; ++v) {
-        const float b = decay(stat[v].x, high);
-        all += stat[v].y * b;
-        for (int e = 0; e < E; ++e) o[e] += vals[v][lane * E + e] * b;
-    }
-    const float inv = all == 0.f ? 0.f : 1.f / all;
-    uint16_t *to = p.out + (int64_t)(first + r / p.group) * p.ld_out + (int64_t)(j.y * p.group + r % p.group) * D;
-    for (int e = 0; e < E; ++e) to[lane * E + e] = f32_to_bf16_rne(o[e] * inv);
 }
 
 }  // namespace
@@ -615,7 +804,8 @@ AttendPlan plan_tree_attention(int64_t M, int64_t S, int64_t H, int64_t KVH, int
     AttendPlan p{};
     const int64_t rows = (M * (H / KVH) + S - 1) / S;  // of a sequence, on average
     p.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    p.grid = num_cus;
+    // workgroups that a compute unit's LDS and registers hold at once
+    p.grid = num_cus * (D == 256 ? 1 : 2);
     const size_t slots = 2 * (size_t)p.grid * p.block_rows;
     p.workspace_bytes = kCounterBytes + (((size_t)p.grid * 16 + 255) & ~(size_t)255) + slots * (D * 4 + 8);
     return p;
@@ -630,7 +820,7 @@ hipError_t launch_shape(const Params &p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(p.grid), dim3(Z::kThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(join_kernel<D>, dim3(p.grid, Z::kRows), dim3(256), 0, stream, p, Z::kRows);
+    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.grid, 16), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -640,7 +830,7 @@ hipError_t launch_rows(const Params &p, int block_rows, hipStream_t stream) {
     case 16: return launch_shape<D, E4M3, 1, 1, 4>(p, stream);
     case 32: return launch_shape<D, E4M3, 2, 1, 4>(p, stream);
     case 64: return launch_shape<D, E4M3, 2, 2, 2>(p, stream);
-    default: return launch_shape<D, E4M3, 2, 4, 1>(p, stream);
+    default: return launch_shape<D, E4M3, 2, 4, 2>(p, stream);
     }
 }
 
@@ -660,10 +850,12 @@ hipError_t launch_tree_attention(const AttendPlan &plan, const void *q, int64_t 
     const int64_t size = e4m3 ? 1 : 2;
     p.q = (const uint16_t *)q;
     p.ld_q = ld_q;
-    p.k = Side{(const char *)c.k, c.k_strides[0] * size, c.k_strides[1] * size, c.k_strides[2] * size, c.k_scale,
-               (const uint16_t *)k, ld_k};
-    p.v = Side{(const char *)c.v, c.v_strides[0] * size, c.v_strides[1] * size, c.v_strides[2] * size, c.v_scale,
-               (const uint16_t *)v, ld_v};
+    auto side = [&](const void *cache, const int64_t *st, const float *by, const void *rows, int64_t ld) {
+        return Side{(const char *)cache, (uint32_t)(st[0] * size), (uint32_t)(st[1] * size), st[2] * size, by,
+                    (const uint16_t *)rows, ld};
+    };
+    p.k = side(c.k, c.k_strides, c.k_scale, k, ld_k);
+    p.v = side(c.v, c.v_strides, c.v_scale, v, ld_v);
     p.table = c.page_table;
     p.ld_table = c.ld_table;
     p.lengths = c.lengths;
