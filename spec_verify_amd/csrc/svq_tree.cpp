@@ -87,12 +87,15 @@ int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
     if (c.type != SVQ_CACHE_BF16 && c.type != SVQ_CACHE_E4M3) return SVQ_ERR_UNSUPPORTED;
     if (c.type == SVQ_CACHE_BF16 && (c.k_scale || c.v_scale)) return SVQ_ERR_UNSUPPORTED;
     const int64_t most = int64_t(1) << 31, qc = (int64_t)H * D, kc = (int64_t)KVH * D;
-    if (ld_q < qc || ld_out < qc || ld_k < kc || ld_v < kc || ld_q > most || ld_k > most || ld_v > most || ld_out > most)
+    if (ld_q < qc || ld_out < qc || ld_k < kc || ld_v < kc || ld_q > most || ld_k >= most || ld_v >= most || ld_out > most)
         return SVQ_ERR_DIM;
     if (ld_q % 8 || ld_k % 8 || ld_v % 8 || ld_out % 8) return SVQ_ERR_DIVISIBILITY;
     if (c.pages < 0 || c.pages > INT32_MAX || c.page_size <= 0 || c.page_size > (1 << 20) || c.max_pages < 0 ||
         (int64_t)c.max_pages * c.page_size > kMaxTokens || c.ld_table < c.max_pages || c.ld_table > most)
         return SVQ_ERR_DIM;
+    // steps (a tile of 64 tokens, a run of blocks of 16 rows or more) are counted in 31 bits
+    const int64_t tiles = ((int64_t)c.max_pages * c.page_size + M) / 64 + 2, runs = M * (H / KVH) / 16 + S;
+    if (tiles > (int64_t(1) << 31) / KVH / runs) return SVQ_ERR_DIM;
     const int64_t size = c.type == SVQ_CACHE_E4M3 ? 1 : 2;
     size_t kb, vb;
     if ((st = check_strides(c.k_strides, c, KVH, D, size, &kb)) != SVQ_OK) return st;

@@ -7,11 +7,11 @@
 
 namespace svq {
 
-// Tree attention: `grid` workgroups share the chunk's (sequence, KV head, block of
-// `block_rows` rows, tile of tokens) steps evenly; what they leave unfinished is joined by
-// a second launch.
+// Tree attention: `teams` of workgroups share the chunk's (sequence, KV head, tile of
+// tokens) steps evenly, the members of a team taking different blocks of `block_rows` rows;
+// what they leave unfinished is joined by a second launch.
 struct AttendPlan {
-    int block_rows, grid;
+    int block_rows, teams, members;
     size_t workspace_bytes;
 };
 AttendPlan plan_tree_attention(int64_t M, int64_t S, int64_t H, int64_t KVH, int64_t D, int num_cus);

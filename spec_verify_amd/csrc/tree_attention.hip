@@ -37,6 +37,21 @@ constexpr int kEntries = 2048;     // page table entries kept in LDS
 constexpr float kSlack = 8.f;      // how far (in powers of two) scores may pass the maximum that weights refer to
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// floor(n / d) for n < 2^31: n * ceil(2^(31 + L) / d) >> (31 + L) with 2^(L-1) < d <= 2^L
+struct Divide {
+    uint32_t magic, shift;  // shift: L - 1; d = 1 has neither
+
+    static Divide by(uint32_t d) {
+        int L = 0;
+        while ((uint64_t(1) << L) < d) ++L;
+        return L ? Divide{(uint32_t)(((uint64_t(1) << (31 + L)) + d - 1) / d), (uint32_t)L - 1} : Divide{0, 0};
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return magic ? (int)(__umulhi((uint32_t)n, magic) >> shift) : n;
+    }
+};
 
 struct Side {
     const char *cache;            // keys or values of the cache
@@ -44,7 +59,7 @@ struct Side {
     int64_t head;
     const float *scale;
     const uint16_t *rows;         // of the chunk
-    int64_t ld;
+    uint32_t ld;                  // in bytes
 };
 
 struct Params {
@@ -53,64 +68,53 @@ struct Params {
     Side k, v;
     const int32_t *table, *lengths, *starts, *parents;
     int64_t ld_table;
-    uint32_t pages, page_size, page_magic, page_shift;
+    uint32_t pages, page_size;
+    Divide by_page, by_group;
     int cache_tokens;             // most of a sequence: max_pages * page_size
     float scale;                  // log2(e) times the caller's: weights are powers of two
     int window, sinks;            // window <= 0: none
     uint16_t *out;
     int64_t ld_out;
     int M, S, heads, group;       // KV heads, query heads of each
-    int grid;
-    int4 *joins;                  // [grid]: sequence, head, block of rows, parts that follow the first
+    int teams, members;
+    int4 *joins;                  // [team][member]: sequence, head, block of rows, parts that follow the first
     float *parts;                 // [grid][2] blocks of sums, then of (maximum, sum)
     float2 *stats;
 };
 
-// floor(n / page_size) for n < 2^31
-__device__ __forceinline__ uint32_t page_of(const Params &p, uint32_t n) {
-    return p.page_size == 1 ? n : __umulhi(n, p.page_magic) >> p.page_shift;
-}
-
 // A sequence's rows and the numbering of the tokens that they may see.
 struct Sequence {
-    int s, first, n;   // its rows
+    int first, n;      // its rows
     int len;           // cached tokens
     int sinks, from;   // tokens 0 .. sinks - 1 of the cache come first, then those from `from` on
     int cached;        // how many that are
-    int sink_pages, from_page;  // pages of the first ones, and the page that holds token `from`
     int cache_tiles;   // E4M3: tiles of cached tokens; the chunk's follow in tiles of their own
     int tiles;
-    int blocks;
+    int blocks, runs;  // blocks of rows; times that a team takes as many as it has members
 
-    template <bool E4M3>
-    __device__ __forceinline__ void load(const Params &p, int seq, int block_rows) {
-        s = seq;
+    __device__ __forceinline__ void read(const Params &p, int s) {
         first = min(max(p.starts[s], 0), p.M);
         n = max(min(p.starts[s + 1], p.M) - first, 0);
         len = min(max(p.lengths[s], 0), p.cache_tokens);
+    }
+    template <bool E4M3, int ROWS>
+    __device__ __forceinline__ void count(const Params &p) {
         sinks = 0;
         from = 0;
         if (p.window > 0) {
             sinks = min(max(p.sinks, 0), len);
             // the first row, at position len, sees the window's oldest token
-            from = max((int)max((int64_t)len - p.window + 1, (int64_t)0), sinks);
-            if (from > len) from = len;
+            from = min(max(max(len - p.window, -1) + 1, sinks), len);
         }
         cached = sinks + len - from;
-        sink_pages = sinks > 0 ? (int)page_of(p, sinks - 1) + 1 : 0;
-        from_page = (int)page_of(p, from);
-        cache_tiles = (int)(((int64_t)cached + kTile - 1) / kTile);
-        tiles = E4M3 ? cache_tiles + (int)(((int64_t)n + kTile - 1) / kTile)
-                     : (int)(((int64_t)cached + n + kTile - 1) / kTile);
-        blocks = (int)(((int64_t)n * p.group + block_rows - 1) / block_rows);
+        cache_tiles = (cached + kTile - 1) / kTile;
+        tiles = E4M3 ? cache_tiles + (n + kTile - 1) / kTile : (cached + n + kTile - 1) / kTile;
+        blocks = (n * p.group + ROWS - 1) / ROWS;
+        runs = ((uint32_t)blocks + p.members - 1) / p.members;
     }
     // place in the table of the cached token numbered u
     __device__ __forceinline__ int position(int u) const { return u < sinks ? u : u - sinks + from; }
-    // its page, of the pages in use counted without a gap
-    __device__ __forceinline__ int page(const Params &p, int u) const {
-        return u < sinks ? (int)page_of(p, u) : sink_pages + (int)page_of(p, u - sinks + from) - from_page;
-    }
-    __device__ __forceinline__ int64_t steps(const Params &p) const { return (int64_t)p.heads * blocks * tiles; }
+    __device__ __forceinline__ int steps(const Params &p) const { return p.heads * runs * tiles; }
 };
 
 // In LDS the 16-byte chunks of a tile's row stand at other places, by the row's number, so
@@ -166,10 +170,47 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // exp2(m - top) for a maximum m <= top; no weight has been seen below -inf
 __device__ __forceinline__ float decay(float m, float top) { return exp2_fast(m - (top == -INFINITY ? 0.f : top)); }
 
-// A value that all lanes hold, in scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
+// A value that all lanes hold, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The same value, computed from again where it is used: what is made of lane numbers would
+// otherwise be kept across the loop over tiles, in memory where registers are short, and
+// reading it back there would wait for all tiles in flight.
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Sums of the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_dpp(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = add_dpp<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v = add_dpp<0x112, 0xF>(v);
+    v = add_dpp<0x114, 0xF>(v);
+    v = add_dpp<0x118, 0xF>(v);
+    v = add_dpp<0x142, 0xA>(v);  // lane 15 of the row before, to rows 1 and 3
+    return add_dpp<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+}
+
+// The steps are shared as `q` for every team and one more for the first `r`.
+struct Shares {
+    uint32_t q, r;
+    __device__ __forceinline__ int begin(int team) const { return (int)(q * team + min((uint32_t)team, r)); }
+    __device__ __forceinline__ int team_of(uint32_t step) const {
+        const uint32_t head = (q + 1) * r;
+        return (int)(step < head ? step / (q + 1) : r + (step - head) / q);
+    }
+};
+
+// Waits until at most PER * n loads are in flight, n <= MOST.
+template <int PER, int MOST>
+__device__ __forceinline__ void wait_parts(int n) {
+    if constexpr (MOST == 0) wait_vmcnt<0>();
+    else if (n >= MOST) wait_vmcnt<PER * MOST>();
+    else wait_parts<PER, MOST - 1>(n);
 }
 
 // D elements a head; RT 16-row tiles a wave, WR waves over rows, WK waves over tokens.
@@ -179,102 +220,118 @@ struct Shape {
     static constexpr int kRows = 16 * RT * WR;
     static constexpr int kBlocks = kTile / 16 / WK;   // 16-token blocks of a tile that a wave takes
     static constexpr int kPart = kTile * D * (E4M3 ? 1 : 2);  // bytes of a tile's keys, or values
-    static constexpr int kJoin = WK / 2 * kRows * D * 4;      // of half the waves' sums
-    static constexpr int kArea = 4 * kPart > kJoin ? 4 * kPart : kJoin;
+    // Places for keys, and for values: as many as keep some 100 KiB a compute unit in flight (8 KiB
+    // pieces are not worth more waits)
+    static constexpr int kSlots = kPart >= 32768 ? 2 : 4;
+    static constexpr int kArea = 2 * kSlots * kPart;
     static constexpr int kOdd = 3 * kRows * D / 8;            // a bit each: infinities and NaN that rows see
-    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + 256 + kOdd;
+    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + kSlots * 8 + 256 + kOdd;
+    static_assert((WK - 1) * kRows * D * 4 <= kArea, "the waves' sums fit the tiles' place");
 };
 
 template <int D, bool E4M3, int RT, int WR, int WK>
 __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params p) {
     using Z = Shape<D, E4M3, RT, WR, WK>;
-    constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16;
+    constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16, SLOTS = Z::kSlots;
+    // keys of SLOTS tiles, values of as many; or one tile of bf16 beside an 8-bit cache; or sums
     __shared__ __attribute__((aligned(256))) char lds[Z::kLds];
-    // keys of two tiles, values of two; or one tile of bf16 beside an 8-bit cache; or sums
     uint64_t *const masks = (uint64_t *)(lds + Z::kArea);
     int *const staged = (int *)(masks + Z::kRows);
     int *const entries = staged + kStaged;
-    int64_t *const scratch = (int64_t *)(entries + kEntries);
-    uint32_t *const odd = (uint32_t *)(scratch + 32);  // [kind][row][D / 32]
+    uint64_t *const seen = (uint64_t *)(entries + kEntries);  // of the tiles in LDS, which tokens are there
+    int *const scratch = (int *)(seen + SLOTS);
+    uint32_t *const odd = (uint32_t *)(scratch + 64);         // [kind][row][D / 32]
     const uint32_t area = lds_addr(lds);
 
     const int lane = threadIdx.x & 63, wave = wave_id(), tid = threadIdx.x;
     const int wr = wave / WK, wk = wave % WK;
     const int col = lane & 15, quad = lane >> 4;
 
-    // ---- this workgroup's steps, of all sequences' in order ----
-    const int w = xcd_contiguous(blockIdx.x, p.grid);
+    // ---- this team's steps, of all sequences' in order ----
+    const int w = xcd_contiguous(blockIdx.x, p.teams * p.members);
+    const int team = (uint32_t)w / p.members, member = w - team * p.members;
     Sequence sq;
-    int64_t total, seq_at;  // all steps, and those before sq
-    int parts;
+    Shares shares;
+    int seq, seq_at, used;  // the sequence of the first step, the steps before it; teams with any
     {
         const int per = (p.S + Z::kThreads - 1) / Z::kThreads;
         const int s0 = min(tid * per, p.S), s1 = min(s0 + per, p.S);
         Sequence each;
-        int64_t sum = 0;
+        int sum = 0;
         for (int s = s0; s < s1; ++s) {
-            each.load<E4M3>(p, s, Z::kRows);
+            each.read(p, s);
+            each.count<E4M3, Z::kRows>(p);
             sum += each.steps(p);
         }
-        int64_t run = sum;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t up = __shfl_up(run, d);
-            if (lane >= d) run += up;
-        }
+        const int run = wave_scan(sum);
         if (lane == 63) scratch[wave] = run;
         __syncthreads();
-        int64_t before = run - sum, all = 0;
+        int before = run - sum, total = 0;
+#pragma unroll
         for (int i = 0; i < Z::kWaves; ++i) {
             if (i < wave) before += scratch[i];
-            all += scratch[i];
+            total += scratch[i];
         }
-        total = uniform(all);
-        parts = (int)min((int64_t)p.grid, total);
-        if (w >= parts) {
+        total = uniform(total);
+        used = min(p.teams, total);
+        if (team >= used) {
             if (tid == 0) p.joins[w] = make_int4(0, 0, 0, 0);
             return;
         }
-        __syncthreads();
-        const int64_t x0 = total * w / parts;
+        shares.q = (uint32_t)total / used;
+        shares.r = total - shares.q * used;
+        const int x0 = shares.begin(team);
         if (before <= x0 && x0 < before + sum) {
             int s = s0;
-            for (;; ++s) {
-                each.load<E4M3>(p, s, Z::kRows);
-                const int64_t st = each.steps(p);
+            while (per > 1) {
+                each.read(p, s);
+                each.count<E4M3, Z::kRows>(p);
+                const int st = each.steps(p);
                 if (x0 < before + st) break;
                 before += st;
+                ++s;
             }
-            scratch[0] = s;
-            scratch[1] = before;
+            scratch[16] = s;
+            scratch[17] = before;
+            scratch[18] = each.first;
+            scratch[19] = each.n;
+            scratch[20] = each.len;
         }
         __syncthreads();
-        sq.load<E4M3>(p, (int)uniform(scratch[0]), Z::kRows);
-        seq_at = uniform(scratch[1]);
+        seq = uniform(scratch[16]);
+        seq_at = uniform(scratch[17]);
+        sq.first = uniform(scratch[18]);
+        sq.n = uniform(scratch[19]);
+        sq.len = uniform(scratch[20]);
+        sq.count<E4M3, Z::kRows>(p);
     }
-    const int64_t end = total * (w + 1) / parts;
-    int64_t x = total * w / parts;
+    const int end = shares.begin(team + 1);
+    int x = shares.begin(team);
     int4 join = make_int4(0, 0, 0, 0);
 
     while (x < end) {
         while (x >= seq_at + sq.steps(p)) {
             seq_at += sq.steps(p);
-            sq.load<E4M3>(p, sq.s + 1, Z::kRows);
+            sq.read(p, ++seq);
+            sq.count<E4M3, Z::kRows>(p);
         }
-        const int64_t unit = (x - seq_at) / sq.tiles;
-        const int t0 = (int)(x - seq_at - unit * sq.tiles);
-        const int t1 = (int)min((int64_t)sq.tiles, t0 + (end - x));
-        const int h = (int)(unit / sq.blocks), block = (int)(unit % sq.blocks);
+        const int unit = (uint32_t)(x - seq_at) / (uint32_t)sq.tiles;
+        const int t0 = x - seq_at - unit * sq.tiles, t1 = min(sq.tiles, t0 + end - x);
+        const int h = (uint32_t)unit / (uint32_t)sq.runs, block = (unit - h * sq.runs) * p.members + member;
+        x += t1 - t0;
+        if (block >= sq.blocks) continue;
         const int rows = sq.n * p.group;  // (host: M * H < 2^31)
         const int row0 = block * Z::kRows;
+        auto node_of = [&](int r) { return p.by_group(r); };
+        auto head_of = [&](int r, int node) { return h * p.group + r - node * p.group; };
 
-        // ---- q, and each lane's rows ----
+        // ---- q; the parents; the pages of the first tiles ----
         uint4 qf[RT][C];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int r = row0 + (wr * RT + rt) * 16 + col;
-            const int node = r / p.group, head = h * p.group + r % p.group;
+            const int r = row0 + (wr * RT + rt) * 16 + col, node = node_of(r);
             // elements that a lane's keys hold: 8 of every 32, or 16 codes of every 64
-            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head * D);
+            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head_of(r, node) * D);
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 qf[rt][c] = r < rows ? src[E4M3 ? 8 * (c / 2) + 2 * quad + c % 2 : 4 * c + quad] : make_uint4(0, 0, 0, 0);
@@ -284,9 +341,30 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             if (p.k.scale) ks *= p.k.scale[h];
             if (p.v.scale) vs = p.v.scale[h];
         }
+        const int cut = E4M3 ? min(t1, sq.cache_tiles) : t1;  // tiles past it hold the chunk's rows alone
         const int32_t *parents = p.parents ? p.parents + sq.first : nullptr;
+        const int32_t *table = p.table + (int64_t)seq * p.ld_table;
+        // pages in use, counted without a gap between the first tokens' and the window's
+        const int sink_pages = sq.sinks > 0 ? p.by_page(sq.sinks - 1) + 1 : 0;
+        const int page_gap = p.by_page(sq.from) - sink_pages;
+        auto page_number = [&](int u, int page) { return u < sq.sinks ? page : page - page_gap; };
+        int entry0 = 0, entry1 = 0;  // those whose table entries LDS holds
+        auto look_up = [&](int base) {
+            if (base >= sq.cached) return;
+            const int last = min(base + kTile, sq.cached) - 1;
+            if (page_number(last, p.by_page(sq.position(last))) < entry1) return;
+            __syncthreads();
+            const int most = min(cut * kTile, sq.cached) - 1;
+            entry0 = page_number(base, p.by_page(sq.position(base)));
+            entry1 = min(entry0 + kEntries, page_number(most, p.by_page(sq.position(most))) + 1);
+            for (int i = fresh(tid); i < entry1 - entry0; i += Z::kThreads) {
+                const int c = entry0 + i;
+                entries[i] = table[c < sink_pages ? c : c + page_gap];
+            }
+            __syncthreads();
+        };
         __syncthreads();  // the last unit's reads of LDS are done
-        if (parents)
+        if (parents && (p.window > 0 || t1 * kTile > sq.cached))
             for (int i = tid; i < min(sq.n, kStaged); i += Z::kThreads) staged[i] = parents[i];
         auto parent_of = [&](int i) {
             const int up = i < kStaged ? staged[i] : parents[i];
@@ -303,61 +381,46 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             for (int dt = 0; dt < DT; ++dt) acc[rt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        const int cut = E4M3 ? min(t1, sq.cache_tiles) : t1;  // tiles past it hold the chunk's rows alone
-        int entry0 = 0, entry1 = 0;                            // pages whose table entries LDS holds
-
         // Where the tokens of a tile lie: lane i finds token base + i; kZeros for none. Returns
         // the bits of those that are there.
         uint64_t ka = 0, va = 0;
         const uint64_t k_cache = (uint64_t)(p.k.cache + h * p.k.head), v_cache = (uint64_t)(p.v.cache + h * p.v.head);
+        // (of the chunk's rows as if they began at token 0)
+        auto rows_from = [&](const Side &x) {
+            return (uint64_t)(x.rows + (int64_t)h * D) + ((int64_t)sq.first - sq.cached) * (int64_t)x.ld;
+        };
+        const uint64_t k_rows = rows_from(p.k), v_rows = rows_from(p.v);
         auto locate = [&](int base, int limit) {
-            const int u = base + lane;
+            const int u = base + fresh(lane);
             ka = va = (uint64_t)kZeros;
             bool there = false;
-            if (u < limit) {
-                if (u < sq.cached) {
-                    const int pos = sq.position(u);
-                    const uint32_t page = (uint32_t)entries[sq.page(p, u) - entry0];
-                    const uint32_t in = (uint32_t)pos - page_of(p, pos) * p.page_size;
-                    if (page < p.pages) {
-                        ka = k_cache + (uint64_t)page * p.k.page + (uint64_t)in * p.k.token;
-                        va = v_cache + (uint64_t)page * p.v.page + (uint64_t)in * p.v.token;
-                        there = true;
-                    }
-                } else {
-                    const int64_t m = sq.first + (u - sq.cached);
-                    ka = (uint64_t)(p.k.rows + m * p.k.ld + (int64_t)h * D);
-                    va = (uint64_t)(p.v.rows + m * p.v.ld + (int64_t)h * D);
+            if (u < min(limit, sq.cached)) {
+                const int pos = sq.position(u), page = p.by_page(pos);
+                const uint32_t entry = (uint32_t)entries[page_number(u, page) - entry0];
+                const uint32_t in = (uint32_t)pos - page * p.page_size;
+                if (entry < p.pages) {
+                    ka = k_cache + (uint64_t)entry * p.k.page + (uint64_t)in * p.k.token;
+                    va = v_cache + (uint64_t)entry * p.v.page + (uint64_t)in * p.v.token;
                     there = true;
                 }
+            } else if (u < limit) {
+                ka = k_rows + (uint64_t)(uint32_t)u * p.k.ld;
+                va = v_rows + (uint64_t)(uint32_t)u * p.v.ld;
+                there = true;
             }
             return __ballot(there);
-        };
-        // The table's entries for a tile, if they are not in LDS (for as many more as it holds).
-        auto look_up = [&](int base) {
-            if (base >= sq.cached) return;
-            const int last = sq.page(p, min(base + kTile, sq.cached) - 1);
-            if (last < entry1) return;
-            lds_barrier();
-            entry0 = sq.page(p, base);
-            entry1 = min(entry0 + kEntries, sq.page(p, min(cut * kTile, sq.cached) - 1) + 1);
-            const int32_t *table = p.table + (int64_t)sq.s * p.ld_table;
-            for (int i = tid; i < entry1 - entry0; i += Z::kThreads) {
-                const int c = entry0 + i;
-                entries[i] = table[c < sq.sink_pages ? c : c - sq.sink_pages + sq.from_page];
-            }
-            __syncthreads();
         };
         // A tile's rows of BYTES bytes into LDS, in pieces of 1 KiB that the waves share.
         auto fill = [&](auto row_bytes, uint64_t from, uint32_t to) {
             constexpr int BYTES = decltype(row_bytes)::value, CHUNKS = BYTES / 16, kPieces = kTile * BYTES / 1024;
             constexpr int kMine = kPieces > Z::kWaves ? kPieces / Z::kWaves : 1;
+            const int l = fresh(lane);
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int piece = wave * kMine + i;
                 if (kPieces < Z::kWaves && piece >= kPieces) break;
-                const int row = piece * (64 / CHUNKS) + lane / CHUNKS;
-                const int chunk = lane % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
+                const int row = piece * (64 / CHUNKS) + l / CHUNKS;
+                const int chunk = l % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
                 const uint64_t a = (uint64_t)__shfl((long long)from, row);
                 load_to_lds(a + chunk * 16, to + piece * 1024);
             }
@@ -372,8 +435,8 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             return p.window > 0 && base < (int64_t)sq.sinks + sq.n - 1 && base + kTile > sq.sinks;
         };
         auto make_masks = [&](int base, uint64_t there) {
-            for (int i = tid; i < Z::kRows; i += Z::kThreads) {
-                const int r = row0 + i, node = r / p.group;
+            for (int i = fresh(tid); i < Z::kRows; i += Z::kThreads) {
+                const int r = row0 + i, node = node_of(r);
                 uint64_t bits = 0;
                 if (r < rows) {
                     auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
@@ -414,6 +477,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             // chunk c of a row is at c ^ swizzle: the lane's own bits are in the address from the
             // start, those of an operand are changed or added to it
             constexpr bool WIDE = CODES || E4M3;  // a lane's two operands are neighbours
+            const int l = fresh(lane), col = l & 15, quad = l >> 4;
             const int row = wk * NB * 16 + col;
             const lds_u8 *const from = lds_opaque(keys + row * BYTES + ((WIDE && !CODES ? 2 * quad : quad) ^ swizzle<CHUNKS, CODES>(row)) * 16);
             auto chunk_at = [&](int b, int chunk) {
@@ -449,18 +513,24 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         auto weigh = [&](float to2, bool masked) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                uint64_t bits = ~0ull;
-                if (masked) bits = masks[(wr * RT + rt) * 16 + col] >> (wk * NB * 16 + 4 * quad);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sc[rt][b] *= to2;
+                if (masked) {
+                    const int l = fresh(lane), quad = l >> 4;
+                    const uint32_t *mask = (const uint32_t *)(masks + (wr * RT + rt) * 16 + (l & 15));
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t bits = mask[(wk * NB + b) / 2] >> (16 * ((wk * NB + b) & 1) + 4 * quad);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(bits >> i & 1)) sc[rt][b][i] = -INFINITY;
+                    }
+                }
                 float high = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float s = sc[rt][b][i] * to2;
-                        if (masked && !(bits >> (16 * b + i) & 1)) s = -INFINITY;
-                        sc[rt][b][i] = s;
-                        high = fmaxf(high, s);
-                    }
+                    for (int i = 0; i < 4; ++i) high = fmaxf(high, sc[rt][b][i]);
                 high = rows4_max(high);
                 if (__any(high > top[rt] + kSlack)) {
                     high = fmaxf(high, top[rt]);
@@ -488,11 +558,11 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         auto add_values = [&](auto codes, uint32_t values) {
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16, kMixed = CHUNKS < 16 ? CHUNKS - 1 : 15;
+            const int l = fresh(lane), col = l & 15, quad = l >> 4;
             const int row = wk * NB * 16 + 4 * quad + (CODES ? col >> 1 & 3 : col >> 2) + (CODES && NB > 1 ? col >> 3 << 4 : 0);
             const int chunk = CODES ? (NB == 1 ? col >> 3 : 0) : col >> 1 & 1;
             const uint32_t from = (uint32_t)(uintptr_t)lds_opaque(values + row * BYTES + (chunk ^ swizzle<CHUNKS, CODES>(row)) * 16 +
                                                                   (col & 1) * 8);
-            typedef int i32x2 __attribute__((ext_vector_type(2)));
             auto read = [&](int b, int chunk) {
                 const lds_u8 *at = (const lds_u8 *)(from ^ (chunk & kMixed) * 16) + (chunk & ~kMixed) * 16 + b * 16 * BYTES;
                 if constexpr (CODES)
@@ -548,7 +618,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16;
             auto each = [&](auto found) {
-                for (int i = tid; i < kTile * CHUNKS; i += Z::kThreads) {
+                for (int i = fresh(tid); i < kTile * CHUNKS; i += Z::kThreads) {
                     const uint4 v = ((const uint4 *)values)[i];
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                     for (int e = 0; e < (CODES ? 16 : 8); ++e) {
@@ -561,7 +631,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             each([&](int, int, uint32_t) { here = true; });
             if (!__syncthreads_or(here)) return;
             if (!any_odd)
-                for (int i = tid; i < Z::kOdd / 4; i += Z::kThreads) odd[i] = 0;
+                for (int i = fresh(tid); i < Z::kOdd / 4; i += Z::kThreads) odd[i] = 0;
             any_odd = true;
             __syncthreads();
             each([&](int i, int e, uint32_t y) {
@@ -576,156 +646,175 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         };
 
         // ---- the cache's tiles (bf16: and the chunk's rows) ----
-        // Keys and values have two places each. At the first barrier of a step its keys are
-        // there and the last step's values are done with: their place takes the next tile's.
-        // At the second its values are there and the keys' place takes those after the next.
-        if (t0 < cut) {
-            const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
-            look_up(t0 * kTile);
-            uint64_t there = locate(t0 * kTile, limit), next = 0, after = 0;
-            fill(cache_row, ka, area);
-            fill(cache_row, va, area + 2 * Z::kPart);
-            if (t0 + 1 < cut) {
-                look_up((t0 + 1) * kTile);
-                next = locate((t0 + 1) * kTile, limit);
-                fill(cache_row, ka, area + Z::kPart);
-            }
-            for (int t = t0; t < cut; ++t) {
-                const int at = (t - t0) & 1;
-                const uint32_t keys = area + at * Z::kPart, values = area + (2 + at) * Z::kPart;
-                const bool more = t + 1 < cut;
-                if (more) wait_vmcnt<2 * kMine>();
-                else wait_vmcnt<kMine>();
-                lds_barrier();
-                if (more) fill(cache_row, va, area + (3 - at) * Z::kPart);
-                const bool masked = needs_mask(t * kTile, there);
-                if (masked) {
-                    make_masks(t * kTile, there);
+        // Keys and values have SLOTS places each. At the first barrier of a tile's step its keys
+        // are there and the values of the one before are done with: their place takes those of the
+        // tile SLOTS - 1 further on. At the second its values are there and the keys' place takes
+        // those of the tile SLOTS further on. The first SLOTS steps only load.
+        const int count = cut - t0;
+        const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
+        uint32_t masked = 0;  // of the tiles in LDS, which need a mask: bit 0 the last located
+        // (the compiler knows of q's loads but not of the tiles': without this it would wait for all
+        // of them at q's first use, in every step)
+        wait_vmcnt<0>();
+        if (count > 0)
+            for (int i = -SLOTS; i < count; ++i) {
+                const int left = count - 1 - i;
+                if (i >= 0) {
+                    // loaded since: the tile's values, and keys and values of those after it
+                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                    else wait_parts<kMine, 2 * (SLOTS - 1)>(2 * left + 1);
                     lds_barrier();
                 }
-                scores(std::bool_constant<E4M3>{}, keys);
-                weigh(ks, masked);
-                if (more) wait_vmcnt<2 * kMine>();
-                else wait_vmcnt<0>();
-                lds_barrier();
-                if (t + 2 < cut) {
-                    look_up((t + 2) * kTile);
-                    after = locate((t + 2) * kTile, limit);
-                    fill(cache_row, ka, area + at * Z::kPart);
+                if (i + SLOTS > 0 && left >= SLOTS - 1)
+                    fill(cache_row, va, area + (SLOTS + ((i + SLOTS - 1) & (SLOTS - 1))) * Z::kPart);
+                const bool mask = masked >> (SLOTS - 1) & 1;
+                if (i >= 0) {
+                    if (mask) {
+                        make_masks((t0 + i) * kTile, seen[i & (SLOTS - 1)]);
+                        lds_barrier();
+                    }
+                    scores(std::bool_constant<E4M3>{}, area + (i & (SLOTS - 1)) * Z::kPart);
+                    weigh(ks, mask);
+                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                    else wait_parts<kMine, 2 * (SLOTS - 1)>(2 * left);
+                    lds_barrier();
                 }
-                if (masked) set_apart(std::bool_constant<E4M3>{}, lds + (2 + at) * Z::kPart);
-                add_values(std::bool_constant<E4M3>{}, values);
-                there = next;
-                next = after;
+                masked <<= 1;
+                if (left >= SLOTS) {
+                    const int base = (t0 + i + SLOTS) * kTile;
+                    look_up(base);
+                    const uint64_t there = locate(base, limit);
+                    if (tid == 0) seen[i & (SLOTS - 1)] = there;
+                    masked |= needs_mask(base, there);
+                    fill(cache_row, ka, area + (i & (SLOTS - 1)) * Z::kPart);
+                }
+                if (i >= 0) {
+                    if (mask) set_apart(std::bool_constant<E4M3>{}, lds + (SLOTS + (i & (SLOTS - 1))) * Z::kPart);
+                    add_values(std::bool_constant<E4M3>{}, area + (SLOTS + (i & (SLOTS - 1))) * Z::kPart);
+                }
             }
-            if (E4M3)
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
-        }
         // ---- beside an 8-bit cache, the chunk's rows ----
-        if constexpr (E4M3)
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
             for (int t = max(t0, sq.cache_tiles); t < t1; ++t) {
                 const int base = sq.cached + (t - sq.cache_tiles) * kTile;
                 const uint64_t there = locate(base, sq.cached + sq.n);
                 lds_barrier();
                 fill(bf16_row, ka, area);
-                fill(bf16_row, va, area + 2 * Z::kPart);
+                fill(bf16_row, va, area + kTile * 2 * D);
                 make_masks(base, there);
                 wait_vmcnt<0>();
                 lds_barrier();
                 scores(std::false_type{}, area);
                 weigh(p.scale, true);
-                set_apart(std::false_type{}, lds + 2 * Z::kPart);
-                add_values(std::false_type{}, area + 2 * Z::kPart);
+                set_apart(std::false_type{}, lds + kTile * 2 * D);
+                add_values(std::false_type{}, area + kTile * 2 * D);
             }
+        }
 
-        // ---- the sums of the four 16-lane rows, then of the waves over tokens ----
+        // ---- the waves over tokens meet: each gets its share of the columns from the others ----
+        constexpr int MINE = DT / WK;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sum[rt] = rows4_sum(sum[rt]);
+        if constexpr (WK > 1) {
+            lds_barrier();
+            float2 *const st = (float2 *)staged;  // [wave over tokens][row]
+            static_assert(WK * Z::kRows * 8 <= kStaged * 4, "statistics fit the parents' place");
 #pragma unroll
-        for (int half = WK / 2; half >= 1; half /= 2) {
-            __syncthreads();
-            float *const at = (float *)lds;
-            float2 *const st = (float2 *)masks;  // [waves over rows][half][16 RT], in place of masks and parents
-            static_assert(WK / 2 <= 2, "statistics fit the masks and the parents");
-            if (wk >= half && wk < 2 * half) {
-                const int slot = wr * half + wk - half;
+            for (int rt = 0; rt < RT; ++rt)
+                if (quad == 0) st[wk * Z::kRows + (wr * RT + rt) * 16 + col] = make_float2(top[rt], sum[rt]);
+            lds_barrier();
+            f32x4 *const give = (f32x4 *)lds;  // [wave over rows][to][from the one before it, ...][rt][column block][lane]
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if (quad == 0) st[(slot * RT + rt) * 16 + col] = make_float2(top[rt], sum[rt]);
+            for (int rt = 0; rt < RT; ++rt) {
+                float high = -INFINITY, all = 0.f;
+                float2 each[WK];
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) ((f32x4 *)at)[((slot * RT + rt) * DT + dt) * 64 + lane] = acc[rt][dt];
+                for (int v = 0; v < WK; ++v) {
+                    each[v] = st[v * Z::kRows + (wr * RT + rt) * 16 + col];
+                    high = fmaxf(high, each[v].x);
+                }
+#pragma unroll
+                for (int v = 0; v < WK; ++v) all += each[v].y * decay(each[v].x, high);
+                const float down = decay(top[rt], high);
+                top[rt] = high;
+                sum[rt] = all;
+#pragma unroll
+                for (int v = 0; v < WK; ++v) {
+                    const int k = wk > v ? wk - v - 1 : wk - v + WK - 1;  // this wave's place among those that give to v
+#pragma unroll
+                    for (int d = 0; d < MINE; ++d) {
+                        acc[rt][v * MINE + d] *= down;
+                        if (v != wk)
+                            give[((((wr * WK + v) * (WK - 1) + k) * RT + rt) * MINE + d) * 64 + lane] =
+                                acc[rt][v * MINE + d];
+                    }
                 }
             }
-            __syncthreads();
-            if (wk < half) {
-                const int slot = wr * half + wk;
+            lds_barrier();
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float2 o = st[(slot * RT + rt) * 16 + col];
-                    const float high = fmaxf(top[rt], o.x);
-                    const float a = decay(top[rt], high), b = decay(o.x, high);
-                    top[rt] = high;
-                    sum[rt] = sum[rt] * a + o.y * b;
+            for (int v = 0; v < WK; ++v)
+                if (v == wk)
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-                        acc[rt][dt] = acc[rt][dt] * a + ((f32x4 *)at)[((slot * RT + rt) * DT + dt) * 64 + lane] * b;
-                }
-            }
+                    for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int d = 0; d < MINE; ++d)
+                                acc[rt][v * MINE + d] +=
+                                    give[((((wr * WK + v) * (WK - 1) + k) * RT + rt) * MINE + d) * 64 + lane];
         }
 
         // ---- out, or a part of it ----
         const bool whole = t0 == 0 && t1 == sq.tiles;
-        if (wk == 0) {
-            const int64_t slot = 2 * (int64_t)w + (t0 == 0);
+        const int64_t slot = 2 * (int64_t)w + (t0 == 0);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int i = (wr * RT + rt) * 16 + col, r = row0 + i;
-                if (r >= rows) continue;
-                if (whole) {
-                    const int node = r / p.group, head = h * p.group + r % p.group;
-                    uint16_t *o = p.out + (int64_t)(sq.first + node) * p.ld_out + (int64_t)head * D + 4 * quad;
-                    const float inv = sum[rt] == 0.f ? 0.f : 1.f / sum[rt];
+        for (int v = 0; v < WK; ++v)
+            if (v == wk)
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        const f32x4 a = acc[rt][dt] * inv;
-                        *(uint2 *)(o + 16 * dt) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int i = (wr * RT + rt) * 16 + col, r = row0 + i, node = node_of(r);
+                    if (r >= rows) continue;
+                    if (whole) {
+                        uint16_t *o = p.out + (int64_t)(sq.first + node) * p.ld_out + (int64_t)head_of(r, node) * D +
+                                      16 * v * MINE + 4 * quad;
+                        const float inv = sum[rt] == 0.f ? 0.f : 1.f / sum[rt];
+#pragma unroll
+                        for (int d = 0; d < MINE; ++d) {
+                            const f32x4 a = acc[rt][v * MINE + d] * inv;
+                            *(uint2 *)(o + 16 * d) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
+                        }
+                    } else {
+                        float *o = p.parts + (slot * Z::kRows + i) * D + 16 * v * MINE + 4 * quad;
+#pragma unroll
+                        for (int d = 0; d < MINE; ++d) *(f32x4 *)(o + 16 * d) = acc[rt][v * MINE + d];
+                        if (v == 0 && quad == 0) p.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
                     }
-                } else {
-                    float *o = p.parts + (slot * Z::kRows + i) * D + 4 * quad;
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) *(f32x4 *)(o + 16 * dt) = acc[rt][dt];
-                    if (quad == 0) p.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
                 }
-            }
-        }
         if (any_odd) {
             // infinities and NaN that rows see
             __threadfence_block();
             __syncthreads();
             for (int i = tid; i < Z::kRows * D; i += Z::kThreads) {
-                const int at = i / D, d = i % D, r = row0 + at;
+                const int at = i / D, d = i % D, r = row0 + at, node = node_of(r);
                 auto is = [&](int kind) { return odd[(kind * Z::kRows * D + i) / 32] >> (d & 31) & 1; };
                 const bool up = is(0), down = is(1);
                 if (r >= rows || !(up || down || is(2))) continue;
                 const float add = is(2) || (up && down) ? NAN : up ? INFINITY : -INFINITY;
                 if (whole) {
-                    uint16_t *o = p.out + (int64_t)(sq.first + r / p.group) * p.ld_out + (int64_t)(h * p.group + r % p.group) * D + d;
+                    uint16_t *o = p.out + (int64_t)(sq.first + node) * p.ld_out + (int64_t)head_of(r, node) * D + d;
                     *o = f32_to_bf16_rne(bits_f32((uint32_t)*o << 16) + add);
                 } else {
-                    p.parts[((2 * (int64_t)w + (t0 == 0)) * Z::kRows + at) * D + d] += add;
+                    p.parts[(slot * Z::kRows + at) * D + d] += add;
                 }
             }
         }
-        if (t0 == 0 && t1 < sq.tiles) {
-            // the parts that follow: one a workgroup, up to the one with this unit's last step
-            const int64_t last = x + sq.tiles - 1;
-            const int64_t to = ((last + 1) * parts - 1) / total;
-            join = make_int4(sq.s, h, block, (int)(to - w));
-        }
-        x += t1 - t0;
+        if (t0 == 0 && t1 < sq.tiles)
+            // the parts that follow: one a team, up to the one with this unit's last step
+            join = make_int4(seq, h, block, shares.team_of(x - t1 + sq.tiles - 1) - team);
     }
     if (tid == 0) p.joins[w] = join;
 }
@@ -749,7 +838,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
         const bool here = r < n * p.group;
         float top = -INFINITY, sum = 0.f;
         row_t acc = 0.f;
-        auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part)) * ROWS + i; };
+        auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part * p.members)) * ROWS + i; };
         if (here)
             // 64 parts at a time: lane l's statistics, then the values by their weights
             for (int p0 = wave % RW; p0 <= j.w; p0 += 64 * RW) {
@@ -804,10 +893,17 @@ AttendPlan plan_tree_attention(int64_t M, int64_t S, int64_t H, int64_t KVH, int
     AttendPlan p{};
     const int64_t rows = (M * (H / KVH) + S - 1) / S;  // of a sequence, on average
     p.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    // workgroups that a compute unit's LDS and registers hold at once
-    p.grid = num_cus * (D == 256 ? 1 : 2);
-    const size_t slots = 2 * (size_t)p.grid * p.block_rows;
-    p.workspace_bytes = kCounterBytes + (((size_t)p.grid * 16 + 255) & ~(size_t)255) + slots * (D * 4 + 8);
+    // A sequence's blocks of rows read the same tokens: up to 8 workgroups take them side by side.
+    // Of the numbers of members that leave fewest idle the largest.
+    const int64_t blocks = (rows + p.block_rows - 1) / p.block_rows;
+    p.members = 1;
+    for (int64_t m = 2; m <= 8 && m <= blocks; ++m) {
+        auto places = [&](int64_t k) { return (blocks + k - 1) / k * k; };
+        if (places(m) <= places(p.members)) p.members = (int)m;
+    }
+    p.teams = std::max(1, num_cus / p.members);
+    const size_t groups = (size_t)p.teams * p.members;
+    p.workspace_bytes = kCounterBytes + ((groups * 16 + 255) & ~(size_t)255) + 2 * groups * p.block_rows * (D * 4 + 8);
     return p;
 }
 
@@ -817,10 +913,10 @@ template <int D, bool E4M3, int RT, int WR, int WK>
 hipError_t launch_shape(const Params &p, hipStream_t stream) {
     using Z = Shape<D, E4M3, RT, WR, WK>;
     auto kernel = attend_kernel<D, E4M3, RT, WR, WK>;
-    hipLaunchKernelGGL(kernel, dim3(p.grid), dim3(Z::kThreads), 0, stream, p);
+    hipLaunchKernelGGL(kernel, dim3(p.teams * p.members), dim3(Z::kThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.grid, 16), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.teams * p.members, 16), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -852,7 +948,7 @@ hipError_t launch_tree_attention(const AttendPlan &plan, const void *q, int64_t 
     p.ld_q = ld_q;
     auto side = [&](const void *cache, const int64_t *st, const float *by, const void *rows, int64_t ld) {
         return Side{(const char *)cache, (uint32_t)(st[0] * size), (uint32_t)(st[1] * size), st[2] * size, by,
-                    (const uint16_t *)rows, ld};
+                    (const uint16_t *)rows, (uint32_t)(ld * 2)};
     };
     p.k = side(c.k, c.k_strides, c.k_scale, k, ld_k);
     p.v = side(c.v, c.v_strides, c.v_scale, v, ld_v);
@@ -863,13 +959,7 @@ hipError_t launch_tree_attention(const AttendPlan &plan, const void *q, int64_t 
     p.parents = parents;
     p.pages = (uint32_t)c.pages;
     p.page_size = (uint32_t)c.page_size;
-    // n / d = n * ceil(2^(31 + L) / d) >> (31 + L) for every n < 2^31, with 2^(L-1) < d <= 2^L
-    int L = 0;
-    while ((int64_t(1) << L) < c.page_size) ++L;
-    if (L) {
-        p.page_magic = (uint32_t)(((uint64_t(1) << (31 + L)) + c.page_size - 1) / c.page_size);
-        p.page_shift = (uint32_t)(L - 1);
-    }
+    p.by_page = Divide::by(p.page_size);
     p.cache_tokens = (int)((int64_t)c.max_pages * c.page_size);
     p.scale = scale * 1.44269504088896340736f;
     p.window = window;
@@ -880,10 +970,13 @@ hipError_t launch_tree_attention(const AttendPlan &plan, const void *q, int64_t 
     p.S = (int)S;
     p.heads = KVH;
     p.group = H / KVH;
-    p.grid = plan.grid;
+    p.by_group = Divide::by(p.group);
+    p.teams = plan.teams;
+    p.members = plan.members;
+    const size_t groups = (size_t)plan.teams * plan.members;
     p.joins = (int4 *)ws_partials(workspace);
-    p.parts = (float *)((char *)p.joins + (((size_t)plan.grid * 16 + 255) & ~(size_t)255));
-    p.stats = (float2 *)(p.parts + 2 * (size_t)plan.grid * plan.block_rows * D);
+    p.parts = (float *)((char *)p.joins + ((groups * 16 + 255) & ~(size_t)255));
+    p.stats = (float2 *)(p.parts + 2 * groups * plan.block_rows * D);
     switch (D) {
     case 64: return launch_type<64>(p, plan.block_rows, e4m3, stream);
     case 128: return launch_type<128>(p, plan.block_rows, e4m3, stream);
