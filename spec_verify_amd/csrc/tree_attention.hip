@@ -135,9 +135,10 @@ __device__ __forceinline__ int swizzle(int row) {
 __device__ __attribute__((aligned(16))) const uint4 kZeros[32] = {};
 
 // 16 bytes a lane from memory into LDS, lane i's at lds + 16 i. (Not counted by the compiler,
-// which would wait for all loads in flight before each read of LDS: the waits are explicit.)
+// which would wait for all loads in flight before each read of LDS: the waits are explicit.
+// Reads of other places may pass it; barriers, which are volatile too, may not.)
 __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(from), "s"(lds) : "m0");
 }
 
 // Eight E4M3 codes as bf16 (exact).
@@ -179,6 +180,14 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ int fresh(int v) {
     asm volatile("" : "+v"(v));
     return v;
+}
+
+// The kernel's arguments, read from memory again where this is called: kept in scalar
+// registers throughout, they would push others (and those vector registers) out.
+__device__ __forceinline__ const Params &arguments() {
+    auto a = (const __attribute__((address_space(4))) Params *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return *(const Params *)a;
 }
 
 // Sums of the lanes up to each.
@@ -223,23 +232,27 @@ struct Shape {
     // Places for keys, and for values: as many as keep some 100 KiB a compute unit in flight (8 KiB
     // pieces are not worth more waits)
     static constexpr int kSlots = kPart >= 32768 ? 2 : 4;
+    static constexpr bool kLag = kRows >= 128 && kWaves == 8;  // products, not bytes
     static constexpr int kArea = 2 * kSlots * kPart;
+    // groups of operands read from LDS before their use: as registers allow
+    static constexpr int kAhead = D * RT >= 512 ? 2 : 4;
     static constexpr int kOdd = 3 * kRows * D / 8;            // a bit each: infinities and NaN that rows see
-    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + kSlots * 8 + 256 + kOdd;
+    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + kSlots * 16 + 256 + kOdd;
     static_assert((WK - 1) * kRows * D * 4 <= kArea, "the waves' sums fit the tiles' place");
 };
 
 template <int D, bool E4M3, int RT, int WR, int WK>
-__global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params p) {
+__global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params) {
+    const Params &p = arguments();
     using Z = Shape<D, E4M3, RT, WR, WK>;
-    constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16, SLOTS = Z::kSlots;
+    constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16, SLOTS = Z::kSlots, kAhead = Z::kAhead;
     // keys of SLOTS tiles, values of as many; or one tile of bf16 beside an 8-bit cache; or sums
     __shared__ __attribute__((aligned(256))) char lds[Z::kLds];
     uint64_t *const masks = (uint64_t *)(lds + Z::kArea);
     int *const staged = (int *)(masks + Z::kRows);
     int *const entries = staged + kStaged;
     uint64_t *const seen = (uint64_t *)(entries + kEntries);  // of the tiles in LDS, which tokens are there
-    int *const scratch = (int *)(seen + SLOTS);
+    int *const scratch = (int *)(seen + 2 * SLOTS);
     uint32_t *const odd = (uint32_t *)(scratch + 64);         // [kind][row][D / 32]
     const uint32_t area = lds_addr(lds);
 
@@ -310,6 +323,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
     int4 join = make_int4(0, 0, 0, 0);
 
     while (x < end) {
+        const Params &p = arguments();
         while (x >= seq_at + sq.steps(p)) {
             seq_at += sq.steps(p);
             sq.read(p, ++seq);
@@ -322,16 +336,16 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         if (block >= sq.blocks) continue;
         const int rows = sq.n * p.group;  // (host: M * H < 2^31)
         const int row0 = block * Z::kRows;
-        auto node_of = [&](int r) { return p.by_group(r); };
-        auto head_of = [&](int r, int node) { return h * p.group + r - node * p.group; };
+        auto node_of = [&](const Params &p, int r) { return p.by_group(r); };
+        auto head_of = [&](const Params &p, int r, int node) { return h * p.group + r - node * p.group; };
 
         // ---- q; the parents; the pages of the first tiles ----
         uint4 qf[RT][C];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int r = row0 + (wr * RT + rt) * 16 + col, node = node_of(r);
+            const int r = row0 + (wr * RT + rt) * 16 + col, node = node_of(p, r);
             // elements that a lane's keys hold: 8 of every 32, or 16 codes of every 64
-            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head_of(r, node) * D);
+            const uint4 *src = (const uint4 *)(p.q + (int64_t)(sq.first + node) * p.ld_q + (int64_t)head_of(p, r, node) * D);
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 qf[rt][c] = r < rows ? src[E4M3 ? 8 * (c / 2) + 2 * quad + c % 2 : 4 * c + quad] : make_uint4(0, 0, 0, 0);
@@ -342,21 +356,26 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             if (p.v.scale) vs = p.v.scale[h];
         }
         const int cut = E4M3 ? min(t1, sq.cache_tiles) : t1;  // tiles past it hold the chunk's rows alone
-        const int32_t *parents = p.parents ? p.parents + sq.first : nullptr;
-        const int32_t *table = p.table + (int64_t)seq * p.ld_table;
+        const int32_t *const parents = p.parents ? p.parents + sq.first : nullptr;
         // pages in use, counted without a gap between the first tokens' and the window's
         const int sink_pages = sq.sinks > 0 ? p.by_page(sq.sinks - 1) + 1 : 0;
         const int page_gap = p.by_page(sq.from) - sink_pages;
+        const Divide by_page = p.by_page;
         auto page_number = [&](int u, int page) { return u < sq.sinks ? page : page - page_gap; };
         int entry0 = 0, entry1 = 0;  // those whose table entries LDS holds
+        bool all_entries = false;    // LDS holds those of all tiles that follow
         auto look_up = [&](int base) {
-            if (base >= sq.cached) return;
+            if (all_entries || base >= sq.cached) return;
             const int last = min(base + kTile, sq.cached) - 1;
-            if (page_number(last, p.by_page(sq.position(last))) < entry1) return;
+            if (page_number(last, by_page(sq.position(last))) < entry1) return;
             __syncthreads();
+            const Params &p = arguments();
+            const int32_t *table = p.table + (int64_t)seq * p.ld_table;
             const int most = min(cut * kTile, sq.cached) - 1;
             entry0 = page_number(base, p.by_page(sq.position(base)));
-            entry1 = min(entry0 + kEntries, page_number(most, p.by_page(sq.position(most))) + 1);
+            entry1 = page_number(most, p.by_page(sq.position(most))) + 1;
+            all_entries = entry1 <= entry0 + kEntries;
+            entry1 = min(entry1, entry0 + kEntries);
             for (int i = fresh(tid); i < entry1 - entry0; i += Z::kThreads) {
                 const int c = entry0 + i;
                 entries[i] = table[c < sink_pages ? c : c + page_gap];
@@ -390,53 +409,56 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             return (uint64_t)(x.rows + (int64_t)h * D) + ((int64_t)sq.first - sq.cached) * (int64_t)x.ld;
         };
         const uint64_t k_rows = rows_from(p.k), v_rows = rows_from(p.v);
+        const uint32_t pages = p.pages, page_size = p.page_size, k_page = p.k.page, k_token = p.k.token, v_page = p.v.page,
+                       v_token = p.v.token;
         auto locate = [&](int base, int limit) {
-            const int u = base + fresh(lane);
-            ka = va = (uint64_t)kZeros;
-            bool there = false;
-            if (u < min(limit, sq.cached)) {
-                const int pos = sq.position(u), page = p.by_page(pos);
-                const uint32_t entry = (uint32_t)entries[page_number(u, page) - entry0];
-                const uint32_t in = (uint32_t)pos - page * p.page_size;
-                if (entry < p.pages) {
-                    ka = k_cache + (uint64_t)entry * p.k.page + (uint64_t)in * p.k.token;
-                    va = v_cache + (uint64_t)entry * p.v.page + (uint64_t)in * p.v.token;
-                    there = true;
-                }
-            } else if (u < limit) {
-                ka = k_rows + (uint64_t)(uint32_t)u * p.k.ld;
-                va = v_rows + (uint64_t)(uint32_t)u * p.v.ld;
-                there = true;
+            const int u = base + fresh(lane), last = min(limit, sq.cached);
+            const int uc = min(u, max(last, 1) - 1);  // (a tile of the chunk's rows alone reads any entry)
+            const int pos = sq.position(uc), page = by_page(pos);
+            const uint32_t entry = (uint32_t)entries[base < last ? page_number(uc, page) - entry0 : 0];
+            const uint32_t in = (uint32_t)pos - page * page_size;
+            bool there = u < last && entry < pages;
+            ka = there ? k_cache + (uint64_t)entry * k_page + (uint64_t)in * k_token : (uint64_t)kZeros;
+            va = there ? v_cache + (uint64_t)entry * v_page + (uint64_t)in * v_token : (uint64_t)kZeros;
+            if (base + kTile > last && last < limit) {
+                const Params &p = arguments();
+                const bool row = u >= last && u < limit;
+                ka = row ? k_rows + (uint64_t)(uint32_t)u * p.k.ld : ka;
+                va = row ? v_rows + (uint64_t)(uint32_t)u * p.v.ld : va;
+                there |= row;
             }
             return __ballot(there);
         };
-        // A tile's rows of BYTES bytes into LDS, in pieces of 1 KiB that the waves share.
-        auto fill = [&](auto row_bytes, uint64_t from, uint32_t to) {
+        // A tile's rows of BYTES bytes into LDS, in pieces of 1 KiB that the waves share: this
+        // wave's i-th.
+        auto fill_piece = [&](auto row_bytes, uint64_t from, uint32_t to, int i) {
             constexpr int BYTES = decltype(row_bytes)::value, CHUNKS = BYTES / 16, kPieces = kTile * BYTES / 1024;
             constexpr int kMine = kPieces > Z::kWaves ? kPieces / Z::kWaves : 1;
-            const int l = fresh(lane);
+            const int l = fresh(lane), piece = wave * kMine + i;
+            if (kPieces < Z::kWaves && piece >= kPieces) return;
+            const int row = piece * (64 / CHUNKS) + l / CHUNKS;
+            const int chunk = l % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
+            const uint64_t a = (uint64_t)__shfl((long long)from, row);
+            load_to_lds(a + chunk * 16, to + piece * 1024);
+        };
+        auto fill = [&](auto row_bytes, uint64_t from, uint32_t to) {
+            constexpr int kPieces = kTile * decltype(row_bytes)::value / 1024;
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int piece = wave * kMine + i;
-                if (kPieces < Z::kWaves && piece >= kPieces) break;
-                const int row = piece * (64 / CHUNKS) + l / CHUNKS;
-                const int chunk = l % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
-                const uint64_t a = (uint64_t)__shfl((long long)from, row);
-                load_to_lds(a + chunk * 16, to + piece * 1024);
-            }
+            for (int i = 0; i < (kPieces > Z::kWaves ? kPieces / Z::kWaves : 1); ++i) fill_piece(row_bytes, from, to, i);
         };
         constexpr int kMine = Z::kPart / 1024 > Z::kWaves ? Z::kPart / 1024 / Z::kWaves : 1;  // pieces a wave loads at once
         constexpr std::integral_constant<int, D * (E4M3 ? 1 : 2)> cache_row{};
         constexpr std::integral_constant<int, 2 * D> bf16_row{};
 
         // tiles that every row sees whole need no mask
+        const int edge = p.window > 0 ? sq.sinks + sq.n - 1 : 0;  // (n - 1: no row is deeper)
         auto needs_mask = [&](int base, uint64_t there) {
-            if (~there != 0 || base + kTile > sq.cached) return true;
-            return p.window > 0 && base < (int64_t)sq.sinks + sq.n - 1 && base + kTile > sq.sinks;
+            return ~there != 0 || base + kTile > sq.cached || (base < edge && base + kTile > sq.sinks);
         };
         auto make_masks = [&](int base, uint64_t there) {
+            const Params &p = arguments();
             for (int i = fresh(tid); i < Z::kRows; i += Z::kThreads) {
-                const int r = row0 + i, node = node_of(r);
+                const int r = row0 + i, node = node_of(p, r);
                 uint64_t bits = 0;
                 if (r < rows) {
                     auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
@@ -471,7 +493,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         f32x4 sc[RT][NB];
         uint2 wt[RT][NB];  // bf16 weights of tokens 4 quad .. 4 quad + 3 of each block
         // scores of this wave's blocks of tokens, from keys in LDS
-        auto scores = [&](auto codes, uint32_t keys) {
+        auto scores = [&](auto codes, uint32_t keys, auto between) {
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16;
             // chunk c of a row is at c ^ swizzle: the lane's own bits are in the address from the
@@ -486,26 +508,35 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                                 (chunk & ~kMixed) * 16 + b * 16 * BYTES);
             };
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) sc[rt][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // groups of one operand (of codes two), the blocks in turn, read kAhead groups before
+            // their use
+            constexpr int PER = CODES ? 2 : 1, GROUPS = NB * C / PER;
+            auto read = [&](int g) {
+                const int b = g % NB, c = g / NB * PER;
+                // (codes: the next block's swizzle differs in its highest bit)
+                if constexpr (CODES) return chunk_at(b, 2 * c ^ (b % 2 ? (CHUNKS < 16 ? CHUNKS / 2 : 8) : 0));
+                else return chunk_at(b, WIDE ? 4 * (c & ~1) + c % 2 : 4 * c);
+            };
+            uint4 raw[kAhead + 1];
 #pragma unroll
-                for (int c = 0; c < C; c += 2) {
-                    uint4 kf[2];
-                    if constexpr (CODES) {
-                        // (the next block's swizzle differs in its highest bit)
-                        const uint4 x = chunk_at(b, 2 * c ^ (b % 2 ? (CHUNKS < 16 ? CHUNKS / 2 : 8) : 0));
-                        kf[0] = decode8(x.x, x.y);
-                        kf[1] = decode8(x.z, x.w);
-                    } else {
+            for (int g = 0; g < kAhead && g < GROUPS; ++g) raw[g] = read(g);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) kf[e] = chunk_at(b, WIDE ? 4 * c + e : 4 * (c + e));
-                    }
+            for (int g = 0; g < GROUPS; ++g) {
+                if (g + kAhead < GROUPS) raw[(g + kAhead) % (kAhead + 1)] = read(g + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+                const uint4 r = raw[g % (kAhead + 1)];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < PER; ++e) {
+                    const uint4 kf = !CODES ? r : e ? decode8(r.z, r.w) : decode8(r.x, r.y);
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) sc[rt][b] = mfma16x16x32(kf[e], qf[rt][c + e], sc[rt][b]);
+                    for (int rt = 0; rt < RT; ++rt)
+                        sc[rt][g % NB] = mfma16x16x32(kf, qf[rt][g / NB * PER + e], sc[rt][g % NB]);
                 }
+                between(g, GROUPS);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         // their weights, relative to a maximum that follows the scores' once these pass it by
@@ -555,7 +586,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         // The weighted values of a tile in LDS. A transposed read gives a lane 4 tokens of its
         // column (4 quad .. 4 quad + 3 of a block), of codes 8: of two blocks of tokens, or (a wave
         // with one) of two blocks of columns.
-        auto add_values = [&](auto codes, uint32_t values) {
+        auto add_values = [&](auto codes, uint32_t values, auto between) {
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16, kMixed = CHUNKS < 16 ? CHUNKS - 1 : 15;
             const int l = fresh(lane), col = l & 15, quad = l >> 4;
@@ -571,44 +602,46 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                     return __builtin_bit_cast(
                         i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at));
             };
+            // groups of one block of columns (of codes, where a wave has one block of tokens, two)
+            constexpr int PER = CODES && NB == 1 ? 2 : 1, GROUPS = (NB + 1) / 2 * (DT / PER), READS = CODES || NB == 1 ? 1 : 2;
+            struct Raw {
+                i32x2 x[READS];
+            };
+            auto read_group = [&](int g) {
+                const int b = g / (DT / PER) * 2, dt = g % (DT / PER) * PER;
+                Raw r;
 #pragma unroll
-            for (int b = 0; b < NB; b += 2)
+                for (int k = 0; k < READS; ++k) r.x[k] = read(b + k, CODES ? dt : 2 * dt);
+                return r;
+            };
+            Raw raw[kAhead + 1];
 #pragma unroll
-                for (int dt = 0; dt < DT; dt += 2) {
-                    uint4 a[2];  // of columns 16 dt and 16 dt + 16: a block's tokens, and the next one's
-                    if constexpr (CODES && NB == 1) {
-                        const i32x2 x = read(0, dt);
-                        const uint4 d = decode8(x[0], x[1]);
-                        a[0] = d;
-                        a[1] = make_uint4(d.z, d.w, 0, 0);
-                    } else if constexpr (CODES) {
+            for (int g = 0; g < kAhead && g < GROUPS; ++g) raw[g] = read_group(g);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const i32x2 x = read(b, dt + e);
-                            a[e] = decode8(x[0], x[1]);
-                        }
+            for (int g = 0; g < GROUPS; ++g) {
+                if (g + kAhead < GROUPS) raw[(g + kAhead) % (kAhead + 1)] = read_group(g + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+                const int b = g / (DT / PER) * 2, dt = g % (DT / PER) * PER;
+                const Raw &r = raw[g % (kAhead + 1)];
+                uint4 a;  // a block's tokens and the next one's, or two blocks of columns
+                if constexpr (CODES) a = decode8(r.x[0][0], r.x[0][1]);
+                else if constexpr (NB == 1) a = make_uint4(r.x[0][0], r.x[0][1], 0, 0);
+                else a = make_uint4(r.x[0][0], r.x[0][1], r.x[READS - 1][0], r.x[READS - 1][1]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    if constexpr (NB == 1) {
+#pragma unroll
+                        for (int e = 0; e < PER; ++e)
+                            acc[rt][dt + e] = mfma16x16x16(__builtin_bit_cast(s16x4, e ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y)),
+                                                           __builtin_bit_cast(s16x4, wt[rt][0]), acc[rt][dt + e]);
                     } else {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const i32x2 x = read(b, 2 * (dt + e));
-                            i32x2 y = {};
-                            if (NB > 1) y = read(b + 1, 2 * (dt + e));
-                            a[e] = make_uint4(x[0], x[1], y[0], y[1]);
-                        }
+                        acc[rt][dt] = mfma16x16x32(
+                            a, make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x, wt[rt][b + 1].y), acc[rt][dt]);
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            if constexpr (NB == 1)
-                                acc[rt][dt + e] = mfma16x16x16(__builtin_bit_cast(s16x4, make_uint2(a[e].x, a[e].y)),
-                                                               __builtin_bit_cast(s16x4, wt[rt][0]), acc[rt][dt + e]);
-                            else
-                                acc[rt][dt + e] = mfma16x16x32(
-                                    a[e], make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x, wt[rt][b + 1].y),
-                                    acc[rt][dt + e]);
-                        }
                 }
+                between(g, GROUPS);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
         // In a tile that some row does not see whole, 0 * infinity must not reach the rows that do
         // not see it: infinities and NaN become zeros there, and the rows that see one get it when
@@ -618,81 +651,162 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16;
             auto each = [&](auto found) {
-                for (int i = fresh(tid); i < kTile * CHUNKS; i += Z::kThreads) {
-                    const uint4 v = ((const uint4 *)values)[i];
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    for (int e = 0; e < (CODES ? 16 : 8); ++e) {
-                        const uint32_t y = CODES ? x[e / 4] >> (8 * (e % 4)) & 0xFF : x[e / 2] >> (16 * (e % 2)) & 0xFFFF;
-                        if (CODES ? (y & 0x7F) == 0x7F : (y & 0x7F80) == 0x7F80) found(i, e, y);
+                const uint32_t *const words = (const uint32_t *)values;
+#pragma unroll 2
+                for (int i = fresh(tid); i < kTile * BYTES / 4; i += Z::kThreads) {
+                    const uint32_t x = words[i];
+                    if (CODES) {  // 0x7F and 0xFF: all ones but the sign
+                        const uint32_t y = ~x & 0x7F7F7F7Fu;
+                        if ((y - 0x01010101u) & ~y & 0x80808080u) found(i, x);
+                    } else if ((x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u) {
+                        found(i, x);
                     }
                 }
             };
             bool here = false;
-            each([&](int, int, uint32_t) { here = true; });
+            each([&](int, uint32_t) { here = true; });
             if (!__syncthreads_or(here)) return;
             if (!any_odd)
                 for (int i = fresh(tid); i < Z::kOdd / 4; i += Z::kThreads) odd[i] = 0;
             any_odd = true;
             __syncthreads();
-            each([&](int i, int e, uint32_t y) {
-                const int row = i / CHUNKS, d = ((i % CHUNKS) ^ swizzle<CHUNKS, CODES>(row)) * (CODES ? 16 : 8) + e;
-                const int kind = CODES || (y & 0x7F) ? 2 : y >> 15;  // 0 inf, 1 -inf, 2 NaN
-                for (int r = 0; r < Z::kRows; ++r)
-                    if (masks[r] >> row & 1) atomicOr(&odd[((kind * Z::kRows + r) * D + d) / 32], 1u << (d & 31));
-                if (CODES) values[i * 16 + e] = 0;
-                else ((uint16_t *)values)[i * 8 + e] = 0;
+            each([&](int word, uint32_t x) {
+                constexpr int kBits = CODES ? 8 : 16;
+#pragma unroll 1
+                for (int e = 0; e < 32 / kBits; ++e) {
+                    const uint32_t y = x >> (kBits * e) & ((1u << kBits) - 1);
+                    if (CODES ? (y & 0x7F) != 0x7F : (y & 0x7F80) != 0x7F80) continue;
+                    const int i = word / 4, row = i / CHUNKS;
+                    const int d = (((i % CHUNKS) ^ swizzle<CHUNKS, CODES>(row)) * 4 + word % 4) * (32 / kBits) + e;
+                    const int kind = CODES || (y & 0x7F) ? 2 : y >> 15;  // 0 inf, 1 -inf, 2 NaN
+#pragma unroll 1
+                    for (int r = 0; r < Z::kRows; ++r)
+                        if (masks[r] >> row & 1) atomicOr(&odd[((kind * Z::kRows + r) * D + d) / 32], 1u << (d & 31));
+                    if (CODES) values[word * 4 + e] = 0;
+                    else ((uint16_t *)values)[word * 2 + e] = 0;
+                }
             });
             __syncthreads();
         };
 
         // ---- the cache's tiles (bf16: and the chunk's rows) ----
-        // Keys and values have SLOTS places each. At the first barrier of a tile's step its keys
-        // are there and the values of the one before are done with: their place takes those of the
-        // tile SLOTS - 1 further on. At the second its values are there and the keys' place takes
-        // those of the tile SLOTS further on. The first SLOTS steps only load.
+        // A tile is two halves of a step: scores and weights, then values. Keys and values have
+        // SLOTS places each, and a place is filled again as soon as its tile is done with, by loads
+        // between the matrix instructions. At the barrier before a tile's first half its keys are
+        // there, at the one before the second its values. Where the chip is short of products and
+        // not of bytes (LAG), the second half of the waves is half a step behind: the ones' weights
+        // are made beside the others' products.
         const int count = cut - t0;
         const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
-        uint32_t masked = 0;  // of the tiles in LDS, which need a mask: bit 0 the last located
-        // (the compiler knows of q's loads but not of the tiles': without this it would wait for all
-        // of them at q's first use, in every step)
-        wait_vmcnt<0>();
-        if (count > 0)
-            for (int i = -SLOTS; i < count; ++i) {
-                const int left = count - 1 - i;
-                if (i >= 0) {
-                    // loaded since: the tile's values, and keys and values of those after it
-                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
-                    else wait_parts<kMine, 2 * (SLOTS - 1)>(2 * left + 1);
-                    lds_barrier();
-                }
-                if (i + SLOTS > 0 && left >= SLOTS - 1)
-                    fill(cache_row, va, area + (SLOTS + ((i + SLOTS - 1) & (SLOTS - 1))) * Z::kPart);
-                const bool mask = masked >> (SLOTS - 1) & 1;
-                if (i >= 0) {
-                    if (mask) {
-                        make_masks((t0 + i) * kTile, seen[i & (SLOTS - 1)]);
-                        lds_barrier();
-                    }
-                    scores(std::bool_constant<E4M3>{}, area + (i & (SLOTS - 1)) * Z::kPart);
-                    weigh(ks, mask);
-                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
-                    else wait_parts<kMine, 2 * (SLOTS - 1)>(2 * left);
-                    lds_barrier();
-                }
-                masked <<= 1;
-                if (left >= SLOTS) {
-                    const int base = (t0 + i + SLOTS) * kTile;
-                    look_up(base);
-                    const uint64_t there = locate(base, limit);
-                    if (tid == 0) seen[i & (SLOTS - 1)] = there;
-                    masked |= needs_mask(base, there);
-                    fill(cache_row, ka, area + (i & (SLOTS - 1)) * Z::kPart);
-                }
-                if (i >= 0) {
-                    if (mask) set_apart(std::bool_constant<E4M3>{}, lds + (SLOTS + (i & (SLOTS - 1))) * Z::kPart);
-                    add_values(std::bool_constant<E4M3>{}, area + (SLOTS + (i & (SLOTS - 1))) * Z::kPart);
-                }
+        auto nothing = [](int, int) {};
+        auto keys_at = [&](int i) { return area + (i & (SLOTS - 1)) * Z::kPart; };
+        auto values_at = [&](int i) { return area + (SLOTS + (i & (SLOTS - 1))) * Z::kPart; };
+        uint32_t masked = 0;  // of the tiles in LDS, which need a mask: bit i & (2 SLOTS - 1)
+        auto find = [&](int i) {
+            const int base = (t0 + i) * kTile;
+            look_up(base);
+            const uint64_t there = locate(base, limit);
+            if (tid == 0) seen[i & (2 * SLOTS - 1)] = there;
+            const uint32_t bit = 1u << (i & (2 * SLOTS - 1));
+            masked = needs_mask(base, there) ? masked | bit : masked & ~bit;
+        };
+        // loads of a part, one piece at a time between `steps` groups of matrix instructions
+        auto loading = [&](bool any, uint64_t from, uint32_t to) {
+            return [&, any, from, to](int step, int steps) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (any && step == i * steps / kMine) fill_piece(cache_row, from, to, i);
+            };
+        };
+        auto first_half = [&](int i, auto between) {
+            const bool mask = masked >> (i & (2 * SLOTS - 1)) & 1;
+            scores(std::bool_constant<E4M3>{}, keys_at(i), between);
+            weigh(ks, mask);
+        };
+        auto prepare = [&](int i) {  // masks of a tile that needs them, for both groups of waves
+            if (masked >> (i & (2 * SLOTS - 1)) & 1) {
+                make_masks((t0 + i) * kTile, seen[i & (2 * SLOTS - 1)]);
+                lds_barrier();
             }
+        };
+        auto sift = [&](int i) {
+            if (masked >> (i & (2 * SLOTS - 1)) & 1) set_apart(std::bool_constant<E4M3>{}, lds + (values_at(i) - area));
+        };
+        if (count > 0) {
+            uint64_t vb = 0;
+            // (the compiler knows of q's loads but not of the tiles': without this it would wait for
+            // all of them at q's first use, in every step)
+            wait_vmcnt<0>();
+            if constexpr (!Z::kLag) {
+                // keys of SLOTS tiles ahead, values of SLOTS - 1
+                for (int i = 0; i < min(SLOTS, count); ++i) {
+                    if (i) fill(cache_row, vb, values_at(i - 1));
+                    find(i);
+                    vb = va;
+                    fill(cache_row, ka, keys_at(i));
+                }
+                if (count < SLOTS) fill(cache_row, vb, values_at(count - 1));
+                for (int i = 0; i < count; ++i) {
+                    const int left = count - 1 - i;
+                    // loaded since its keys: values from its own on, keys of the tiles after it
+                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                    else wait_parts<kMine, 2 * SLOTS>(2 * left + 1);
+                    lds_barrier();
+                    prepare(i);
+                    first_half(i, loading(left >= SLOTS - 1, vb, values_at(i + SLOTS - 1)));
+                    if (left >= SLOTS) find(i + SLOTS);
+                    vb = va;
+                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                    else wait_parts<kMine, 2 * SLOTS>(2 * left);
+                    lds_barrier();
+                    sift(i);
+                    add_values(std::bool_constant<E4M3>{}, values_at(i), loading(left >= SLOTS, ka, keys_at(i)));
+                }
+            } else {
+                const int late = wave >= Z::kWaves / 2;
+                for (int i = 0; i < min(SLOTS - 1, count); ++i) {
+                    find(i);
+                    fill(cache_row, ka, keys_at(i));
+                    fill(cache_row, va, values_at(i));
+                }
+                // Half 2 i is the early waves' first half of step i and the late ones' second half of
+                // step i - 1: keys of tile i + SLOTS - 1 are loaded, and in half 2 i + 1 its values.
+                // Their places were last read half a step before.
+                auto begin = [&](int half) {
+                    const int i = half >> 1;
+                    if (i < count) {
+                        // loaded since keys i: values i, and both of up to SLOTS - 2 tiles; since
+                        // values i: those, and the keys of the tile ahead
+                        const int since = 2 * max(min(SLOTS - 2, count - 1 - i), 0);
+                        wait_parts<kMine, 2 * SLOTS - 3>(half & 1 ? since + (i + SLOTS - 1 < count) : since + 1);
+                    }
+                    lds_barrier();
+                    if (i >= count) return;
+                    if (half & 1) {
+                        sift(i);
+                    } else {
+                        if (i + SLOTS - 1 < count) find(i + SLOTS - 1);
+                        prepare(i);
+                    }
+                };
+                auto loads_of = [&](int half) {
+                    const int ahead = (half >> 1) + SLOTS - 1;
+                    return loading(ahead < count, half & 1 ? va : ka, half & 1 ? values_at(ahead) : keys_at(ahead));
+                };
+                if (late) {
+                    begin(0);
+                    for (int k = 0; k < kMine; ++k) loads_of(0)(k, kMine);
+                }
+                for (int i = 0; i < count; ++i) {
+                    const int half = 2 * i + late;
+                    begin(half);
+                    first_half(i, loads_of(half));
+                    begin(half + 1);
+                    add_values(std::bool_constant<E4M3>{}, values_at(i), loads_of(half + 1));
+                }
+                if (!late) begin(2 * count);
+            }
+        }
         // ---- beside an 8-bit cache, the chunk's rows ----
         if constexpr (E4M3) {
 #pragma unroll
@@ -708,10 +822,10 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                 make_masks(base, there);
                 wait_vmcnt<0>();
                 lds_barrier();
-                scores(std::false_type{}, area);
+                scores(std::false_type{}, area, nothing);
                 weigh(p.scale, true);
                 set_apart(std::false_type{}, lds + kTile * 2 * D);
-                add_values(std::false_type{}, area + kTile * 2 * D);
+                add_values(std::false_type{}, area + kTile * 2 * D, nothing);
             }
         }
 
@@ -769,6 +883,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
         }
 
         // ---- out, or a part of it ----
+        const Params &po = arguments();
         const bool whole = t0 == 0 && t1 == sq.tiles;
         const int64_t slot = 2 * (int64_t)w + (t0 == 0);
 #pragma unroll
@@ -776,10 +891,10 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             if (v == wk)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const int i = (wr * RT + rt) * 16 + col, r = row0 + i, node = node_of(r);
+                    const int i = (wr * RT + rt) * 16 + col, r = row0 + i, node = node_of(po, r);
                     if (r >= rows) continue;
                     if (whole) {
-                        uint16_t *o = p.out + (int64_t)(sq.first + node) * p.ld_out + (int64_t)head_of(r, node) * D +
+                        uint16_t *o = po.out + (int64_t)(sq.first + node) * po.ld_out + (int64_t)head_of(po, r, node) * D +
                                       16 * v * MINE + 4 * quad;
                         const float inv = sum[rt] == 0.f ? 0.f : 1.f / sum[rt];
 #pragma unroll
@@ -788,10 +903,10 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
                             *(uint2 *)(o + 16 * d) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
                         }
                     } else {
-                        float *o = p.parts + (slot * Z::kRows + i) * D + 16 * v * MINE + 4 * quad;
+                        float *o = po.parts + (slot * Z::kRows + i) * D + 16 * v * MINE + 4 * quad;
 #pragma unroll
                         for (int d = 0; d < MINE; ++d) *(f32x4 *)(o + 16 * d) = acc[rt][v * MINE + d];
-                        if (v == 0 && quad == 0) p.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
+                        if (v == 0 && quad == 0) po.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
                     }
                 }
         if (any_odd) {
@@ -799,16 +914,16 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             __threadfence_block();
             __syncthreads();
             for (int i = tid; i < Z::kRows * D; i += Z::kThreads) {
-                const int at = i / D, d = i % D, r = row0 + at, node = node_of(r);
+                const int at = i / D, d = i % D, r = row0 + at, node = node_of(po, r);
                 auto is = [&](int kind) { return odd[(kind * Z::kRows * D + i) / 32] >> (d & 31) & 1; };
                 const bool up = is(0), down = is(1);
                 if (r >= rows || !(up || down || is(2))) continue;
                 const float add = is(2) || (up && down) ? NAN : up ? INFINITY : -INFINITY;
                 if (whole) {
-                    uint16_t *o = p.out + (int64_t)(sq.first + node) * p.ld_out + (int64_t)head_of(r, node) * D + d;
+                    uint16_t *o = po.out + (int64_t)(sq.first + node) * po.ld_out + (int64_t)head_of(po, r, node) * D + d;
                     *o = f32_to_bf16_rne(bits_f32((uint32_t)*o << 16) + add);
                 } else {
-                    p.parts[(slot * Z::kRows + at) * D + d] += add;
+                    po.parts[(slot * Z::kRows + at) * D + d] += add;
                 }
             }
         }
@@ -816,7 +931,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params 
             // the parts that follow: one a team, up to the one with this unit's last step
             join = make_int4(seq, h, block, shares.team_of(x - t1 + sq.tiles - 1) - team);
     }
-    if (tid == 0) p.joins[w] = join;
+    if (tid == 0) arguments().joins[w] = join;
 }
 
 // Joins a block of rows whose first part is workgroup x's: a sixteenth of the rows a
@@ -924,9 +1039,9 @@ template <int D, bool E4M3>
 hipError_t launch_rows(const Params &p, int block_rows, hipStream_t stream) {
     switch (block_rows) {
     case 16: return launch_shape<D, E4M3, 1, 1, 4>(p, stream);
-    case 32: return launch_shape<D, E4M3, 2, 1, 4>(p, stream);
-    case 64: return launch_shape<D, E4M3, 2, 2, 2>(p, stream);
-    default: return launch_shape<D, E4M3, 2, 4, 2>(p, stream);
+    case 32: return launch_shape<D, E4M3, 1, 2, 4>(p, stream);
+    case 64: return launch_shape<D, E4M3, 1, 4, 2>(p, stream);
+    default: return launch_shape<D, E4M3, 1, 8, 1>(p, stream);
     }
 }
 
