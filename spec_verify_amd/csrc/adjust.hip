@@ -2,8 +2,9 @@
 // sequence's history and of a row's path in the tree of drafts, biases, grammar masks.
 //
 // A workgroup takes a range of the vocabulary for some rows of one sequence. It counts the
-// history's tokens of that range in LDS once, and for each row adds its path's, streams the
-// row's logits past the counts, and takes the path's out again.
+// history's tokens of that range in LDS once (16384 words of 32 bits: two workgroups a compute
+// unit). Then, row by row, it adds the row's path to the counts and takes the row before's out,
+// and streams the row's logits past them; the next row's are loaded meanwhile.
 #include <algorithm>
 
 #include "svq_tree.h"
@@ -12,9 +13,12 @@ namespace svq {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMostRange = 16384;  // tokens of a workgroup's range
-constexpr int kPath = 1024;        // tokens of a path taken at a time
+constexpr int kThreads = 512;
+constexpr int kMostRange = 16384;                     // tokens of a workgroup's range
+constexpr int kVectors = kMostRange / 8 / kThreads;   // of 8 logits, a thread's of one row
+constexpr int kNodes = 64;                            // trees up to this size have their paths as bits
+constexpr int kStaged = 1024;                         // of wider ones, parents kept in LDS
+constexpr int kPath = 512;                            // and tokens of a path taken at a time
 
 constexpr uint32_t kPrompt = 0x80000000u;  // occurs in the prompt
 constexpr uint32_t kBiased = 0x40000000u;  // has biases
@@ -31,10 +35,19 @@ struct Params {
     int M, S, V, range, ranges, groups;
 };
 
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
     __shared__ __attribute__((aligned(16))) uint32_t table[kMostRange + 8];
-    __shared__ int path[kPath], path_n, path_at;
-    const int tid = threadIdx.x;
+    __shared__ uint64_t lines[kNodes];  // of each node, itself and its ancestors
+    __shared__ int nodes[kNodes];       // the nodes' inputs
+    __shared__ int staged[kStaged], path[kPath], path_n, path_at;
+    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
     const svq_adjustments &a = p.a;
     for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
         const int c = (int)(item % p.ranges);
@@ -44,20 +57,62 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
         const int v0 = c * p.range, v1 = min(v0 + p.range, p.V);
         const int end = min(v1 + 8, p.V);  // counted too: a vector of 8 may begin before v1 and end after it
         const int32_t *parents = a.parents ? a.parents + first : nullptr;
+        // (a product with 1 / r instead of a quotient: one more rounding in fp32, 2^-16 of bf16's)
         const float rep = a.repetition ? a.repetition[s] : 1.f, inv = 1.f / rep;
         const float pres = a.presence ? a.presence[s] : 0.f, freq = a.frequency ? a.frequency[s] : 0.f;
+
+        // ---- the first row's logits are on their way while the history is counted ----
+        auto row_in = [&](int row) { return p.logits + (int64_t)(first + row) * p.ld; };
+        auto lead_of = [&](const uint16_t *x) { return (int)((uintptr_t)x / 2 & 7); };
+        // the first vector of 8 on a 16-byte line that begins in the range (a row's first may begin before it)
+        auto first_vector = [&](int lead) { return (v0 + lead + (v0 ? 7 : 0)) / 8; };
+        uint4 next[kVectors];
+        auto load = [&](int row) {
+            const uint16_t *in = row_in(row);
+            const int lead = lead_of(in), j0 = first_vector(lead) + tid;
+#pragma unroll
+            for (int k = 0; k < kVectors; ++k) {
+                const int v = 8 * (j0 + k * kThreads) - lead;
+                next[k] = make_uint4(0, 0, 0, 0);
+                if (v >= 0 && v < v1 && v + 8 <= p.V) next[k] = *(const uint4 *)(in + v);
+            }
+        };
+        load(g);
+
         __syncthreads();
         for (int i = tid; i < (p.range + 8) / 4; i += kThreads) ((uint4 *)table)[i] = make_uint4(0, 0, 0, 0);
+        if (n <= kNodes) {
+            if (wave == 0) {
+                // twice as far up in every round
+                int up = lane - 1;
+                if (parents) up = lane < n ? parents[lane] : -1;
+                if (up >= lane) up = -1;
+                uint64_t line = 1ull << lane;
+                for (int far = 1; far < n; far *= 2) {
+                    const int from = up < 0 ? lane : up;
+                    const uint64_t more = __shfl((unsigned long long)line, from);
+                    const int next_up = __shfl(up, from);
+                    if (up >= 0) line |= more;
+                    up = up < 0 ? -1 : next_up;
+                }
+                lines[lane] = line;
+                nodes[lane] = lane < n ? a.inputs[first + lane] : -1;
+            }
+        } else if (parents) {
+            for (int i = tid; i < min(n, kStaged); i += kThreads) staged[i] = parents[i];
+        }
         __syncthreads();
-        auto in_range = [&](int v) { return v >= v0 && v < end; };
+        auto count = [&](int v, uint32_t by) {
+            if (v >= v0 && v < end) atomicAdd(&table[v - v0], by);
+        };
         const int len = min(max(a.lengths[s], 0), a.max_history);
         const int prompt = a.prompt_lengths ? a.prompt_lengths[s] : 0;
         const int32_t *history = a.history + (int64_t)s * a.ld_history;
+#pragma unroll 4
         for (int i = tid; i < len; i += kThreads) {
             const int v = history[i];
-            if (!in_range(v)) continue;
-            if (i < prompt) atomicOr(&table[v - v0], kPrompt);
-            else atomicAdd(&table[v - v0], 1u);
+            if (i >= prompt) count(v, 1u);
+            else if (v >= v0 && v < end) atomicOr(&table[v - v0], kPrompt);
         }
         int64_t b0 = 0, b1 = 0;
         if (a.bias_starts) {
@@ -65,85 +120,121 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
             b1 = min((int64_t)a.bias_starts[s + 1], a.biases);
             for (int64_t b = b0 + tid; b < b1; b += kThreads) {
                 const int v = a.bias_tokens[b];
-                if (in_range(v)) atomicOr(&table[v - v0], kBiased);
+                if (v >= v0 && v < end) atomicOr(&table[v - v0], kBiased);
             }
         }
-        // adds `by` to the counts of the path of a row
-        auto along_path = [&](int row, uint32_t by) {
+        // adds `by` to the counts of a row's path; large trees: a walk
+        auto walk = [&](int row, uint32_t by) {
+            if (!parents) {
+                for (int i = tid; i <= row; i += kThreads) count(a.inputs[first + i], by);
+                return;
+            }
             int at = row;
             while (at >= 0) {
                 __syncthreads();
                 if (tid == 0) {
                     int k = 0;
                     while (at >= 0 && k < kPath) {
-                        path[k++] = a.inputs[first + at];
-                        const int up = parents ? parents[at] : at - 1;
+                        path[k++] = at;
+                        const int up = at < kStaged ? staged[at] : parents[at];
                         at = up >= 0 && up < at ? up : -1;
                     }
                     path_n = k;
                     path_at = at;
                 }
                 __syncthreads();
-                for (int i = tid; i < path_n; i += kThreads)
-                    if (in_range(path[i])) atomicAdd(&table[path[i] - v0], by);
+                for (int i = tid; i < path_n; i += kThreads) count(a.inputs[first + path[i]], by);
                 at = path_at;
             }
-            __syncthreads();
         };
+
         for (int row = g; row < n; row += p.groups) {
-            along_path(row, 1u);
+            // ---- this row's path in, the last one's out ----
+            __syncthreads();
+            if (n <= kNodes) {
+                if (wave == 0 && lines[row] >> lane & 1) count(nodes[lane], 1u);
+                if (wave == 1 && row > g && lines[row - p.groups] >> lane & 1) count(nodes[lane], ~0u);
+            } else {
+                walk(row, 1u);
+                if (row > g) walk(row - p.groups, ~0u);
+            }
+            uint4 x[kVectors];
+#pragma unroll
+            for (int k = 0; k < kVectors; ++k) x[k] = next[k];
+            if (row + p.groups < n) load(row + p.groups);
+            __syncthreads();
+
             const int64_t m = first + row;
-            const uint16_t *in = p.logits + m * p.ld;
+            const uint16_t *in = row_in(row);
             uint16_t *out = p.out + m * p.ld_out;
             const uint32_t *allowed = nullptr;
             if (a.allowed) {
                 const int64_t mask = a.mask_rows[m];
                 if (mask >= 0 && mask < a.masks) allowed = (const uint32_t *)a.allowed + mask * a.ld_allowed;
             }
-            auto change = [&](uint32_t bits, uint32_t word, int v) {
-                if (word == 0) return bits;
-                float x = bits_f32(bits << 16);
+            auto biased = [&](float x, int v) {
+                for (int64_t b = b0; b < b1; ++b)
+                    if (a.bias_tokens[b] == v) x += a.bias_values[b];
+                return x;
+            };
+            auto change = [&](float x, uint32_t word) {
                 const uint32_t count = word & kCount;
-                if (word & ~kBiased) x *= x > 0.f ? inv : rep;
-                if (count) x = x - freq * (float)count - pres;
-                if (word & kBiased)
-                    for (int64_t b = b0; b < b1; ++b)
-                        if (a.bias_tokens[b] == v) x += a.bias_values[b];
-                return (uint32_t)f32_to_bf16_rne(x);
+                x *= word & ~kBiased ? (x > 0.f ? inv : rep) : 1.f;
+                return __builtin_fmaf(-freq, (float)count, x) - (count ? pres : 0.f);
             };
             auto single = [&](int v) {
-                uint32_t r = change(in[v], table[v - v0], v);
+                const uint32_t word = table[v - v0];
+                uint32_t r = in[v];
+                if (word) {
+                    float x = change(bits_f32(r << 16), word);
+                    if (word & kBiased) x = biased(x, v);
+                    r = f32_to_bf16_rne(x);
+                }
                 if (allowed && !(allowed[v >> 5] >> (v & 31) & 1)) r = 0xFF80u;
                 out[v] = (uint16_t)r;
             };
-            const int lead = (int)((uintptr_t)in / 2 & 7);
-            if (lead != (int)((uintptr_t)out / 2 & 7)) {
+            const int lead = lead_of(in);
+            if (lead != lead_of(out)) {
                 for (int v = v0 + tid; v < v1; v += kThreads) single(v);
-            } else {
-                // vectors of 8 logits on 16-byte lines; the first of a row may begin before it
-                for (int j = (v0 + lead + (v0 ? 7 : 0)) / 8 + tid; 8 * j - lead < v1; j += kThreads) {
-                    const int v = 8 * j - lead;
-                    if (v < 0 || v + 8 > p.V) {
-                        for (int e = max(v, 0); e < min(v + 8, p.V); ++e) single(e);
-                        continue;
-                    }
-                    uint4 x = *(const uint4 *)(in + v);
-                    uint32_t *const xs = (uint32_t *)&x;
-                    uint32_t bits = 0xFFu;
-                    if (allowed) {
-                        bits = allowed[v >> 5] >> (v & 31);
-                        if ((v & 31) > 24) bits |= allowed[min((v >> 5) + 1, (p.V - 1) >> 5)] << (32 - (v & 31));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t r = change(xs[e / 2] >> (16 * (e & 1)) & 0xFFFFu, table[v - v0 + e], v + e);
-                        if (!(bits >> e & 1)) r = 0xFF80u;
-                        xs[e / 2] = e & 1 ? (xs[e / 2] & 0xFFFFu) | r << 16 : (xs[e / 2] & 0xFFFF0000u) | r;
-                    }
-                    *(uint4 *)(out + v) = x;
-                }
+                continue;
             }
-            along_path(row, ~0u);
+            auto vector = [&](uint4 x, int v) {
+                uint32_t bits = 0xFFu;
+                if (allowed) {
+                    bits = allowed[v >> 5] >> (v & 31);
+                    if ((v & 31) > 24) bits |= allowed[min((v >> 5) + 1, (p.V - 1) >> 5)] << (32 - (v & 31));
+                }
+                uint32_t w[8], any = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) any |= w[e] = table[v - v0 + e];
+                uint32_t *const xs = (uint32_t *)&x;
+                if (any & kBiased) {
+                    for (int e = 0; e < 8; ++e) single(v + e);
+                    return;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const uint32_t was = xs[e / 2];
+                    const uint32_t now = pack_bf16(change(bits_f32(was << 16), w[e]), change(bits_f32(was & 0xFFFF0000u), w[e + 1]));
+                    uint32_t lo = w[e] ? now : was, hi = w[e + 1] ? now : was;
+                    if (!(bits >> e & 1)) lo = 0xFF80u;
+                    if (!(bits >> e & 2)) hi = 0xFF800000u;
+                    xs[e / 2] = (lo & 0xFFFFu) | (hi & 0xFFFF0000u);
+                }
+                *(uint4 *)(out + v) = x;
+            };
+            const int j0 = first_vector(lead) + tid;
+            auto place = [&](int j, auto whole) {
+                const int v = 8 * j - lead;
+                if (v >= v1) return;
+                if (v >= 0 && v + 8 <= p.V) whole(v);
+                else
+                    for (int e = max(v, 0); e < min(v + 8, p.V); ++e) single(e);
+            };
+#pragma unroll
+            for (int k = 0; k < kVectors; ++k) place(j0 + k * kThreads, [&](int v) { vector(x[k], v); });
+            // (a row that does not begin on a line may have one more)
+            place(j0 + kVectors * kThreads, [&](int v) { vector(*(const uint4 *)(in + v), v); });
         }
     }
 }
@@ -162,8 +253,8 @@ hipError_t launch_adjust_logits(const void *logits, int64_t ld, const int32_t *s
     p.M = (int)M;
     p.S = (int)S;
     p.V = (int)V;
-    // enough workgroups to fill the chip: ranges of the vocabulary first, then rows
-    const int64_t want = 4 * (int64_t)num_cus, rows = (M + S - 1) / S;
+    // two workgroups a compute unit: ranges of the vocabulary first, then rows
+    const int64_t want = 2 * (int64_t)num_cus, rows = (M + S - 1) / S;
     int64_t ranges = std::max<int64_t>((V + kMostRange - 1) / kMostRange, std::min<int64_t>((want + S - 1) / S, (V + 1023) / 1024));
     p.range = (int)(((V + ranges - 1) / ranges + 7) & ~(int64_t)7);
     p.ranges = (int)((V + p.range - 1) / p.range);

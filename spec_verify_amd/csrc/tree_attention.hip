@@ -32,8 +32,8 @@ namespace svq {
 namespace {
 
 constexpr int kTile = 64;          // tokens in a tile
-constexpr int kStaged = 1024;      // parents kept in LDS; of wider trees the rest is read where it lies
-constexpr int kEntries = 2048;     // page table entries kept in LDS
+constexpr int kStaged = 256;       // parents kept in LDS; of wider trees the rest is read where it lies
+constexpr int kEntries = 1024;     // page table entries kept in LDS
 constexpr float kSlack = 8.f;      // how far (in powers of two) scores may pass the maximum that weights refer to
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -147,10 +147,6 @@ __device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b) {
                       e4m3_pair_scaled<true>(b, 1.f));
 }
 
-__device__ __forceinline__ f32x4 mfma16x16x16(s16x4 a, s16x4 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -168,7 +164,7 @@ __device__ __forceinline__ float rows4_max(float v) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// exp2(m - top) for a maximum m <= top; no weight has been seen below -inf
+// exp2(m - top) for a reference m <= top; no weight has been seen below -inf
 __device__ __forceinline__ float decay(float m, float top) { return exp2_fast(m - (top == -INFINITY ? 0.f : top)); }
 
 // A value that all lanes hold, in a scalar register.
@@ -222,38 +218,43 @@ __device__ __forceinline__ void wait_parts(int n) {
     else wait_parts<PER, MOST - 1>(n);
 }
 
-// D elements a head; RT 16-row tiles a wave, WR waves over rows, WK waves over tokens.
+// D elements a head; WR groups of waves over rows, RT 16-row tiles each; WK waves a group,
+// which share a tile's tokens for the scores, and the columns for the sums.
 template <int D, bool E4M3, int RT, int WR, int WK>
 struct Shape {
     static constexpr int kWaves = WR * WK, kThreads = 64 * kWaves;
     static constexpr int kRows = 16 * RT * WR;
-    static constexpr int kBlocks = kTile / 16 / WK;   // 16-token blocks of a tile that a wave takes
+    static constexpr int kBlocks = kTile / 16 / WK;           // 16-token blocks of a tile that a wave weighs
     static constexpr int kPart = kTile * D * (E4M3 ? 1 : 2);  // bytes of a tile's keys, or values
     // Places for keys, and for values: as many as keep some 100 KiB a compute unit in flight (8 KiB
     // pieces are not worth more waits)
     static constexpr int kSlots = kPart >= 32768 ? 2 : 4;
-    static constexpr bool kLag = kRows >= 128 && kWaves == 8;  // products, not bytes
+    static constexpr bool kLag = kRows >= 128 && WR > 1;      // products, not bytes
     static constexpr int kArea = 2 * kSlots * kPart;
     // groups of operands read from LDS before their use: as registers allow
-    static constexpr int kAhead = D * RT >= 512 ? 2 : 4;
-    static constexpr int kOdd = 3 * kRows * D / 8;            // a bit each: infinities and NaN that rows see
-    static constexpr int kLds = kArea + kRows * 8 + kStaged * 4 + kEntries * 4 + kSlots * 16 + 256 + kOdd;
-    static_assert((WK - 1) * kRows * D * 4 <= kArea, "the waves' sums fit the tiles' place");
+    static constexpr int kAhead = D * RT >= 512 ? 3 : 4;
+    static constexpr int kOdd = 2 * kRows * D / 8;            // two bits each: infinities and NaN that rows see
+    static constexpr int kWeights = kRows * kTile * 2;
+    static constexpr int kRefs = kRows * WK * 4;
+    static constexpr int kLds = kArea + kWeights + kRefs + kRows * 8 + kStaged * 4 + kEntries * 4 + kSlots * 16 + 256 + kOdd;
+    static_assert(kLds <= 160 * 1024, "a compute unit's LDS");
 };
 
 template <int D, bool E4M3, int RT, int WR, int WK>
 __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params) {
     const Params &p = arguments();
     using Z = Shape<D, E4M3, RT, WR, WK>;
-    constexpr int NB = Z::kBlocks, C = D / 32, DT = D / 16, SLOTS = Z::kSlots, kAhead = Z::kAhead;
-    // keys of SLOTS tiles, values of as many; or one tile of bf16 beside an 8-bit cache; or sums
+    constexpr int NB = Z::kBlocks, C = D / 32, MINE = D / 16 / WK, SLOTS = Z::kSlots, kAhead = Z::kAhead;
+    // keys of SLOTS tiles, values of as many; or one tile of bf16 beside an 8-bit cache
     __shared__ __attribute__((aligned(256))) char lds[Z::kLds];
-    uint64_t *const masks = (uint64_t *)(lds + Z::kArea);
+    uint2 *const weights = (uint2 *)(lds + Z::kArea);                  // [row tile][block][lane]
+    float *const refs = (float *)(lds + Z::kArea + Z::kWeights);       // [wave of a group][row]
+    uint64_t *const masks = (uint64_t *)(lds + Z::kArea + Z::kWeights + Z::kRefs);
     int *const staged = (int *)(masks + Z::kRows);
     int *const entries = staged + kStaged;
     uint64_t *const seen = (uint64_t *)(entries + kEntries);  // of the tiles in LDS, which tokens are there
     int *const scratch = (int *)(seen + 2 * SLOTS);
-    uint32_t *const odd = (uint32_t *)(scratch + 64);         // [kind][row][D / 32]
+    uint32_t *const odd = (uint32_t *)(scratch + 64);  // [infinity, -infinity (NaN: both)][row][D / 32]
     const uint32_t area = lds_addr(lds);
 
     const int lane = threadIdx.x & 63, wave = wave_id(), tid = threadIdx.x;
@@ -350,7 +351,19 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             for (int c = 0; c < C; ++c)
                 qf[rt][c] = r < rows ? src[E4M3 ? 8 * (c / 2) + 2 * quad + c % 2 : 4 * c + quad] : make_uint4(0, 0, 0, 0);
         }
-        float ks = p.scale, vs = 1.f;
+        float own = p.scale, ks, vs = 1.f;
+        if (!(own > 0.f)) {
+            // a scale that is not positive goes into q: the largest score is then the largest product's
+            const uint32_t keep = own < 0.f ? ~0u : own == 0.f ? 0u : ~0u, turn = own < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    qf[rt][c] = make_uint4((qf[rt][c].x ^ turn) & keep, (qf[rt][c].y ^ turn) & keep, (qf[rt][c].z ^ turn) & keep,
+                                           (qf[rt][c].w ^ turn) & keep);
+            own = own < 0.f ? -own : own == 0.f ? 1.f : own;
+        }
+        ks = own;
         if (E4M3) {
             if (p.k.scale) ks *= p.k.scale[h];
             if (p.v.scale) vs = p.v.scale[h];
@@ -390,14 +403,17 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             return up >= 0 && up < i ? up : -1;
         };
 
-        f32x4 acc[RT][DT];
-        float top[RT], sum[RT];
+        // Weights are 2^(score - reference), and a row's reference the same for all of its group's
+        // waves: the smallest whole number not below a score that has passed the one before by
+        // kSlack (2^kSlack is nothing to fp32 sums; what is whole rescales bf16 weights exactly).
+        f32x4 acc[RT][MINE];        // columns 16 MINE wk and on
+        float top[RT], sum[RT];     // reference; sum of this wave's weights
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             top[rt] = -INFINITY;
             sum[rt] = 0.f;
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) acc[rt][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int d = 0; d < MINE; ++d) acc[rt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
         // Where the tokens of a tile lie: lane i finds token base + i; kZeros for none. Returns
@@ -491,7 +507,8 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         };
 
         f32x4 sc[RT][NB];
-        uint2 wt[RT][NB];  // bf16 weights of tokens 4 quad .. 4 quad + 3 of each block
+        uint2 wt[RT][kTile / 16];  // bf16 weights of tokens 4 quad .. 4 quad + 3 of each block
+        float mine[RT];            // the reference of its own
         // scores of this wave's blocks of tokens, from keys in LDS
         auto scores = [&](auto codes, uint32_t keys, auto between) {
             constexpr bool CODES = decltype(codes)::value;
@@ -539,16 +556,13 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        // their weights, relative to a maximum that follows the scores' once these pass it by
-        // kSlack: 2^kSlack is nothing to fp32 sums, and sums are rarely rescaled
+        // their weights, for all waves of the group
         auto weigh = [&](float to2, bool masked) {
+            const int l = fresh(lane), col = l & 15, quad = l >> 4;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b) sc[rt][b] *= to2;
                 if (masked) {
-                    const int l = fresh(lane), quad = l >> 4;
-                    const uint32_t *mask = (const uint32_t *)(masks + (wr * RT + rt) * 16 + (l & 15));
+                    const uint32_t *mask = (const uint32_t *)(masks + (wr * RT + rt) * 16 + col);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const uint32_t bits = mask[(wk * NB + b) / 2] >> (16 * ((wk * NB + b) & 1) + 4 * quad);
@@ -562,83 +576,104 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) high = fmaxf(high, sc[rt][b][i]);
-                high = rows4_max(high);
+                high = rows4_max(high) * to2;
+                mine[rt] = top[rt];
                 if (__any(high > top[rt] + kSlack)) {
-                    high = fmaxf(high, top[rt]);
-                    const float down = decay(top[rt], high);
-                    top[rt] = high;
-                    sum[rt] *= down;
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= down;
+                    mine[rt] = high > top[rt] + kSlack ? ceilf(high) : top[rt];
+                    sum[rt] *= decay(top[rt], mine[rt]);
                 }
-                const float safe = top[rt] == -INFINITY ? 0.f : top[rt];
+                const float ref = mine[rt] == -INFINITY ? 0.f : mine[rt];
                 float add = 0.f;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     float e[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) add += e[i] = exp2_fast(sc[rt][b][i] - safe);
-                    wt[rt][b] = make_uint2(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]));
+                    for (int i = 0; i < 4; ++i) add += e[i] = exp2_fast(__builtin_fmaf(sc[rt][b][i], to2, -ref));
+                    weights[((wr * RT + rt) * (kTile / 16) + wk * NB + b) * 64 + l] =
+                        make_uint2(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]));
                 }
                 sum[rt] += add;
+                if (quad == 0) refs[wk * Z::kRows + (wr * RT + rt) * 16 + col] = mine[rt];
             }
         };
-        // The weighted values of a tile in LDS. A transposed read gives a lane 4 tokens of its
-        // column (4 quad .. 4 quad + 3 of a block), of codes 8: of two blocks of tokens, or (a wave
-        // with one) of two blocks of columns.
+        // the weights of all blocks, and one reference for all
+        auto meet = [&]() {
+            const int l = fresh(lane), col = l & 15;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float each[WK], high = -INFINITY;
+                bool other = false;
+#pragma unroll
+                for (int v = 0; v < WK; ++v) {
+                    each[v] = refs[v * Z::kRows + (wr * RT + rt) * 16 + col];
+                    high = fmaxf(high, each[v]);
+                    other |= each[v] != top[rt];
+                }
+#pragma unroll
+                for (int b = 0; b < kTile / 16; ++b) wt[rt][b] = weights[((wr * RT + rt) * (kTile / 16) + b) * 64 + l];
+                if (__any(other)) {
+                    sum[rt] *= decay(mine[rt], high);
+                    const float down = decay(top[rt], high);
+#pragma unroll
+                    for (int d = 0; d < MINE; ++d) acc[rt][d] *= down;
+                    top[rt] = high;
+#pragma unroll
+                    for (int b = 0; b < kTile / 16; ++b) {
+                        const float by = decay(each[b / NB], high);
+                        uint2 &x = wt[rt][b];
+                        x = make_uint2(pack_bf16(bits_f32(x.x << 16) * by, bits_f32(x.x & 0xFFFF0000u) * by),
+                                       pack_bf16(bits_f32(x.y << 16) * by, bits_f32(x.y & 0xFFFF0000u) * by));
+                    }
+                }
+            }
+        };
+        // The weighted values of a tile in LDS: this wave's columns. A transposed read gives a lane 4
+        // tokens of its column (4 quad .. 4 quad + 3 of a block), of codes those of two blocks.
         auto add_values = [&](auto codes, uint32_t values, auto between) {
             constexpr bool CODES = decltype(codes)::value;
             constexpr int BYTES = CODES ? D : 2 * D, CHUNKS = BYTES / 16, kMixed = CHUNKS < 16 ? CHUNKS - 1 : 15;
             const int l = fresh(lane), col = l & 15, quad = l >> 4;
-            const int row = wk * NB * 16 + 4 * quad + (CODES ? col >> 1 & 3 : col >> 2) + (CODES && NB > 1 ? col >> 3 << 4 : 0);
-            const int chunk = CODES ? (NB == 1 ? col >> 3 : 0) : col >> 1 & 1;
-            const uint32_t from = (uint32_t)(uintptr_t)lds_opaque(values + row * BYTES + (chunk ^ swizzle<CHUNKS, CODES>(row)) * 16 +
-                                                                  (col & 1) * 8);
+            const int row = 4 * quad + (CODES ? (col >> 1 & 3) + (col >> 3 << 4) : col >> 2);
+            const int first = wk * MINE * (CODES ? 1 : 2);  // chunk of the wave's first column
+            const uint32_t from = (uint32_t)(uintptr_t)lds_opaque(
+                values + row * BYTES + (((CODES ? 0 : col >> 1 & 1) ^ swizzle<CHUNKS, CODES>(row)) ^ (first & kMixed)) * 16 +
+                (first & ~kMixed) * 16 + (col & 1) * 8);
             auto read = [&](int b, int chunk) {
-                const lds_u8 *at = (const lds_u8 *)(from ^ (chunk & kMixed) * 16) + (chunk & ~kMixed) * 16 + b * 16 * BYTES;
+                const lds_u8 *const at = (const lds_u8 *)(from ^ (chunk & kMixed) * 16) + (chunk & ~kMixed) * 16 + b * 16 * BYTES;
                 if constexpr (CODES)
                     return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2 *)at);
                 else
                     return __builtin_bit_cast(
                         i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at));
             };
-            // groups of one block of columns (of codes, where a wave has one block of tokens, two)
-            constexpr int PER = CODES && NB == 1 ? 2 : 1, GROUPS = (NB + 1) / 2 * (DT / PER), READS = CODES || NB == 1 ? 1 : 2;
+            constexpr int GROUPS = kTile / 32 * MINE, READS = CODES ? 1 : 2;
             struct Raw {
                 i32x2 x[READS];
             };
             auto read_group = [&](int g) {
-                const int b = g / (DT / PER) * 2, dt = g % (DT / PER) * PER;
+                const int b = g / MINE * 2, d = g % MINE;
                 Raw r;
 #pragma unroll
-                for (int k = 0; k < READS; ++k) r.x[k] = read(b + k, CODES ? dt : 2 * dt);
+                for (int k = 0; k < READS; ++k) r.x[k] = read(b + k, CODES ? d : 2 * d);
                 return r;
             };
             Raw raw[kAhead + 1];
 #pragma unroll
             for (int g = 0; g < kAhead && g < GROUPS; ++g) raw[g] = read_group(g);
+            meet();
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 if (g + kAhead < GROUPS) raw[(g + kAhead) % (kAhead + 1)] = read_group(g + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
-                const int b = g / (DT / PER) * 2, dt = g % (DT / PER) * PER;
+                const int b = g / MINE * 2, d = g % MINE;
                 const Raw &r = raw[g % (kAhead + 1)];
-                uint4 a;  // a block's tokens and the next one's, or two blocks of columns
+                uint4 a;
                 if constexpr (CODES) a = decode8(r.x[0][0], r.x[0][1]);
-                else if constexpr (NB == 1) a = make_uint4(r.x[0][0], r.x[0][1], 0, 0);
                 else a = make_uint4(r.x[0][0], r.x[0][1], r.x[READS - 1][0], r.x[READS - 1][1]);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if constexpr (NB == 1) {
-#pragma unroll
-                        for (int e = 0; e < PER; ++e)
-                            acc[rt][dt + e] = mfma16x16x16(__builtin_bit_cast(s16x4, e ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y)),
-                                                           __builtin_bit_cast(s16x4, wt[rt][0]), acc[rt][dt + e]);
-                    } else {
-                        acc[rt][dt] = mfma16x16x32(
-                            a, make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x, wt[rt][b + 1].y), acc[rt][dt]);
-                    }
-                }
+                for (int rt = 0; rt < RT; ++rt)
+                    acc[rt][d] = mfma16x16x32(
+                        a, make_uint4(wt[rt][b].x, wt[rt][b].y, wt[rt][b + 1].x, wt[rt][b + 1].y), acc[rt][d]);
                 between(g, GROUPS);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -678,10 +713,13 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                     if (CODES ? (y & 0x7F) != 0x7F : (y & 0x7F80) != 0x7F80) continue;
                     const int i = word / 4, row = i / CHUNKS;
                     const int d = (((i % CHUNKS) ^ swizzle<CHUNKS, CODES>(row)) * 4 + word % 4) * (32 / kBits) + e;
-                    const int kind = CODES || (y & 0x7F) ? 2 : y >> 15;  // 0 inf, 1 -inf, 2 NaN
+                    const bool none = CODES || (y & 0x7F);
 #pragma unroll 1
-                    for (int r = 0; r < Z::kRows; ++r)
-                        if (masks[r] >> row & 1) atomicOr(&odd[((kind * Z::kRows + r) * D + d) / 32], 1u << (d & 31));
+                    for (int r = 0; r < Z::kRows; ++r) {
+                        if (!(masks[r] >> row & 1)) continue;
+                        if (none || !(y >> 15)) atomicOr(&odd[(r * D + d) / 32], 1u << (d & 31));
+                        if (none || y >> 15) atomicOr(&odd[((Z::kRows + r) * D + d) / 32], 1u << (d & 31));
+                    }
                     if (CODES) values[word * 4 + e] = 0;
                     else ((uint16_t *)values)[word * 2 + e] = 0;
                 }
@@ -812,7 +850,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= vs;
+                for (int d = 0; d < MINE; ++d) acc[rt][d] *= vs;
             for (int t = max(t0, sq.cache_tiles); t < t1; ++t) {
                 const int base = sq.cached + (t - sq.cache_tiles) * kTile;
                 const uint64_t there = locate(base, sq.cached + sq.n);
@@ -823,63 +861,29 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 wait_vmcnt<0>();
                 lds_barrier();
                 scores(std::false_type{}, area, nothing);
-                weigh(p.scale, true);
+                weigh(own, true);
+                lds_barrier();
                 set_apart(std::false_type{}, lds + kTile * 2 * D);
                 add_values(std::false_type{}, area + kTile * 2 * D, nothing);
             }
         }
 
-        // ---- the waves over tokens meet: each gets its share of the columns from the others ----
-        constexpr int MINE = DT / WK;
+        // ---- the waves' sums of weights ----
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sum[rt] = rows4_sum(sum[rt]);
-        if constexpr (WK > 1) {
-            lds_barrier();
-            float2 *const st = (float2 *)staged;  // [wave over tokens][row]
-            static_assert(WK * Z::kRows * 8 <= kStaged * 4, "statistics fit the parents' place");
+        lds_barrier();
+        {
+            const int l = fresh(lane), row = wr * RT * 16 + (l & 15);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                if (quad == 0) st[wk * Z::kRows + (wr * RT + rt) * 16 + col] = make_float2(top[rt], sum[rt]);
+                if (l < 16) refs[wk * Z::kRows + row + rt * 16] = sum[rt];
             lds_barrier();
-            f32x4 *const give = (f32x4 *)lds;  // [wave over rows][to][from the one before it, ...][rt][column block][lane]
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                float high = -INFINITY, all = 0.f;
-                float2 each[WK];
+                sum[rt] = 0.f;
 #pragma unroll
-                for (int v = 0; v < WK; ++v) {
-                    each[v] = st[v * Z::kRows + (wr * RT + rt) * 16 + col];
-                    high = fmaxf(high, each[v].x);
-                }
-#pragma unroll
-                for (int v = 0; v < WK; ++v) all += each[v].y * decay(each[v].x, high);
-                const float down = decay(top[rt], high);
-                top[rt] = high;
-                sum[rt] = all;
-#pragma unroll
-                for (int v = 0; v < WK; ++v) {
-                    const int k = wk > v ? wk - v - 1 : wk - v + WK - 1;  // this wave's place among those that give to v
-#pragma unroll
-                    for (int d = 0; d < MINE; ++d) {
-                        acc[rt][v * MINE + d] *= down;
-                        if (v != wk)
-                            give[((((wr * WK + v) * (WK - 1) + k) * RT + rt) * MINE + d) * 64 + lane] =
-                                acc[rt][v * MINE + d];
-                    }
-                }
+                for (int v = 0; v < WK; ++v) sum[rt] += refs[v * Z::kRows + row + rt * 16];
             }
-            lds_barrier();
-#pragma unroll
-            for (int v = 0; v < WK; ++v)
-                if (v == wk)
-#pragma unroll
-                    for (int k = 0; k < WK - 1; ++k)
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                            for (int d = 0; d < MINE; ++d)
-                                acc[rt][v * MINE + d] +=
-                                    give[((((wr * WK + v) * (WK - 1) + k) * RT + rt) * MINE + d) * 64 + lane];
         }
 
         // ---- out, or a part of it ----
@@ -887,28 +891,25 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         const bool whole = t0 == 0 && t1 == sq.tiles;
         const int64_t slot = 2 * (int64_t)w + (t0 == 0);
 #pragma unroll
-        for (int v = 0; v < WK; ++v)
-            if (v == wk)
+        for (int rt = 0; rt < RT; ++rt) {
+            const int l = fresh(lane), quad = l >> 4, i = (wr * RT + rt) * 16 + (l & 15), r = row0 + i, node = node_of(po, r);
+            if (r >= rows) continue;
+            if (whole) {
+                uint16_t *o = po.out + (int64_t)(sq.first + node) * po.ld_out + (int64_t)head_of(po, r, node) * D +
+                              16 * MINE * wk + 4 * quad;
+                const float inv = sum[rt] == 0.f ? 0.f : 1.f / sum[rt];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const int i = (wr * RT + rt) * 16 + col, r = row0 + i, node = node_of(po, r);
-                    if (r >= rows) continue;
-                    if (whole) {
-                        uint16_t *o = po.out + (int64_t)(sq.first + node) * po.ld_out + (int64_t)head_of(po, r, node) * D +
-                                      16 * v * MINE + 4 * quad;
-                        const float inv = sum[rt] == 0.f ? 0.f : 1.f / sum[rt];
-#pragma unroll
-                        for (int d = 0; d < MINE; ++d) {
-                            const f32x4 a = acc[rt][v * MINE + d] * inv;
-                            *(uint2 *)(o + 16 * d) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
-                        }
-                    } else {
-                        float *o = po.parts + (slot * Z::kRows + i) * D + 16 * v * MINE + 4 * quad;
-#pragma unroll
-                        for (int d = 0; d < MINE; ++d) *(f32x4 *)(o + 16 * d) = acc[rt][v * MINE + d];
-                        if (v == 0 && quad == 0) po.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
-                    }
+                for (int d = 0; d < MINE; ++d) {
+                    const f32x4 a = acc[rt][d] * inv;
+                    *(uint2 *)(o + 16 * d) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
                 }
+            } else {
+                float *o = po.parts + (slot * Z::kRows + i) * D + 16 * MINE * wk + 4 * quad;
+#pragma unroll
+                for (int d = 0; d < MINE; ++d) *(f32x4 *)(o + 16 * d) = acc[rt][d];
+                if (wk == 0 && quad == 0) po.stats[slot * Z::kRows + i] = make_float2(top[rt], sum[rt]);
+            }
+        }
         if (any_odd) {
             // infinities and NaN that rows see
             __threadfence_block();
@@ -917,8 +918,8 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 const int at = i / D, d = i % D, r = row0 + at, node = node_of(po, r);
                 auto is = [&](int kind) { return odd[(kind * Z::kRows * D + i) / 32] >> (d & 31) & 1; };
                 const bool up = is(0), down = is(1);
-                if (r >= rows || !(up || down || is(2))) continue;
-                const float add = is(2) || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+                if (r >= rows || !(up || down)) continue;
+                const float add = up && down ? NAN : up ? INFINITY : -INFINITY;
                 if (whole) {
                     uint16_t *o = po.out + (int64_t)(sq.first + node) * po.ld_out + (int64_t)head_of(po, r, node) * D + d;
                     *o = f32_to_bf16_rne(bits_f32((uint32_t)*o << 16) + add);
@@ -1040,8 +1041,8 @@ hipError_t launch_rows(const Params &p, int block_rows, hipStream_t stream) {
     switch (block_rows) {
     case 16: return launch_shape<D, E4M3, 1, 1, 4>(p, stream);
     case 32: return launch_shape<D, E4M3, 1, 2, 4>(p, stream);
-    case 64: return launch_shape<D, E4M3, 1, 4, 2>(p, stream);
-    default: return launch_shape<D, E4M3, 1, 8, 1>(p, stream);
+    case 64: return launch_shape<D, E4M3, 2, 2, 4>(p, stream);
+    default: return launch_shape<D, E4M3, 2, 4, 2>(p, stream);
     }
 }
 
