@@ -68,17 +68,28 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
         // the first vector of 8 on a 16-byte line that begins in the range (a row's first may begin before it)
         auto first_vector = [&](int lead) { return (v0 + lead + (v0 ? 7 : 0)) / 8; };
         uint4 next[kVectors];
-        auto load = [&](int row) {
+        uint32_t next_open[kVectors];  // the row's mask where its vectors begin
+        auto mask_row = [&](int row) { return a.allowed && row < n ? a.mask_rows[first + row] : -1; };
+        auto mask_of = [&](int mask) {
+            return mask >= 0 && mask < a.masks ? (const uint32_t *)a.allowed + mask * a.ld_allowed : nullptr;
+        };
+        auto load = [&](int row, int mask) {
             const uint16_t *in = row_in(row);
+            const uint32_t *allowed = mask_of(mask);
             const int lead = lead_of(in), j0 = first_vector(lead) + tid;
 #pragma unroll
             for (int k = 0; k < kVectors; ++k) {
                 const int v = 8 * (j0 + k * kThreads) - lead;
                 next[k] = make_uint4(0, 0, 0, 0);
-                if (v >= 0 && v < v1 && v + 8 <= p.V) next[k] = *(const uint4 *)(in + v);
+                next_open[k] = ~0u;
+                if (v >= 0 && v < v1 && v + 8 <= p.V) {
+                    next[k] = *(const uint4 *)(in + v);
+                    if (allowed) next_open[k] = allowed[v >> 5];
+                }
             }
         };
-        load(g);
+        int mask_now = mask_row(g), mask_next = mask_row(g + p.groups);
+        load(g, mask_now);
 
         __syncthreads();
         for (int i = tid; i < (p.range + 8) / 4; i += kThreads) ((uint4 *)table)[i] = make_uint4(0, 0, 0, 0);
@@ -168,19 +179,20 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
                 if (row > g) walk(row - p.groups, ~0u);
             }
             uint4 x[kVectors];
+            uint32_t open[kVectors];
 #pragma unroll
-            for (int k = 0; k < kVectors; ++k) x[k] = next[k];
-            if (row + p.groups < n) load(row + p.groups);
+            for (int k = 0; k < kVectors; ++k) x[k] = next[k], open[k] = next_open[k];
+            const uint32_t *const allowed = mask_of(mask_now);
+            if (row + p.groups < n) {
+                load(row + p.groups, mask_next);
+                mask_now = mask_next;
+                mask_next = mask_row(row + 2 * p.groups);
+            }
             lds_barrier();
 
             const int64_t m = first + row;
             const uint16_t *in = row_in(row);
             uint16_t *out = p.out + m * p.ld_out;
-            const uint32_t *allowed = nullptr;
-            if (a.allowed) {
-                const int64_t mask = a.mask_rows[m];
-                if (mask >= 0 && mask < a.masks) allowed = (const uint32_t *)a.allowed + mask * a.ld_allowed;
-            }
             auto change = [&](float x, uint32_t word, int v) {
                 const uint32_t count = word & kCount;
                 x *= word & ~kBiased ? (x > 0.f ? inv : rep) : 1.f;
@@ -208,8 +220,8 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
                 if ((v & 31) > 24) b |= words[min((v >> 5) + 1, last)] << (32 - (v & 31));
                 return b & 0xFFu;
             };
-            auto vector = [&](uint4 x, int v) {
-                const uint32_t open = allowed ? bits_at(allowed, v, (p.V - 1) >> 5) : 0xFFu;
+            auto vector = [&](uint4 x, uint32_t open, int v) {
+                open = !allowed ? 0xFFu : lead == 0 ? open >> (v & 31) & 0xFFu : bits_at(allowed, v, (p.V - 1) >> 5);
                 // Few logits are marked (3300 of 248320 by a history of 4096): one after the other in a
                 // lane takes a wave two or three rounds (computing all 8: 312 vector instructions, 220 us
                 // for 512 rows; so 136 us).
@@ -245,9 +257,9 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
                     for (int e = max(v, 0); e < min(v + 8, p.V); ++e) single(e);
             };
 #pragma unroll
-            for (int k = 0; k < kVectors; ++k) place(j0 + k * kThreads, [&](int v) { vector(x[k], v); });
+            for (int k = 0; k < kVectors; ++k) place(j0 + k * kThreads, [&](int v) { vector(x[k], open[k], v); });
             // (a row that does not begin on a line may have one more)
-            place(j0 + kVectors * kThreads, [&](int v) { vector(*(const uint4 *)(in + v), v); });
+            place(j0 + kVectors * kThreads, [&](int v) { vector(*(const uint4 *)(in + v), ~0u, v); });
         }
     }
 }
