@@ -19,6 +19,7 @@ constexpr int kVectors = kMostRange / 8 / kThreads;   // of 8 logits, a thread's
 constexpr int kNodes = 64;                            // trees up to this size have their paths as bits
 constexpr int kStaged = 1024;                         // of wider ones, parents kept in LDS
 constexpr int kPath = 512;                            // and tokens of a path taken at a time
+constexpr int kBiases = 128;                          // biases of a range kept in LDS
 
 constexpr uint32_t kPrompt = 0x80000000u;  // occurs in the prompt
 constexpr uint32_t kBiased = 0x40000000u;  // has biases
@@ -48,6 +49,8 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
     __shared__ uint64_t lines[kNodes];  // of each node, itself and its ancestors
     __shared__ int nodes[kNodes];       // the nodes' inputs
     __shared__ int staged[kStaged], path[kPath], path_n, path_at;
+    __shared__ int bias_token[kBiases], bias_n;  // of the range, in their order
+    __shared__ float bias_value[kBiases];
     const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
     const svq_adjustments &a = p.a;
     for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
@@ -137,9 +140,23 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
         if (a.bias_starts) {
             b0 = min(max((int64_t)a.bias_starts[s], (int64_t)0), a.biases);
             b1 = min((int64_t)a.bias_starts[s + 1], a.biases);
-            for (int64_t b = b0 + tid; b < b1; b += kThreads) {
-                const int v = a.bias_tokens[b];
-                if (mark(v)) atomicOr(&table[v - v0], kBiased);
+            if (wave == 0) {
+                int kept = 0;
+                for (int64_t b = b0; b < b1; b += 64) {
+                    const int v = b + lane < b1 ? a.bias_tokens[b + lane] : -1;
+                    const bool here = mark(v);
+                    const uint64_t all = __ballot(here);
+                    const int at = kept + __popcll(all & ((1ull << lane) - 1));
+                    if (here) {
+                        atomicOr(&table[v - v0], kBiased);
+                        if (at < kBiases) {
+                            bias_token[at] = v;
+                            bias_value[at] = a.bias_values[b + lane];
+                        }
+                    }
+                    kept += __popcll(all);
+                }
+                if (lane == 0) bias_n = kept;
             }
         }
         // adds `by` to the counts of a row's path; large trees: a walk
@@ -197,9 +214,15 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
                 const uint32_t count = word & kCount;
                 x *= word & ~kBiased ? (x > 0.f ? inv : rep) : 1.f;
                 x = __builtin_fmaf(-freq, (float)count, x) - (count ? pres : 0.f);
-                if (word & kBiased)
-                    for (int64_t b = b0; b < b1; ++b)
-                        if (a.bias_tokens[b] == v) x += a.bias_values[b];
+                if (word & kBiased) {
+                    if (bias_n <= kBiases) {
+                        for (int b = 0; b < bias_n; ++b)
+                            if (bias_token[b] == v) x += bias_value[b];
+                    } else {
+                        for (int64_t b = b0; b < b1; ++b)
+                            if (a.bias_tokens[b] == v) x += a.bias_values[b];
+                    }
+                }
                 return x;
             };
             auto single = [&](int v) {
@@ -278,12 +301,15 @@ hipError_t launch_adjust_logits(const void *logits, int64_t ld, const int32_t *s
     p.M = (int)M;
     p.S = (int)S;
     p.V = (int)V;
-    // two workgroups a compute unit: ranges of the vocabulary first, then rows
+    // Two workgroups a compute unit, which is what LDS holds: whole ranges (every further one counts
+    // the history again), fewer rows each, and shorter ranges only where there are too few rows (512
+    // rows of 8 sequences: 16 ranges, 4 groups of rows 112 us, 64 ranges of all rows 182).
     const int64_t want = 2 * (int64_t)num_cus, rows = (M + S - 1) / S;
-    int64_t ranges = std::max<int64_t>((V + kMostRange - 1) / kMostRange, std::min<int64_t>((want + S - 1) / S, (V + 1023) / 1024));
+    int64_t ranges = (V + kMostRange - 1) / kMostRange;
+    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (want + S * ranges - 1) / (S * ranges)));
+    ranges = std::max<int64_t>(ranges, std::min<int64_t>((want + S * p.groups - 1) / (S * p.groups), (V + 1023) / 1024));
     p.range = (int)(((V + ranges - 1) / ranges + 7) & ~(int64_t)7);
     p.ranges = (int)((V + p.range - 1) / p.range);
-    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(rows, (want + S * p.ranges - 1) / (S * p.ranges)));
     p.items = (int64_t)p.ranges * p.groups * S;
     hipLaunchKernelGGL(adjust_kernel, dim3((uint32_t)std::min<int64_t>(p.items, 1 << 20)), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
