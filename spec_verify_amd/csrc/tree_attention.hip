@@ -32,7 +32,8 @@ namespace svq {
 namespace {
 
 constexpr int kTile = 64;          // tokens in a tile
-constexpr int kStaged = 256;       // parents kept in LDS; of wider trees the rest is read where it lies
+constexpr int kNodes = 64;         // trees up to this size have their paths as bits
+constexpr int kStaged = 256;       // of wider ones, parents kept in LDS; the rest is read where it lies
 constexpr int kEntries = 1024;     // page table entries kept in LDS
 constexpr float kSlack = 8.f;      // how far (in powers of two) scores may pass the maximum that weights refer to
 
@@ -62,6 +63,12 @@ struct Side {
     uint32_t ld;                  // in bytes
 };
 
+// A block of rows that its workgroup began and others go on with.
+struct Join {
+    int first, rows, head, row0;  // of the sequence: first row, number of (row, head) pairs; KV head; the block's first pair
+    int more;                     // parts that follow, one a team; 0: none
+};
+
 struct Params {
     const uint16_t *q;
     int64_t ld_q;
@@ -77,7 +84,7 @@ struct Params {
     int64_t ld_out;
     int M, S, heads, group;       // KV heads, query heads of each
     int teams, members;
-    int4 *joins;                  // [team][member]: sequence, head, block of rows, parts that follow the first
+    struct Join *joins;           // [team][member]
     float *parts;                 // [grid][2] blocks of sums, then of (maximum, sum)
     float2 *stats;
 };
@@ -229,7 +236,6 @@ struct Shape {
     // Places for keys, and for values: as many as keep some 100 KiB a compute unit in flight (8 KiB
     // pieces are not worth more waits)
     static constexpr int kSlots = kPart >= 32768 ? 2 : 4;
-    static constexpr bool kLag = kRows >= 128 && WR > 1;      // products, not bytes
     static constexpr int kArea = 2 * kSlots * kPart;
     // groups of operands read from LDS before their use: as registers allow
     static constexpr int kAhead = D * RT >= 512 ? 3 : 4;
@@ -289,7 +295,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         total = uniform(total);
         used = min(p.teams, total);
         if (team >= used) {
-            if (tid == 0) p.joins[w] = make_int4(0, 0, 0, 0);
+            if (tid == 0) p.joins[w].more = 0;
             return;
         }
         shares.q = (uint32_t)total / used;
@@ -321,7 +327,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
     }
     const int end = shares.begin(team + 1);
     int x = shares.begin(team);
-    int4 join = make_int4(0, 0, 0, 0);
+    Join join = {};
 
     while (x < end) {
         const Params &p = arguments();
@@ -396,8 +402,25 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             __syncthreads();
         };
         __syncthreads();  // the last unit's reads of LDS are done
-        if (parents && (p.window > 0 || t1 * kTile > sq.cached))
-            for (int i = tid; i < min(sq.n, kStaged); i += Z::kThreads) staged[i] = parents[i];
+        uint64_t *const lines = (uint64_t *)staged;  // of each node, itself and its ancestors
+        if (parents && (p.window > 0 || t1 * kTile > sq.cached)) {
+            if (sq.n > kNodes) {
+                for (int i = tid; i < min(sq.n, kStaged); i += Z::kThreads) staged[i] = parents[i];
+            } else if (wave == 0) {
+                // twice as far up in every round
+                int up = lane < sq.n ? parents[lane] : -1;
+                if (up >= lane) up = -1;
+                uint64_t line = 1ull << lane;
+                for (int far = 1; far < sq.n; far *= 2) {
+                    const int from = up < 0 ? lane : up;
+                    const uint64_t more = __shfl((unsigned long long)line, from);
+                    const int next = __shfl(up, from);
+                    if (up >= 0) line |= more;
+                    up = up < 0 ? -1 : next;
+                }
+                lines[lane] = line;
+            }
+        }
         auto parent_of = [&](int i) {
             const int up = i < kStaged ? staged[i] : parents[i];
             return up >= 0 && up < i ? up : -1;
@@ -446,25 +469,30 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             return __ballot(there);
         };
         // A tile's rows of BYTES bytes into LDS, in pieces of 1 KiB that the waves share: this
-        // wave's i-th.
-        auto fill_piece = [&](auto row_bytes, uint64_t from, uint32_t to, int i) {
+        // wave's i-th. (Its rows are the first piece's with other bits, and the swizzle is linear.)
+        auto place = [&](auto row_bytes) {
+            constexpr int BYTES = decltype(row_bytes)::value, CHUNKS = BYTES / 16, kPieces = kTile * BYTES / 1024;
+            const int row = wave * (kPieces > Z::kWaves ? kPieces / Z::kWaves : 1) * (64 / CHUNKS) + lane / CHUNKS;
+            return make_int2(row * 4, (lane % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row)) * 16);
+        };
+        auto fill_piece = [&](auto row_bytes, int2 at, uint64_t from, uint32_t to, int i) {
             constexpr int BYTES = decltype(row_bytes)::value, CHUNKS = BYTES / 16, kPieces = kTile * BYTES / 1024;
             constexpr int kMine = kPieces > Z::kWaves ? kPieces / Z::kWaves : 1;
-            const int l = fresh(lane), piece = wave * kMine + i;
-            if (kPieces < Z::kWaves && piece >= kPieces) return;
-            const int row = piece * (64 / CHUNKS) + l / CHUNKS;
-            const int chunk = l % CHUNKS ^ swizzle<CHUNKS, BYTES == D>(row);
-            const uint64_t a = (uint64_t)__shfl((long long)from, row);
-            load_to_lds(a + chunk * 16, to + piece * 1024);
+            if (kPieces < Z::kWaves && wave >= kPieces) return;
+            const int row = at.x + i * (64 / CHUNKS) * 4, chunk = at.y ^ swizzle<CHUNKS, BYTES == D>(i * (64 / CHUNKS)) * 16;
+            const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(row, (int)from);
+            const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(row, (int)(from >> 32));
+            load_to_lds(((uint64_t)hi << 32 | lo) + chunk, to + (wave * kMine + i) * 1024);
         };
-        auto fill = [&](auto row_bytes, uint64_t from, uint32_t to) {
+        auto fill = [&](auto row_bytes, int2 at, uint64_t from, uint32_t to) {
             constexpr int kPieces = kTile * decltype(row_bytes)::value / 1024;
 #pragma unroll
-            for (int i = 0; i < (kPieces > Z::kWaves ? kPieces / Z::kWaves : 1); ++i) fill_piece(row_bytes, from, to, i);
+            for (int i = 0; i < (kPieces > Z::kWaves ? kPieces / Z::kWaves : 1); ++i) fill_piece(row_bytes, at, from, to, i);
         };
         constexpr int kMine = Z::kPart / 1024 > Z::kWaves ? Z::kPart / 1024 / Z::kWaves : 1;  // pieces a wave loads at once
         constexpr std::integral_constant<int, D * (E4M3 ? 1 : 2)> cache_row{};
         constexpr std::integral_constant<int, 2 * D> bf16_row{};
+        const int2 cache_place = place(cache_row);
 
         // tiles that every row sees whole need no mask
         const int edge = p.window > 0 ? sq.sinks + sq.n - 1 : 0;  // (n - 1: no row is deeper)
@@ -479,7 +507,11 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 if (r < rows) {
                     auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
                     int depth = node;
-                    if (parents && p.window > 0) {
+                    uint64_t line = 0;
+                    if (parents && sq.n <= kNodes) {
+                        line = lines[node];
+                        depth = __popcll(line) - 1;
+                    } else if (parents && p.window > 0) {
                         depth = 0;
                         for (int i = parent_of(node); i >= 0; i = parent_of(i)) ++depth;
                     }
@@ -492,8 +524,15 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                     const int far = p.window > 0 ? p.window : INT32_MAX;            // ancestors nearer than that
                     const int64_t sunk = p.window > 0 ? (int64_t)p.sinks - sq.len : 0;  // depths below are sinks
                     const int64_t off = (int64_t)sq.cached - base;                  // bit of the sequence's first row
-                    if (!parents) {
-                        const uint64_t line = below(off + node + 1) & ~below(off);
+                    if (parents && sq.n <= kNodes) {
+                        // a path's nodes ascend with their depths
+                        uint64_t near = line, deep = line;
+                        for (int k = depth + 1 - far; k > 0; --k) near &= near - 1;
+                        for (int k = 0; k < sunk && deep; ++k) deep &= deep - 1;
+                        line = near | (line & ~deep);
+                        bits |= off >= 0 ? line << off : off > -64 ? line >> -off : 0;
+                    } else if (!parents) {
+                        line = below(off + node + 1) & ~below(off);
                         bits |= line & (~below(off + (int64_t)node - far + 1) | below(off + sunk));
                     } else {
                         int d = 0;
@@ -731,9 +770,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         // A tile is two halves of a step: scores and weights, then values. Keys and values have
         // SLOTS places each, and a place is filled again as soon as its tile is done with, by loads
         // between the matrix instructions. At the barrier before a tile's first half its keys are
-        // there, at the one before the second its values. Where the chip is short of products and
-        // not of bytes (LAG), the second half of the waves is half a step behind: the ones' weights
-        // are made beside the others' products.
+        // there, at the one before the second its values and all weights.
         const int count = cut - t0;
         const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
         auto nothing = [](int, int) {};
@@ -753,7 +790,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             return [&, any, from, to](int step, int steps) {
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
-                    if (any && step == i * steps / kMine) fill_piece(cache_row, from, to, i);
+                    if (any && step == i * steps / kMine) fill_piece(cache_row, cache_place, from, to, i);
             };
         };
         auto first_half = [&](int i, auto between) {
@@ -775,15 +812,14 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             // (the compiler knows of q's loads but not of the tiles': without this it would wait for
             // all of them at q's first use, in every step)
             wait_vmcnt<0>();
-            if constexpr (!Z::kLag) {
                 // keys of SLOTS tiles ahead, values of SLOTS - 1
                 for (int i = 0; i < min(SLOTS, count); ++i) {
-                    if (i) fill(cache_row, vb, values_at(i - 1));
+                    if (i) fill(cache_row, cache_place, vb, values_at(i - 1));
                     find(i);
                     vb = va;
-                    fill(cache_row, ka, keys_at(i));
+                    fill(cache_row, cache_place, ka, keys_at(i));
                 }
-                if (count < SLOTS) fill(cache_row, vb, values_at(count - 1));
+                if (count < SLOTS) fill(cache_row, cache_place, vb, values_at(count - 1));
                 for (int i = 0; i < count; ++i) {
                     const int left = count - 1 - i;
                     // loaded since its keys: values from its own on, keys of the tiles after it
@@ -800,50 +836,6 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                     sift(i);
                     add_values(std::bool_constant<E4M3>{}, values_at(i), loading(left >= SLOTS, ka, keys_at(i)));
                 }
-            } else {
-                const int late = wave >= Z::kWaves / 2;
-                for (int i = 0; i < min(SLOTS - 1, count); ++i) {
-                    find(i);
-                    fill(cache_row, ka, keys_at(i));
-                    fill(cache_row, va, values_at(i));
-                }
-                // Half 2 i is the early waves' first half of step i and the late ones' second half of
-                // step i - 1: keys of tile i + SLOTS - 1 are loaded, and in half 2 i + 1 its values.
-                // Their places were last read half a step before.
-                auto begin = [&](int half) {
-                    const int i = half >> 1;
-                    if (i < count) {
-                        // loaded since keys i: values i, and both of up to SLOTS - 2 tiles; since
-                        // values i: those, and the keys of the tile ahead
-                        const int since = 2 * max(min(SLOTS - 2, count - 1 - i), 0);
-                        wait_parts<kMine, 2 * SLOTS - 3>(half & 1 ? since + (i + SLOTS - 1 < count) : since + 1);
-                    }
-                    lds_barrier();
-                    if (i >= count) return;
-                    if (half & 1) {
-                        sift(i);
-                    } else {
-                        if (i + SLOTS - 1 < count) find(i + SLOTS - 1);
-                        prepare(i);
-                    }
-                };
-                auto loads_of = [&](int half) {
-                    const int ahead = (half >> 1) + SLOTS - 1;
-                    return loading(ahead < count, half & 1 ? va : ka, half & 1 ? values_at(ahead) : keys_at(ahead));
-                };
-                if (late) {
-                    begin(0);
-                    for (int k = 0; k < kMine; ++k) loads_of(0)(k, kMine);
-                }
-                for (int i = 0; i < count; ++i) {
-                    const int half = 2 * i + late;
-                    begin(half);
-                    first_half(i, loads_of(half));
-                    begin(half + 1);
-                    add_values(std::bool_constant<E4M3>{}, values_at(i), loads_of(half + 1));
-                }
-                if (!late) begin(2 * count);
-            }
         }
         // ---- beside an 8-bit cache, the chunk's rows ----
         if constexpr (E4M3) {
@@ -854,9 +846,10 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             for (int t = max(t0, sq.cache_tiles); t < t1; ++t) {
                 const int base = sq.cached + (t - sq.cache_tiles) * kTile;
                 const uint64_t there = locate(base, sq.cached + sq.n);
+                const int2 bf16_place = place(bf16_row);
                 lds_barrier();
-                fill(bf16_row, ka, area);
-                fill(bf16_row, va, area + kTile * 2 * D);
+                fill(bf16_row, bf16_place, ka, area);
+                fill(bf16_row, bf16_place, va, area + kTile * 2 * D);
                 make_masks(base, there);
                 wait_vmcnt<0>();
                 lds_barrier();
@@ -930,37 +923,35 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         }
         if (t0 == 0 && t1 < sq.tiles)
             // the parts that follow: one a team, up to the one with this unit's last step
-            join = make_int4(seq, h, block, shares.team_of(x - t1 + sq.tiles - 1) - team);
+            join = Join{sq.first, rows, h, row0, shares.team_of(x - t1 + sq.tiles - 1) - team};
     }
     if (tid == 0) arguments().joins[w] = join;
 }
 
-// Joins a block of rows whose first part is workgroup x's: a sixteenth of the rows a
-// workgroup, RW waves a row (few rows have many parts).
+// Joins a block of rows whose first part is workgroup x's: RW waves a row (few rows have
+// many parts), 4 / RW rows a workgroup.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void join_kernel(const Params p) {
     const int w = blockIdx.x;
-    const int4 j = p.joins[w];
-    if (j.w == 0) return;
-    constexpr int RW = ROWS >= 64 ? 1 : 64 / ROWS, E = D / 64, kAtOnce = 4 / RW;
+    const Join j = p.joins[w];
+    if (j.more == 0) return;
+    constexpr int RW = ROWS >= 64 ? 1 : 64 / ROWS, E = D / 64;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int first = min(max(p.starts[j.x], 0), p.M);
-    const int n = max(min(p.starts[j.x + 1], p.M) - first, 0);
     __shared__ float2 stat[4];
     __shared__ float vals[4][D];
     typedef float row_t __attribute__((ext_vector_type(E)));
-    for (int i0 = 0; i0 < ROWS / 16; i0 += kAtOnce) {
-        const int i = blockIdx.y * (ROWS / 16) + i0 + wave / RW, r = j.z * ROWS + i;
-        const bool here = r < n * p.group;
+    {
+        const int i = blockIdx.y * (4 / RW) + wave / RW, r = j.row0 + i;
+        const bool here = r < j.rows;
         float top = -INFINITY, sum = 0.f;
         row_t acc = 0.f;
         auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part * p.members)) * ROWS + i; };
         if (here)
             // 64 parts at a time: lane l's statistics, then the values by their weights
-            for (int p0 = wave % RW; p0 <= j.w; p0 += 64 * RW) {
+            for (int p0 = wave % RW; p0 <= j.more; p0 += 64 * RW) {
                 const int part = p0 + lane * RW;
                 float2 st = make_float2(-INFINITY, 0.f);
-                if (part <= j.w) st = p.stats[slot(part)];
+                if (part <= j.more) st = p.stats[slot(part)];
                 float high = fmaxf(top, st.x);
                 for (int d = 1; d < 64; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
                 const float b = decay(st.x, high), a = decay(top, high);
@@ -969,7 +960,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
                 sum = sum * a + add;
                 top = high;
                 acc *= a;
-                const int count = min(64, (j.w - p0) / RW + 1);
+                const int count = min(64, (j.more - p0) / RW + 1);
 #pragma unroll 8
                 for (int k = 0; k < count; ++k) {
                     const row_t v = *(const row_t *)(p.parts + slot(p0 + k * RW) * D + lane * E);
@@ -993,7 +984,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
         }
         if (here && wave % RW == 0) {
             const row_t o = acc * (sum == 0.f ? 0.f : 1.f / sum);
-            uint16_t *to = p.out + (int64_t)(first + r / p.group) * p.ld_out + (int64_t)(j.y * p.group + r % p.group) * D;
+            uint16_t *to = p.out + (int64_t)(j.first + p.by_group(r)) * p.ld_out + (int64_t)(j.head * p.group + r - p.by_group(r) * p.group) * D;
             if constexpr (E == 1) to[lane] = f32_to_bf16_rne(o[0]);
             else {
 #pragma unroll
@@ -1019,7 +1010,7 @@ AttendPlan plan_tree_attention(int64_t M, int64_t S, int64_t H, int64_t KVH, int
     }
     p.teams = std::max(1, num_cus / p.members);
     const size_t groups = (size_t)p.teams * p.members;
-    p.workspace_bytes = kCounterBytes + ((groups * 16 + 255) & ~(size_t)255) + 2 * groups * p.block_rows * (D * 4 + 8);
+    p.workspace_bytes = kCounterBytes + ((groups * sizeof(Join) + 255) & ~(size_t)255) + 2 * groups * p.block_rows * (D * 4 + 8);
     return p;
 }
 
@@ -1032,7 +1023,7 @@ hipError_t launch_shape(const Params &p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(p.teams * p.members), dim3(Z::kThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.teams * p.members, 16), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.teams * p.members, Z::kRows <= 64 ? 16 : 32), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1090,8 +1081,8 @@ hipError_t launch_tree_attention(const AttendPlan &plan, const void *q, int64_t 
     p.teams = plan.teams;
     p.members = plan.members;
     const size_t groups = (size_t)plan.teams * plan.members;
-    p.joins = (int4 *)ws_partials(workspace);
-    p.parts = (float *)((char *)p.joins + ((groups * 16 + 255) & ~(size_t)255));
+    p.joins = (Join *)ws_partials(workspace);
+    p.parts = (float *)((char *)p.joins + ((groups * sizeof(Join) + 255) & ~(size_t)255));
     p.stats = (float2 *)(p.parts + 2 * groups * plan.block_rows * D);
     switch (D) {
     case 64: return launch_type<64>(p, plan.block_rows, e4m3, stream);
