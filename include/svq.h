@@ -475,13 +475,13 @@ typedef struct svq_kv_cache {
                               p*strides[0] + t*strides[1] + h*strides[2]; D contiguous
                               elements, 16-byte aligned (pointers and strides) */
     int64_t k_strides[3];  /* page, token, head; in elements. Pages and tokens lie less than
-                              4 GiB apart (if there are several) */
+                              4 GiB apart; of a single one the stride is not used */
     int64_t v_strides[3];
     int64_t pages;         /* pages in the pool; with none k and v may be NULL */
     int32_t page_size;     /* tokens in a page, 1 .. 2^20 */
     int32_t type;          /* SVQ_CACHE_* */
-    const float *k_scale;  /* E4M3: fp32 [KVH], a cached value is code * scale; NULL for 1. */
-    const float *v_scale;  /* BF16: both NULL */
+    const float *k_scale;  /* E4M3: fp32 [KVH], positive; a cached value is code * scale; */
+    const float *v_scale;  /* NULL for 1. BF16: both NULL */
     const int32_t *page_table; /* int32 [S][ld_table], the first max_pages of each row: the
                               pages of a sequence in order. Tokens of an entry outside
                               [0, pages) are not seen */
@@ -503,7 +503,8 @@ size_t svq_tree_attention_workspace_bytes(int64_t M, int64_t S, int32_t H, int32
  * keys and values are rows beside q, not in the cache: what is accepted is written to
  * the cache afterwards. A score of -inf has weight zero; a row that sees nothing, or
  * only such scores, is zero. Rows outside every sequence are left as they were. What a
- * row does not see, infinities and NaN too, does not change its result.
+ * row does not see, infinities and NaN too, does not change its result. With starts that
+ * do not ascend nothing is written.
  * Scores, weights' sums and products are fp32; weights enter the second product as bf16;
  * out is rounded to bf16 (nearest even).
  *   q        bf16 [M][ld_q], the first H*D of each row: H heads of D elements
@@ -515,7 +516,9 @@ size_t svq_tree_attention_workspace_bytes(int64_t M, int64_t S, int32_t H, int32
  *   columns used. D is 64, 128 or 256, H a multiple of KVH, H <= 65536.
  *   workspace  at least svq_tree_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *              not cleared; as for svq_adapter_add.
- * out and the workspace must not overlap any input or each other.
+ * out and the workspace must not overlap any input or each other. KVH times the tiles of 64
+ * tokens that a sequence may have (max_pages * page_size and M) times the blocks of 16
+ * (row, head of a group) pairs must stay below 2^31 (SVQ_ERR_DIM).
  */
 int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
                        const svq_kv_cache *cache, const int32_t *starts, const int32_t *parents, float scale,

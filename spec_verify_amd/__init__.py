@@ -803,7 +803,7 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, starts, paren
 
     q [M, H, D] and the chunk's k, v [M, KVH, D], bf16, may be column slices of a fused
     projection's output. k_cache, v_cache [pages, page_size, KVH, D], bf16 or float8_e4m3fn
-    (or its codes in uint8) with k_scale, v_scale float32 [KVH] or None, in any order of the
+    (or its codes in uint8) with positive k_scale, v_scale float32 [KVH] or None, in any order of the
     first three dimensions; page_table int32 [S, max_pages] and lengths int32 [S]: the pages and the
     number of each sequence's cached tokens. starts int32 [S + 1]: sequence s owns rows
     starts[s] .. starts[s + 1] - 1; parents int32 [M]: each row's parent, counted from its

@@ -49,16 +49,16 @@ int check_attention_shape(int64_t M, int64_t S, int32_t H, int32_t KVH, int32_t 
     return SVQ_OK;
 }
 
-// Strides of one side of a cache: whole 16 bytes, pages and tokens less than 4 GiB apart,
-// and an extent that 63 bits hold.
+// Strides of one side of a cache, in the dimensions that have several entries: whole 16 bytes,
+// pages and tokens less than 4 GiB apart, and an extent that 63 bits hold.
 int check_strides(const int64_t *st, const svq_kv_cache &c, int32_t KVH, int32_t D, int64_t size, size_t *bytes) {
     const int64_t most = int64_t(1) << 46;
     const int64_t count[3] = {c.pages, c.page_size, KVH};
     int64_t extent = D;
     for (int i = 0; i < 3; ++i) {
-        if (st[i] < 0 || st[i] > most || (i < 2 && st[i] * size >= (int64_t(1) << 32))) return SVQ_ERR_DIM;
+        if (count[i] <= 1) continue;
+        if (st[i] < 0 || st[i] > most / (count[i] - 1) || (i < 2 && st[i] * size >= (int64_t(1) << 32))) return SVQ_ERR_DIM;
         if (st[i] * size % 16) return SVQ_ERR_ALIGN;
-        if (count[i] > 1 && st[i] > most / (count[i] - 1)) return SVQ_ERR_DIM;
         extent += st[i] * (count[i] - 1);
     }
     *bytes = c.pages ? (size_t)(extent * size) : 0;

@@ -278,21 +278,24 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         const int s0 = min(tid * per, p.S), s1 = min(s0 + per, p.S);
         Sequence each;
         int sum = 0;
+        bool bad = false;
         for (int s = s0; s < s1; ++s) {
             each.read(p, s);
             each.count<E4M3, Z::kRows>(p);
             sum += each.steps(p);
+            bad |= p.starts[s + 1] < p.starts[s];
         }
         const int run = wave_scan(sum);
         if (lane == 63) scratch[wave] = run;
-        __syncthreads();
+        // (sequences that share rows may have more steps than the host has counted: none is taken)
+        bad = __syncthreads_or(bad);
         int before = run - sum, total = 0;
 #pragma unroll
         for (int i = 0; i < Z::kWaves; ++i) {
             if (i < wave) before += scratch[i];
             total += scratch[i];
         }
-        total = uniform(total);
+        total = bad ? 0 : uniform(total);
         used = min(p.teams, total);
         if (team >= used) {
             if (tid == 0) p.joins[w].more = 0;

@@ -338,6 +338,90 @@ def test_long_cache_past_32_bits():
         del big
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("page,window,sinks", [(1, 0, 0), (1, 1700, 300), (3, 0, 0)])
+def test_more_pages_than_are_kept_at_a_time(page, window, sinks, e4m3):
+    """Workgroups that pass thousands of table entries of a sequence."""
+    n = 32 if page == 1 else 16
+    Problem(20, [1 + i % 2 for i in range(n)], [2500 * page - 7 * i for i in range(n)], H=16, G=8, page=page, e4m3=e4m3,
+            window=window, sinks=sinks).check(f"pages of {page}")
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30, 3.0])
+def test_any_scale(scale):
+    p = Problem(21, [5, 20], [200, 3], tree=True)
+    _say("scale", scale)
+    got = p.call(scale=scale).double().cpu().numpy()
+    want, bound, _ = p.expected(scale=scale)
+    assert (np.abs(got - want) <= bound).all()
+
+
+def test_two_streams_at_once():
+    a, b = Problem(22, [64, 30], [3000, 900], H=12, G=2, D=256), Problem(23, [5], [20000], H=12, G=2, D=128)
+    want = [x.call() for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    held = []
+    for x in (a, b):
+        held.append({k: v for k, v in dict(
+            q=x.q.cuda(), k=x.k.cuda(), v=x.v.cuda(), k_cache=x.caches[0].cuda(), v_cache=x.caches[1].cuda(),
+            page_table=torch.from_numpy(x.table).cuda(), lengths=torch.from_numpy(x.lengths).cuda(),
+            starts=torch.from_numpy(x.starts).cuda(), parents=torch.from_numpy(x.parents).cuda()).items()})
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(x.call(**held[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o.view(torch.int16), want[i].view(torch.int16)) for o in outs[i])
+
+
+def test_starts_that_do_not_ascend_write_nothing():
+    p = Problem(24, [20, 30, 14], [500, 3, 70], tree=True)
+    for starts in ([0, 64, 0, 64], [0, 20, 10, 64], [64, 0, 64, 0]):
+        p.starts = np.array(starts, dtype=np.int32)
+        _say("starts", starts)
+        out = torch.full_like(p.q, 7.0).cuda()
+        p.call(out=out)
+        torch.cuda.synchronize()
+        assert (out == 7.0).all()
+
+
+def test_starts_outside_are_clamped():
+    p = Problem(25, [20, 30, 14], [500, 3, 70], tree=True)
+    want = p.call()
+    p.starts = np.array([-5, 20, 50, 2 ** 31 - 1], dtype=np.int32)
+    assert torch.equal(p.call().view(torch.int16), want.view(torch.int16))
+
+
+def test_a_pool_of_one_page_has_any_stride():
+    """Of a page that has no other beside it the stride is not looked at, 4 GiB or more included."""
+    p = Problem(26, [3], [10], tree=True)
+    p.table[0, 0] = 0
+    p.caches = [c[:1].contiguous() for c in p.caches]
+    want = p.call()
+    wide = [c.cuda().as_strided(c.shape, (1 << 40,) + c.stride()[1:]) for c in p.caches]
+    got = p.call(k_cache=wide[0], v_cache=wide[1])
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    p.check("one page")
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_pages_shared_by_sequences(e4m3):
+    p = Problem(27, [5, 9, 2], [300, 280, 299], H=12, G=2, D=256, e4m3=e4m3)
+    p.table[1, :10] = p.table[0, :10]
+    p.table[2, :15] = p.table[0, :15]
+    p.check("a common prefix")
+
+
+@pytest.mark.parametrize("rows,lengths", [([200, 1, 1, 1, 1, 1], [70, 3000, 0, 1, 64, 900]), ([1] * 40 + [600], [50] * 41)])
+def test_sequences_of_very_different_rows(rows, lengths):
+    """The shape follows the average: long ones take many blocks, some members of a team none."""
+    Problem(28, rows, lengths, H=8, G=1, D=64).check(f"{max(rows)} rows of {sum(rows)}")
+    Problem(29, rows, lengths, H=8, G=1, D=64, window=40, sinks=5, e4m3=True).check(f"{max(rows)} rows of {sum(rows)}, window")
+
+
 def test_split_sequences_are_as_whole_ones():
     """One sequence over all workgroups, and the same among many, where it has few: the same within the bound."""
     one = Problem(15, [5], [20000], H=12, G=2, D=128)

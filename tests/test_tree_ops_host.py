@@ -60,6 +60,29 @@ def test_attention_refusals(L, status, change):
     assert _attend(L, **change) == status
 
 
+# (without a workspace, what is otherwise valid ends with status 8)
+@pytest.mark.parametrize("status,change", [
+    (2, dict(k0=1 << 31)), (2, dict(v1=1 << 31)), (2, dict(type=1, k0=1 << 32)), (8, dict(type=1, k0=(1 << 32) - 16)),
+    (8, dict(k0=1 << 40, pages=1)), (8, dict(v1=1 << 40, page_size=1)), (8, dict(k0=-5, pages=1)), (8, dict(G=1, k2=3)),
+    (2, dict(ldk=1 << 31)), (2, dict(ldv=1 << 31)), (8, dict(ldq=1 << 31, ldo=1 << 31)),
+    (8, dict(max_pages=1 << 20, page_size=1 << 10, ld_table=1 << 20)),
+    (2, dict(max_pages=1 << 20, page_size=1 << 10, ld_table=1 << 20, M=2000)),
+    (2, dict(M=1 << 20)), (8, dict(M=1 << 17)),
+    (8, dict(table=0, max_pages=0)), (8, dict(table=0, max_pages=0, ld_table=0)),
+    (8, dict(parents=None)), (8, dict(type=1)), (8, dict(type=1, ks=P[11], vs=P[12])),
+])
+def test_attention_limits(L, status, change):
+    assert _attend(L, ws=None, **change) == status
+
+
+def test_a_pool_without_pages_has_no_address(L):
+    import spec_verify_amd as svq
+    for pages, status in ((0, 8), (1, 1)):
+        c = svq._CACHE.pack(*{**CACHE, "k": 0, "v": 0, "pages": pages}.values())
+        assert L.svq_tree_attention(P[4], 1024, P[5], 512, P[6], 512, c, P[7], None, 0.1, 0, 0, P[9], 1024, 20, 4, 4, 2, 256,
+                                    None, 0, None) == status
+
+
 def test_attention_workspace_query(L):
     q = L.svq_tree_attention_workspace_bytes
     for bad in ((0, 1, 4, 2, 64), (5, 0, 4, 2, 64), (5, 1, 4, 3, 64), (5, 1, 4, 2, 80), (5, 1, 2, 4, 64),
