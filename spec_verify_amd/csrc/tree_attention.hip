@@ -931,69 +931,83 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
     if (tid == 0) arguments().joins[w] = join;
 }
 
-// Joins a block of rows whose first part is workgroup x's: RW waves a row (few rows have
-// many parts), 4 / RW rows a workgroup.
+// Joins a block of rows whose first part is workgroup x's. A row takes D / 4 lanes of kSplit
+// waves (few rows have many parts).
+template <int D, int ROWS>
+struct JoinShape {
+    static constexpr int kLanes = D / 4, kSplit = ROWS >= 64 ? 1 : 64 / ROWS;
+    static constexpr int kRows = 64 / kLanes * (4 / kSplit);  // of a workgroup of 4 waves
+};
+
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void join_kernel(const Params p) {
+    using Z = JoinShape<D, ROWS>;
     const int w = blockIdx.x;
     const Join j = p.joins[w];
     if (j.more == 0) return;
-    constexpr int RW = ROWS >= 64 ? 1 : 64 / ROWS, E = D / 64;
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    __shared__ float2 stat[4];
-    __shared__ float vals[4][D];
-    typedef float row_t __attribute__((ext_vector_type(E)));
-    {
-        const int i = blockIdx.y * (4 / RW) + wave / RW, r = j.row0 + i;
-        const bool here = r < j.rows;
-        float top = -INFINITY, sum = 0.f;
-        row_t acc = 0.f;
-        auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part * p.members)) * ROWS + i; };
-        if (here)
-            // 64 parts at a time: lane l's statistics, then the values by their weights
-            for (int p0 = wave % RW; p0 <= j.more; p0 += 64 * RW) {
-                const int part = p0 + lane * RW;
-                float2 st = make_float2(-INFINITY, 0.f);
-                if (part <= j.more) st = p.stats[slot(part)];
-                float high = fmaxf(top, st.x);
-                for (int d = 1; d < 64; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
-                const float b = decay(st.x, high), a = decay(top, high);
-                float add = st.y * b;
-                for (int d = 1; d < 64; d <<= 1) add += __shfl_xor(add, d);
-                sum = sum * a + add;
-                top = high;
-                acc *= a;
-                const int count = min(64, (j.more - p0) / RW + 1);
-#pragma unroll 8
-                for (int k = 0; k < count; ++k) {
-                    const row_t v = *(const row_t *)(p.parts + slot(p0 + k * RW) * D + lane * E);
-                    acc += v * bits_f32(__builtin_amdgcn_readlane(f32_bits(b), k));
-                }
-            }
-        if constexpr (RW > 1) {
-            if (lane == 0) stat[wave] = make_float2(top, sum);
-            *(row_t *)&vals[wave][lane * E] = acc;
-            __syncthreads();
-            float high = -INFINITY;
-            for (int v = 0; v < RW; ++v) high = fmaxf(high, stat[wave / RW * RW + v].x);
-            sum = 0.f;
-            acc = 0.f;
-            for (int v = 0; v < RW; ++v) {
-                const float2 st = stat[wave / RW * RW + v];
-                const float b = decay(st.x, high);
-                sum += st.y * b;
-                acc += *(row_t *)&vals[wave / RW * RW + v][lane * E] * b;
-            }
-        }
-        if (here && wave % RW == 0) {
-            const row_t o = acc * (sum == 0.f ? 0.f : 1.f / sum);
-            uint16_t *to = p.out + (int64_t)(j.first + p.by_group(r)) * p.ld_out + (int64_t)(j.head * p.group + r - p.by_group(r) * p.group) * D;
-            if constexpr (E == 1) to[lane] = f32_to_bf16_rne(o[0]);
-            else {
+    constexpr int L = Z::kLanes, RW = Z::kSplit, kBatch = 8;
+    const int lane = threadIdx.x & 63, wave = wave_id(), l = lane % L;
+    __shared__ float2 stat[4][64 / L];
+    __shared__ f32x4 vals[4][64];
+    const int i = blockIdx.y * Z::kRows + wave / RW * (64 / L) + lane / L, r = j.row0 + i;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (rows past the last have a place in every part too: what it holds goes nowhere)
+    auto slot = [&](int part) { return (part == 0 ? 2 * (int64_t)w + 1 : 2 * ((int64_t)w + part * p.members)) * ROWS + i; };
+    // L parts at a time: lane l's statistics, then the values by their weights, the first ones
+    // loaded beside the statistics
+    for (int p0 = wave % RW; p0 <= j.more; p0 += L * RW) {
+        const int part = p0 + l * RW, count = min(L, (j.more - p0) / RW + 1);
+        float2 st = make_float2(-INFINITY, 0.f);
+        if (part <= j.more) st = p.stats[slot(part)];
+        f32x4 v[kBatch];
+        auto load = [&](int k0) {
 #pragma unroll
-                for (int e = 0; e < E; e += 2) ((uint32_t *)to)[(lane * E + e) / 2] = pack_bf16(o[e], o[e + 1]);
+            for (int k = 0; k < kBatch; ++k) {
+                v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (k0 + k < count) v[k] = *(const f32x4 *)(p.parts + slot(p0 + (k0 + k) * RW) * D + l * 4);
             }
+        };
+        load(0);
+        float high = fmaxf(top, st.x);
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) high = fmaxf(high, __shfl_xor(high, d));
+        const float b = decay(st.x, high), a = decay(top, high);
+        float add = st.y * b;
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) add += __shfl_xor(add, d);
+        sum = sum * a + add;
+        top = high;
+        acc *= a;
+        for (int k0 = 0; k0 < count; k0 += kBatch) {
+            if (k0) load(k0);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) acc += v[k] * __shfl(b, k0 + k, L);
         }
+    }
+    if constexpr (RW > 1) {
+        if (l == 0) stat[wave][lane / L] = make_float2(top, sum);
+        vals[wave][lane] = acc;
+        __syncthreads();
+        if (wave % RW) return;
+        float high = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < RW; ++v) high = fmaxf(high, stat[wave + v][lane / L].x);
+        sum = 0.f;
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < RW; ++v) {
+            const float2 st = stat[wave + v][lane / L];
+            const float b = decay(st.x, high);
+            sum += st.y * b;
+            acc += vals[wave + v][lane] * b;
+        }
+    }
+    if (r < j.rows) {
+        const f32x4 o = acc * (sum == 0.f ? 0.f : 1.f / sum);
+        const int node = p.by_group(r);
+        *(uint2 *)(p.out + (int64_t)(j.first + node) * p.ld_out + (int64_t)(j.head * p.group + r - node * p.group) * D + l * 4) =
+            make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
     }
 }
 
@@ -1026,7 +1040,7 @@ hipError_t launch_shape(const Params &p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(p.teams * p.members), dim3(Z::kThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.teams * p.members, Z::kRows <= 64 ? 16 : 32), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((join_kernel<D, Z::kRows>), dim3(p.teams * p.members, Z::kRows / JoinShape<D, Z::kRows>::kRows), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
