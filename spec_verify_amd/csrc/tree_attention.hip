@@ -945,7 +945,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
     const int w = blockIdx.x;
     const Join j = p.joins[w];
     if (j.more == 0) return;
-    constexpr int L = Z::kLanes, RW = Z::kSplit, kBatch = 8;
+    constexpr int L = Z::kLanes, RW = Z::kSplit, kBatch = RW > 1 ? 16 : 8;
     const int lane = threadIdx.x & 63, wave = wave_id(), l = lane % L;
     __shared__ float2 stat[4][64 / L];
     __shared__ f32x4 vals[4][64];
@@ -982,7 +982,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
         for (int k0 = 0; k0 < count; k0 += kBatch) {
             if (k0) load(k0);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) acc += v[k] * __shfl(b, k0 + k, L);
+            for (int k = 0; k < kBatch; ++k) acc += v[k] * (L == 64 ? bits_f32(__builtin_amdgcn_readlane(f32_bits(b), k0 + k)) : __shfl(b, k0 + k, L));
         }
     }
     if constexpr (RW > 1) {
