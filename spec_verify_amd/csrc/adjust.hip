@@ -5,6 +5,12 @@
 // history's tokens of that range in LDS once (16384 words of 32 bits: two workgroups a compute
 // unit). Then, row by row, it adds the row's path to the counts and takes the row before's out,
 // and streams the row's logits past them; the next row's are loaded meanwhile.
+//
+// Bound by the logits' way in and out. Measured (V = 248320; replayed):
+//   1 row behind 1500 tokens              7.2 us  latency of one workgroup: history, row, stores
+//   128 rows of 32, histories of 8192    39.9 us  3.2 TB/s: each of the 16 ranges reads the history again,
+//                                                 and has 4 rows to spread that over
+//   512 rows of 8, histories of 4096    113 us    4.5 TB/s, 94% of a copy
 #include <algorithm>
 
 #include "svq_tree.h"
@@ -246,8 +252,8 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
             auto vector = [&](uint4 x, uint32_t open, int v) {
                 open = !allowed ? 0xFFu : lead == 0 ? open >> (v & 31) & 0xFFu : bits_at(allowed, v, (p.V - 1) >> 5);
                 // Few logits are marked (3300 of 248320 by a history of 4096): one after the other in a
-                // lane takes a wave two or three rounds (computing all 8: 312 vector instructions, 220 us
-                // for 512 rows; so 136 us).
+                // lane takes a wave two or three rounds (for 512 rows, then 203 us; computing all 8 takes 312
+                // vector instructions, 220 us).
                 uint32_t marked = bits_at(marks, v - v0, kMostRange / 32 + 1) & open;
                 while (marked) {
                     const int e = __builtin_ctz(marked), k = e >> 1, shift = 16 * (e & 1);

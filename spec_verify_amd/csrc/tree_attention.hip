@@ -21,6 +21,18 @@
 // every workgroup finds its equal part of all steps from the lengths, so sequences of very
 // different lengths keep the chip equally busy. A block of rows that ends up in several
 // workgroups is joined by a second launch from its parts' maxima, sums and fp32 values.
+//
+// Measured (24 query heads on 4 key heads, D = 256; both launches, replayed):
+//   1 row over 1500 tokens                       16.4 us  latency: 11.7 (lengths 0.8, shares 0.5, q 1,
+//                                                         first tiles 2.4, steps and sums) and the join 4
+//   5 rows over 65000                            66.4 us  the cache at 4.0 TB/s
+//   32 x 4 rows over 8192, 8-bit cache          147 us    the cache at 3.7 TB/s; decoding to bf16 and the
+//                                                         products' issue stand beside the loads
+//   32 x 64 rows over 4096                      365 us    565 TFLOP/s. No unit is full: matrix 28% of
+//                                                         their cycles, LDS 35%, vector 38%; without its
+//                                                         loads 391 of then 399 us, without its products 329
+//   16 x 24 rows, window 2000, D = 128, 20 heads 43 us    34 in 8 steps a workgroup between prologue and
+//                                                         parts, 10 of join
 #include <algorithm>
 #include <type_traits>
 
@@ -35,7 +47,9 @@ constexpr int kTile = 64;          // tokens in a tile
 constexpr int kNodes = 64;         // trees up to this size have their paths as bits
 constexpr int kStaged = 256;       // of wider ones, parents kept in LDS; the rest is read where it lies
 constexpr int kEntries = 1024;     // page table entries kept in LDS
-constexpr float kSlack = 8.f;      // how far (in powers of two) scores may pass the maximum that weights refer to
+// How far (in powers of two) scores may pass the reference of the weights before it moves: weights
+// up to 2^8 cost fp32 sums nothing, and sums and columns are then rescaled in few steps only.
+constexpr float kSlack = 8.f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -226,16 +240,20 @@ __device__ __forceinline__ void wait_parts(int n) {
 }
 
 // D elements a head; WR groups of waves over rows, RT 16-row tiles each; WK waves a group,
-// which share a tile's tokens for the scores, and the columns for the sums.
+// which share a tile's tokens for the scores, and the columns for the sums: each key and each
+// value is read from LDS once a group, and a wave's sums stay in D / 16 / WK * RT quads of
+// registers. (32 x 64 rows at D = 256, then 399 us: 8 groups of one wave 401 to 408, 4 waves of
+// 512 registers 456, half of the waves half a step behind the others 399 for 392 without; 32 rows
+// as one group of two tiles, 4 waves, 165 us for 148 with 8-bit codes.)
 template <int D, bool E4M3, int RT, int WR, int WK>
 struct Shape {
     static constexpr int kWaves = WR * WK, kThreads = 64 * kWaves;
     static constexpr int kRows = 16 * RT * WR;
     static constexpr int kBlocks = kTile / 16 / WK;           // 16-token blocks of a tile that a wave weighs
     static constexpr int kPart = kTile * D * (E4M3 ? 1 : 2);  // bytes of a tile's keys, or values
-    // Places for keys, and for values: as many as keep some 100 KiB a compute unit in flight (8 KiB
-    // pieces are not worth more waits)
-    static constexpr int kSlots = kPart >= 32768 ? 2 : 4;
+    // Places for keys, and for values: a tile is worked on while the next is on its way (four
+    // places of parts under 32 KiB: 151 us for 147 with 8-bit codes, 44.8 for 43.2 at D = 128)
+    static constexpr int kSlots = 2;
     static constexpr int kArea = 2 * kSlots * kPart;
     // groups of operands read from LDS before their use: as registers allow
     static constexpr int kAhead = D * RT >= 512 ? 3 : 4;
@@ -776,7 +794,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         // there, at the one before the second its values and all weights.
         const int count = cut - t0;
         const int limit = E4M3 ? sq.cached : sq.cached + sq.n;
-        auto nothing = [](int, int) {};
+        auto nothing = [](int, int) {};  // (beside the chunk's tiles nothing is loaded)
         auto keys_at = [&](int i) { return area + (i & (SLOTS - 1)) * Z::kPart; };
         auto values_at = [&](int i) { return area + (SLOTS + (i & (SLOTS - 1))) * Z::kPart; };
         uint32_t masked = 0;  // of the tiles in LDS, which need a mask: bit i & (2 SLOTS - 1)
@@ -815,30 +833,30 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             // (the compiler knows of q's loads but not of the tiles': without this it would wait for
             // all of them at q's first use, in every step)
             wait_vmcnt<0>();
-                // keys of SLOTS tiles ahead, values of SLOTS - 1
-                for (int i = 0; i < min(SLOTS, count); ++i) {
-                    if (i) fill(cache_row, cache_place, vb, values_at(i - 1));
-                    find(i);
-                    vb = va;
-                    fill(cache_row, cache_place, ka, keys_at(i));
-                }
-                if (count < SLOTS) fill(cache_row, cache_place, vb, values_at(count - 1));
-                for (int i = 0; i < count; ++i) {
-                    const int left = count - 1 - i;
-                    // loaded since its keys: values from its own on, keys of the tiles after it
-                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
-                    else wait_parts<kMine, 2 * SLOTS>(2 * left + 1);
-                    lds_barrier();
-                    prepare(i);
-                    first_half(i, loading(left >= SLOTS - 1, vb, values_at(i + SLOTS - 1)));
-                    if (left >= SLOTS) find(i + SLOTS);
-                    vb = va;
-                    if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
-                    else wait_parts<kMine, 2 * SLOTS>(2 * left);
-                    lds_barrier();
-                    sift(i);
-                    add_values(std::bool_constant<E4M3>{}, values_at(i), loading(left >= SLOTS, ka, keys_at(i)));
-                }
+            // keys of SLOTS tiles ahead, values of SLOTS - 1
+            for (int i = 0; i < min(SLOTS, count); ++i) {
+                if (i) fill(cache_row, cache_place, vb, values_at(i - 1));
+                find(i);
+                vb = va;
+                fill(cache_row, cache_place, ka, keys_at(i));
+            }
+            if (count < SLOTS) fill(cache_row, cache_place, vb, values_at(count - 1));
+            for (int i = 0; i < count; ++i) {
+                const int left = count - 1 - i;
+                // loaded since its keys: values from its own on, keys of the tiles after it
+                if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                else wait_parts<kMine, 2 * SLOTS>(2 * left + 1);
+                lds_barrier();
+                prepare(i);
+                first_half(i, loading(left >= SLOTS - 1, vb, values_at(i + SLOTS - 1)));
+                if (left >= SLOTS) find(i + SLOTS);
+                vb = va;
+                if (left >= SLOTS - 1) wait_vmcnt<2 * (SLOTS - 1) * kMine>();
+                else wait_parts<kMine, 2 * SLOTS>(2 * left);
+                lds_barrier();
+                sift(i);
+                add_values(std::bool_constant<E4M3>{}, values_at(i), loading(left >= SLOTS, ka, keys_at(i)));
+            }
         }
         // ---- beside an 8-bit cache, the chunk's rows ----
         if constexpr (E4M3) {
@@ -1015,10 +1033,14 @@ __global__ __launch_bounds__(256) void join_kernel(const Params p) {
 
 AttendPlan plan_tree_attention(int64_t M, int64_t S, int64_t H, int64_t KVH, int64_t D, int num_cus) {
     AttendPlan p{};
-    const int64_t rows = (M * (H / KVH) + S - 1) / S;  // of a sequence, on average
+    // Blocks as tall as a sequence's rows on average, up to 128 (of two that hold them the lower):
+    // 6 rows as a block of 16 / 32 take 16.6 / 17.6 us; 24 rows as 32 / 64: 154 / 156; 120 rows as
+    // 32 / 64 / 128: 61 / 48.6 / 48.5; 384 rows: 914 / 553 / 381 (the tokens go through LDS once a block).
+    const int64_t rows = (M * (H / KVH) + S - 1) / S;
     p.block_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    // A sequence's blocks of rows read the same tokens: up to 8 workgroups take them side by side.
-    // Of the numbers of members that leave fewest idle the largest.
+    // A sequence's blocks of rows read the same tokens: up to 8 workgroups take them side by side, so
+    // that the caches keep them (3 blocks: 370 us for 396, 0.6 GB of memory traffic for 1.6). Of the
+    // numbers of members that leave fewest idle the largest.
     const int64_t blocks = (rows + p.block_rows - 1) / p.block_rows;
     p.members = 1;
     for (int64_t m = 2; m <= 8 && m <= blocks; ++m) {
