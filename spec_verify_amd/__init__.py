@@ -803,9 +803,9 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, starts, paren
 
     q [M, H, D] and the chunk's k, v [M, KVH, D], bf16, may be column slices of a fused
     projection's output. k_cache, v_cache [pages, page_size, KVH, D], bf16 or float8_e4m3fn
-    (or its codes in uint8) with positive k_scale, v_scale float32 [KVH] or None, in any order of the
-    first three dimensions; page_table int32 [S, max_pages] and lengths int32 [S]: the pages and the
-    number of each sequence's cached tokens. starts int32 [S + 1]: sequence s owns rows
+    (or its codes in uint8) with positive k_scale, v_scale float32 [KVH] or None, in any order of
+    the first three dimensions; page_table int32 [S, max_pages] and lengths int32 [S]: the pages and
+    the number of each sequence's cached tokens. starts int32 [S + 1]: sequence s owns rows
     starts[s] .. starts[s + 1] - 1; parents int32 [M]: each row's parent, counted from its
     sequence's first row, or None for a chain. scale: 1 / sqrt(D) if None. window > 0: only the
     `window` last positions, the row's own among them, and the first `sinks` are seen. Returns
@@ -815,6 +815,8 @@ def tree_attention(q, k, v, k_cache, v_cache, page_table, lengths, starts, paren
     bf16, i32 = kd.bf16, kd.i32
     if not isinstance(q, kd.Tensor) or q.dim() != 3 or not isinstance(k, kd.Tensor) or k.dim() != 3:
         raise ValueError("q must be [M, H, D] and k [M, KVH, D]")
+    if not (-(1 << 31) <= window < 1 << 31 and -(1 << 31) <= sinks < 1 << 31):
+        raise ValueError(f"window and sinks must fit in 32 bits, got {window} and {sinks}")
     dev = q.device
     if not q.is_cuda:
         raise ValueError(f"q must be a device tensor, got {dev}")

@@ -148,6 +148,9 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
         svq.tree_attention(bf, bf, bf, cache, cache, i.view(1, 4), i[:1], i[:2])
     with pytest.raises(ValueError, match=r"\[M, H, D\]"):
         svq.tree_attention(bf[0], bf, bf, cache, cache, i.view(1, 4), i[:1], i[:2])
+    for limits in (dict(window=(1 << 32) + 5), dict(sinks=1 << 31), dict(window=-(1 << 31) - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            svq.tree_attention(bf, bf, bf, cache, cache, i.view(1, 4), i[:1], i[:2], **limits)
     with pytest.raises(ValueError, match="device tensor"):
         svq.adjust_logits(bf[0], i.view(1, 4), i[:1], i[:2], i[:2])
     with pytest.raises(TypeError, match="logits must be"):
