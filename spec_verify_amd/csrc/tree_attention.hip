@@ -38,13 +38,12 @@
 
 #include "svq_dma.h"
 #include "svq_tree.h"
+#include "svq_tree_sight.h"
 
 namespace svq {
 
 namespace {
 
-constexpr int kTile = 64;          // tokens in a tile
-constexpr int kNodes = 64;         // trees up to this size have their paths as bits
 constexpr int kStaged = 256;       // of wider ones, parents kept in LDS; the rest is read where it lies
 constexpr int kEntries = 1024;     // page table entries kept in LDS
 // How far (in powers of two) scores may pass the reference of the weights before it moves: weights
@@ -104,11 +103,8 @@ struct Params {
 };
 
 // A sequence's rows and the numbering of the tokens that they may see.
-struct Sequence {
+struct Sequence : Numbering {
     int first, n;      // its rows
-    int len;           // cached tokens
-    int sinks, from;   // tokens 0 .. sinks - 1 of the cache come first, then those from `from` on
-    int cached;        // how many that are
     int cache_tiles;   // E4M3: tiles of cached tokens; the chunk's follow in tiles of their own
     int tiles;
     int blocks, runs;  // blocks of rows; times that a team takes as many as it has members
@@ -120,21 +116,12 @@ struct Sequence {
     }
     template <bool E4M3, int ROWS>
     __device__ __forceinline__ void count(const Params &p) {
-        sinks = 0;
-        from = 0;
-        if (p.window > 0) {
-            sinks = min(max(p.sinks, 0), len);
-            // the first row, at position len, sees the window's oldest token
-            from = min(max(max(len - p.window, -1) + 1, sinks), len);
-        }
-        cached = sinks + len - from;
+        Numbering::count(p.window, p.sinks);
         cache_tiles = (cached + kTile - 1) / kTile;
         tiles = E4M3 ? cache_tiles + (n + kTile - 1) / kTile : (cached + n + kTile - 1) / kTile;
         blocks = (n * p.group + ROWS - 1) / ROWS;
         runs = ((uint32_t)blocks + p.members - 1) / p.members;
     }
-    // place in the table of the cached token numbered u
-    __device__ __forceinline__ int position(int u) const { return u < sinks ? u : u - sinks + from; }
     __device__ __forceinline__ int steps(const Params &p) const { return p.heads * runs * tiles; }
 };
 
@@ -515,53 +502,16 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         constexpr std::integral_constant<int, 2 * D> bf16_row{};
         const int2 cache_place = place(cache_row);
 
-        // tiles that every row sees whole need no mask
-        const int edge = p.window > 0 ? sq.sinks + sq.n - 1 : 0;  // (n - 1: no row is deeper)
-        auto needs_mask = [&](int base, uint64_t there) {
-            return ~there != 0 || base + kTile > sq.cached || (base < edge && base + kTile > sq.sinks);
-        };
+        const int edge = sq.edge(p.window, sq.n);  // (tiles that every row sees whole need no mask)
         auto make_masks = [&](int base, uint64_t there) {
             const Params &p = arguments();
             for (int i = fresh(tid); i < Z::kRows; i += Z::kThreads) {
                 const int r = row0 + i, node = node_of(p, r);
                 uint64_t bits = 0;
-                if (r < rows) {
-                    auto below = [](int64_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
-                    int depth = node;
-                    uint64_t line = 0;
-                    if (parents && sq.n <= kNodes) {
-                        line = lines[node];
-                        depth = __popcll(line) - 1;
-                    } else if (parents && p.window > 0) {
-                        depth = 0;
-                        for (int i = parent_of(node); i >= 0; i = parent_of(i)) ++depth;
-                    }
-                    const int64_t at = (int64_t)sq.len + depth;
-                    bits = below((int64_t)sq.cached - base);
-                    if (p.window > 0) {
-                        const int64_t old = sq.sinks + max(at - p.window + 1 - sq.from, (int64_t)0);
-                        bits &= ~below(old - base) | below((int64_t)sq.sinks - base);
-                    }
-                    const int far = p.window > 0 ? p.window : INT32_MAX;            // ancestors nearer than that
-                    const int64_t sunk = p.window > 0 ? (int64_t)p.sinks - sq.len : 0;  // depths below are sinks
-                    const int64_t off = (int64_t)sq.cached - base;                  // bit of the sequence's first row
-                    if (parents && sq.n <= kNodes) {
-                        // a path's nodes ascend with their depths
-                        uint64_t near = line, deep = line;
-                        for (int k = depth + 1 - far; k > 0; --k) near &= near - 1;
-                        for (int k = 0; k < sunk && deep; ++k) deep &= deep - 1;
-                        line = near | (line & ~deep);
-                        bits |= off >= 0 ? line << off : off > -64 ? line >> -off : 0;
-                    } else if (!parents) {
-                        line = below(off + node + 1) & ~below(off);
-                        bits |= line & (~below(off + (int64_t)node - far + 1) | below(off + sunk));
-                    } else {
-                        int d = 0;
-                        for (int i = node; i >= 0 && off + i >= 0; i = parent_of(i), ++d)
-                            if (off + i < 64 && (d < far || depth - d < sunk)) bits |= 1ull << (off + i);
-                    }
-                    bits &= there;
-                }
+                if (r < rows)
+                    bits = there & (!parents         ? sq.chain(p.window, p.sinks, base, node)
+                                    : sq.n <= kNodes ? sq.path(p.window, p.sinks, base, lines[node])
+                                                     : sq.walk(p.window, p.sinks, base, node, parent_of));
                 masks[i] = bits;
             }
         };
@@ -804,7 +754,7 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
             const uint64_t there = locate(base, limit);
             if (tid == 0) seen[i & (2 * SLOTS - 1)] = there;
             const uint32_t bit = 1u << (i & (2 * SLOTS - 1));
-            masked = needs_mask(base, there) ? masked | bit : masked & ~bit;
+            masked = sq.needs_mask(edge, base, there) ? masked | bit : masked & ~bit;
         };
         // loads of a part, one piece at a time between `steps` groups of matrix instructions
         auto loading = [&](bool any, uint64_t from, uint32_t to) {
