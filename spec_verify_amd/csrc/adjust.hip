@@ -13,6 +13,7 @@
 //   512 rows of 8, histories of 4096    113 us    4.5 TB/s, 94% of a copy
 #include <algorithm>
 
+#include "svq_pack.h"
 #include "svq_tree.h"
 
 namespace svq {
@@ -41,13 +42,6 @@ struct Params {
     int64_t items;
     int M, S, V, range, ranges, groups;
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 v = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
 
 __global__ __launch_bounds__(kThreads) void adjust_kernel(const Params p) {
     __shared__ __attribute__((aligned(16))) uint32_t table[kMostRange + 8];

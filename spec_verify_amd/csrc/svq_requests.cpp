@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "svq_check.h"
 #include "svq_requests.h"
 
 using namespace svq;
@@ -14,13 +15,6 @@ using namespace svq;
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 24;  // per dimension
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb + nb && pb < pa + na;
-}
 
 int check_adapter_shape(int64_t M, int64_t N, int64_t K, int32_t R, int32_t slots) {
     // x and y as in the GEMMs: below 2^31 bytes each
@@ -36,31 +30,6 @@ int check_adapter_shape(int64_t M, int64_t N, int64_t K, int32_t R, int32_t slot
 
 int check_sample_shape(int64_t M, int64_t V) {
     return M > 0 && V > 0 && M <= kMaxDim && V <= kMaxDim ? SVQ_OK : SVQ_ERR_DIM;
-}
-
-// Whether N columns from `a` on and N columns from `b` on, of a matrix of 2-byte elements with
-// row stride ld that holds both, share none (both are 16-byte aligned).
-bool columns_apart(const void *a, const void *b, int64_t ld, int64_t N) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    const int64_t q = (int64_t)((pa < pb ? pb - pa : pa - pb) / 2 % (uintptr_t)ld);
-    return q >= N && q + N <= ld;
-}
-
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-// Whether any of `outs` overlaps another of them or any of `ins` (null entries are skipped).
-bool any_overlap(const Span *outs, int no, const Span *ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        if (!outs[i].p) continue;
-        for (int j = i + 1; j < no; ++j)
-            if (outs[j].p && overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
-        for (int j = 0; j < ni; ++j)
-            if (ins[j].p && overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
-    }
-    return false;
 }
 
 }  // namespace
@@ -85,18 +54,18 @@ int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void
         return SVQ_ERR_ALIGN;
     const AdapterPlan plan = plan_adapter(M, N, K, R, slots);
     if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)) return SVQ_ERR_WORKSPACE;
-    const size_t base_bytes = ((size_t)(M - 1) * ld_base + N) * 2;
+    const Span base_span = {base, ((size_t)(M - 1) * ld_base + N) * 2};
     const Span outs[] = {{out, ((size_t)(M - 1) * ld_out + N) * 2}, {workspace, plan.workspace_bytes}};
     const Span ins[] = {{x, (size_t)M * K * 2},
                         {a, (size_t)slots * R * K * 2},
                         {b, (size_t)slots * N * R * 2},
                         {rows, (size_t)M * 4},
                         {scales, (size_t)slots * 4}};
-    if (any_overlap(outs, 2, ins, 5) || overlap(workspace, plan.workspace_bytes, base, base_bytes)) return SVQ_ERR_OVERLAP;
+    if (any_overlap(outs, 2, ins, 5) || overlap(outs[1], base_span)) return SVQ_ERR_OVERLAP;
     // in place is the same rows in the same places, or other columns of the same matrix; anything
     // else between base and out must be apart
     if (!(out == base && ld_out == ld_base) && !(ld_out == ld_base && columns_apart(base, out, ld_base, N)) &&
-        overlap(out, outs[0].bytes, base, base_bytes))
+        overlap(outs[0], base_span))
         return SVQ_ERR_OVERLAP;
     return launch_adapter_add(plan, base, ld_base, x, a, b, rows, scales, out, ld_out, M, N, K, R, slots, workspace,
                               (hipStream_t)stream) == hipSuccess

@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "svq_check.h"
 #include "svq_requests.h"
 
 using namespace svq;
@@ -15,30 +16,6 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 24;     // per dimension
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of a sequence
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(const Span &a, const Span &b) {
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
-    return pa < pb + b.bytes && pb < pa + a.bytes;
-}
-
-// Whether any of `outs` overlaps another of them or any of `ins` (null entries are skipped).
-bool any_overlap(const Span *outs, int no, const Span *ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        if (!outs[i].p) continue;
-        for (int j = i + 1; j < no; ++j)
-            if (outs[j].p && overlap(outs[i], outs[j])) return true;
-        for (int j = 0; j < ni; ++j)
-            if (ins[j].p && overlap(outs[i], ins[j])) return true;
-    }
-    return false;
-}
 
 int check_attention_shape(int64_t M, int64_t S, int32_t H, int32_t KVH, int32_t D) {
     if (M <= 0 || S <= 0 || H <= 0 || KVH <= 0 || M > kMaxDim || S > kMaxDim || H > 65536 || KVH > H ||

@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "svq_dma.h"
+#include "svq_pack.h"
 #include "svq_tree.h"
 #include "svq_tree_sight.h"
 
@@ -153,13 +154,6 @@ __device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
 __device__ __forceinline__ uint4 decode8(uint32_t a, uint32_t b) {
     return make_uint4(e4m3_pair_scaled<false>(a, 1.f), e4m3_pair_scaled<true>(a, 1.f), e4m3_pair_scaled<false>(b, 1.f),
                       e4m3_pair_scaled<true>(b, 1.f));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 v = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 // The largest over the four 16-lane rows of a wave, for each lane of a row.
