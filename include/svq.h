@@ -516,9 +516,10 @@ size_t svq_tree_attention_workspace_bytes(int64_t M, int64_t S, int32_t H, int32
  *   columns used. D is 64, 128 or 256, H a multiple of KVH, H <= 65536.
  *   workspace  at least svq_tree_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *              not cleared; as for svq_adapter_add.
- * out and the workspace must not overlap any input or each other. KVH times the tiles of 64
- * tokens that a sequence may have (max_pages * page_size and M) times the blocks of 16
- * (row, head of a group) pairs must stay below 2^31 (SVQ_ERR_DIM).
+ * out and the workspace must not overlap any input or each other (out, q, k and v may be
+ * different columns of one matrix). KVH times the tiles of 64 tokens that a sequence may have
+ * (max_pages * page_size and M) times the blocks of 16 (row, head of a group) pairs must stay
+ * below 2^31 (SVQ_ERR_DIM).
  */
 int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
                        const svq_kv_cache *cache, const int32_t *starts, const int32_t *parents, float scale,
@@ -560,8 +561,8 @@ typedef struct svq_adjustments {
  * 1 / r, rounded to fp32. A logit that nothing applies to keeps its bits. Tokens outside
  * [0, V) are passed over. Rows outside every sequence are left as they were.
  *   logits   bf16 [M][ld], the first V of each row; 2-byte aligned
- *   out      bf16 [M][ld_out]; may be logits itself (same pointer and stride), and must
- *            otherwise not overlap any input
+ *   out      bf16 [M][ld_out]; may be logits itself (same pointer and stride) or other columns
+ *            of the same matrix, and must otherwise not overlap any input
  */
 int svq_adjust_logits(const void *logits, int64_t ld, const int32_t *starts, const svq_adjustments *adjustments,
                       void *out, int64_t ld_out, int64_t M, int64_t S, int64_t V, void *stream);

@@ -30,12 +30,13 @@ inline bool any_overlap(const Span *outs, int no, const Span *ins, int ni) {
     return false;
 }
 
-// Whether N columns from `a` on and N columns from `b` on, of a matrix of 2-byte elements with
-// row stride ld that holds both, share none (both are 2-byte aligned).
-inline bool columns_apart(const void *a, const void *b, int64_t ld, int64_t N) {
+// Whether na columns from `a` on and nb columns from `b` on, of a matrix of 2-byte elements with
+// row stride ld that holds both, share none (both are 2-byte aligned). Their rows alternate in memory.
+inline bool columns_apart(const void *a, int64_t na, const void *b, int64_t nb, int64_t ld) {
     const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    const int64_t q = (int64_t)((pa < pb ? pb - pa : pa - pb) / 2 % (uintptr_t)ld);
-    return q >= N && q + N <= ld;
+    if (pb < pa) return columns_apart(b, nb, a, na, ld);
+    const int64_t q = (int64_t)((pb - pa) / 2 % (uintptr_t)ld);
+    return q >= na && q + nb <= ld;
 }
 
 }  // namespace svq

@@ -64,7 +64,7 @@ int svq_adapter_add(const void *base, int64_t ld_base, const void *x, const void
     if (any_overlap(outs, 2, ins, 5) || overlap(outs[1], base_span)) return SVQ_ERR_OVERLAP;
     // in place is the same rows in the same places, or other columns of the same matrix; anything
     // else between base and out must be apart
-    if (!(out == base && ld_out == ld_base) && !(ld_out == ld_base && columns_apart(base, out, ld_base, N)) &&
+    if (!(out == base && ld_out == ld_base) && !(ld_out == ld_base && columns_apart(base, N, out, N, ld_base)) &&
         overlap(outs[0], base_span))
         return SVQ_ERR_OVERLAP;
     return launch_adapter_add(plan, base, ld_base, x, a, b, rows, scales, out, ld_out, M, N, K, R, slots, workspace,

@@ -86,9 +86,13 @@ int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
     if (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)) return SVQ_ERR_WORKSPACE;
     auto rows = [&](int64_t ld, int64_t cols) { return ((size_t)(M - 1) * ld + cols) * 2; };
     const Span outs[] = {{out, rows(ld_out, qc)}, {workspace, plan.workspace_bytes}};
-    const Span ins[] = {{q, rows(ld_q, qc)},
-                        {k, rows(ld_k, kc)},
-                        {v, rows(ld_v, kc)},
+    // (q, k and v may be other columns of the matrix that out is in)
+    auto beside = [&](const void *p, int64_t ld, int64_t cols) {
+        return Span{ld == ld_out && columns_apart(p, cols, out, qc, ld) ? nullptr : p, rows(ld, cols)};
+    };
+    const Span ins[] = {beside(q, ld_q, qc),
+                        beside(k, ld_k, kc),
+                        beside(v, ld_v, kc),
                         {c.k, kb},
                         {c.v, vb},
                         {starts, (size_t)(S + 1) * 4},
@@ -98,6 +102,8 @@ int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
                         {c.k_scale, (size_t)KVH * 4},
                         {c.v_scale, (size_t)KVH * 4}};
     if (any_overlap(outs, 2, ins, 11)) return SVQ_ERR_OVERLAP;
+    const Span chunk[] = {{q, rows(ld_q, qc)}, {k, rows(ld_k, kc)}, {v, rows(ld_v, kc)}};
+    if (any_overlap(outs + 1, 1, chunk, 3)) return SVQ_ERR_OVERLAP;
     return launch_tree_attention(plan, q, ld_q, k, ld_k, v, ld_v, c, starts, parents, scale, window, sinks, out, ld_out, M,
                                  S, H, KVH, D, workspace, (hipStream_t)stream) == hipSuccess
                ? SVQ_OK
@@ -143,7 +149,8 @@ int svq_adjust_logits(const void *logits, int64_t ld, const int32_t *starts, con
     for (int i = 1; i < 15; ++i)
         if (!aligned(ins[i].p, 4)) return SVQ_ERR_ALIGN;
     const Span outs[] = {{out, ((size_t)(M - 1) * ld_out + V) * 2}};
-    const bool in_place = out == logits && ld_out == ld;
+    // (in place, or other columns of one matrix)
+    const bool in_place = ld_out == ld && (out == logits || columns_apart(logits, V, out, V, ld));
     if (any_overlap(outs, 1, in_place ? ins + 1 : ins, in_place ? 14 : 15)) return SVQ_ERR_OVERLAP;
     return launch_adjust_logits(logits, ld, starts, a, out, ld_out, M, S, V, device_cus(), (hipStream_t)stream) == hipSuccess
                ? SVQ_OK

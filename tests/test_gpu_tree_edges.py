@@ -1,0 +1,66 @@
+"""GPU: calls of the operators of a tree of drafts that stand at the ends of what their
+documentation allows."""
+import os
+
+import numpy as np
+import pytest
+
+import tree_reference as ref
+import test_gpu_adjust_logits as logits
+from test_gpu_tree_attention import Problem, _say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm GPU (torch.cuda.is_available() is False)")
+    import spec_verify_amd as svq
+    if not os.path.exists(svq.library_path):
+        from spec_verify_amd import build
+        build.build()
+    svq.lib()
+    yield
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16).cpu()
+
+
+@pytest.mark.parametrize("rows,H,D", [([13, 40], 6, 64), ([5], 12, 256), ([64, 30], 4, 128)])
+def test_attention_into_other_columns_of_the_projections_matrix(rows, H, D):
+    """One matrix holds q, k, v and out side by side."""
+    _say("beside", rows, H, D)
+    p = Problem(41, rows, [300, 70][:len(rows)], H=H, G=2, D=D)
+    want = _bits(p.call())
+    M, G = len(p.q), 2
+    for order in ("qkvo", "oqkv", "kovq"):
+        parts = dict(q=p.q, k=p.k, v=p.v, o=torch.full((M, H, D), 7.0).bfloat16())
+        wide = torch.cat([parts[c].reshape(M, -1) for c in order], 1).cuda()
+        cols = dict(zip(order, wide.split([parts[c].shape[1] * D for c in order], 1)))
+        view = {c: x.view(M, -1, D) for c, x in cols.items()}
+        p.call(q=view["q"], k=view["k"], v=view["v"], out=view["o"])
+        assert torch.equal(_bits(view["o"]), want), order
+        for c in "qkv":
+            assert torch.equal(_bits(view[c]), _bits(parts[c])), (order, c)
+
+
+@pytest.mark.parametrize("V,apart", [(1000, 1000), (1001, 1001), (1001, 1010), (77, 80), (40000, 40001)])
+def test_adjusted_logits_into_other_columns_of_their_matrix(V, apart):
+    _say("beside", V, apart)
+    p = logits.Problem(42, [5, 9], [60, 20], V, biases=10, masks=2)
+    want = _bits(p.call())
+    M = len(p.logits)
+    for first, second in ((0, apart), (apart, 0)):
+        wide = torch.full((M, apart + V + 3), 3.0, dtype=torch.bfloat16, device="cuda")
+        src, out = wide[:, first:first + V], wide[:, second:second + V]
+        src.copy_(p.logits)
+        p.call(src, out=out)
+        assert torch.equal(_bits(out), want)
+        assert torch.equal(_bits(src), _bits(p.logits))
+        for c in (src, out):
+            c.fill_(3.0)
+        assert (wide == 3.0).all()
