@@ -72,7 +72,7 @@ int svq_tree_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
         return SVQ_ERR_DIM;
     // steps (a tile of 64 tokens, a run of blocks of 16 rows or more) are counted in 31 bits
     const int64_t tiles = ((int64_t)c.max_pages * c.page_size + M) / 64 + 2, runs = M * (H / KVH) / 16 + S;
-    if (tiles > (int64_t(1) << 31) / KVH / runs) return SVQ_ERR_DIM;
+    if (tiles > INT32_MAX / KVH / runs) return SVQ_ERR_DIM;
     const int64_t size = c.type == SVQ_CACHE_E4M3 ? 1 : 2;
     size_t kb, vb;
     if ((st = check_strides(c.k_strides, c, KVH, D, size, &kb)) != SVQ_OK) return st;

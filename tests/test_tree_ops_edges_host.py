@@ -63,3 +63,11 @@ def test_adjusted_logits_that_share_columns_are_refused(L, at, ld, side):  # noq
     """out's 1000 columns begin `at` behind the logits' 1000, or before: some columns are both's."""
     a, b = (P[13], P[13] + 2 * at) if side > 0 else (P[13] + 2 * at, P[13])
     assert _adjust(L, logits=a, ld=ld, out=b, ldo=ld if at else ld - 8) == 7
+
+
+@pytest.mark.parametrize("pages,status", [((1 << 24) - 3, 8), ((1 << 24) - 2, 2)])
+def test_steps_stay_below_31_bits(L, pages, status):  # noqa: F811
+    """128 heads, one row, pages of a tile: 2^24 tiles would be 2^31 steps, one more than are counted. (Without a
+    workspace, what is otherwise valid ends with status 8.)"""
+    assert _attend(L, ws=None, M=1, S=1, H=128, G=128, D=64, ldq=8192, ldk=8192, ldv=8192, ldo=8192, page_size=64,
+                   max_pages=pages, ld_table=pages, k0=1 << 19, k1=8192, k2=64, v0=1 << 19, v1=8192, v2=64) == status
