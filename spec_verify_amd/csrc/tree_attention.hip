@@ -361,14 +361,15 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         }
         float own = p.scale, ks, vs = 1.f;
         if (!(own > 0.f)) {
-            // a scale that is not positive goes into q: the largest score is then the largest product's
-            const uint32_t keep = own < 0.f ? ~0u : own == 0.f ? 0u : ~0u, turn = own < 0.f ? 0x80008000u : 0u;
+            // a scale that is not positive goes into q, as -1 or 0: the largest score is then the largest
+            // product's (and 0 times an infinity is NaN)
+            const float by = own < 0.f ? -1.f : own == 0.f ? 0.f : 1.f;
+            auto scaled = [&](uint32_t x) { return pack_bf16(bits_f32(x << 16) * by, bits_f32(x & 0xFFFF0000u) * by); };
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    qf[rt][c] = make_uint4((qf[rt][c].x ^ turn) & keep, (qf[rt][c].y ^ turn) & keep, (qf[rt][c].z ^ turn) & keep,
-                                           (qf[rt][c].w ^ turn) & keep);
+                    qf[rt][c] = make_uint4(scaled(qf[rt][c].x), scaled(qf[rt][c].y), scaled(qf[rt][c].z), scaled(qf[rt][c].w));
             own = own < 0.f ? -own : own == 0.f ? 1.f : own;
         }
         ks = own;

@@ -64,3 +64,18 @@ def test_adjusted_logits_into_other_columns_of_their_matrix(V, apart):
         for c in (src, out):
             c.fill_(3.0)
         assert (wide == 3.0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_infinities_and_nan_in_q_at_a_scale_of_zero(e4m3):
+    """0 times an infinite or undefined product is NaN, and the other rows and heads weigh everything alike."""
+    p = Problem(43, [20, 9], [200, 64], H=4, G=2, D=64, e4m3=e4m3)
+    p.q[3, 1, 5], p.q[7, 0, 63], p.q[25, 3, 0] = float("inf"), float("-inf"), float("nan")
+    hit = np.zeros(p.q.shape[:2], dtype=bool)
+    hit[3, 1] = hit[7, 0] = hit[25, 3] = True
+    for scale in (0.0, -0.0):
+        _say("scale", scale)
+        got = p.call(scale=scale).double().cpu().numpy()
+        want, bound, _ = p.expected(scale=scale)
+        assert np.isnan(want[hit]).all() and np.isnan(got[hit]).all()
+        assert (np.abs(got - want) <= bound)[~hit].all()
