@@ -34,6 +34,7 @@
 //   16 x 24 rows, window 2000, D = 128, 20 heads 43 us    34 in 8 steps a workgroup between prologue and
 //                                                         parts, 10 of join
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "svq_dma.h"
@@ -374,7 +375,11 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
         }
         ks = own;
         if (E4M3) {
-            if (p.k.scale) ks *= p.k.scale[h];
+            if (p.k.scale) {
+                // (a product that fp32 does not hold is not 0: what is masked, -inf, would be NaN)
+                ks *= p.k.scale[h];
+                ks = ks < FLT_MIN ? FLT_MIN : ks;
+            }
             if (p.v.scale) vs = p.v.scale[h];
         }
         const int cut = E4M3 ? min(t1, sq.cache_tiles) : t1;  // tiles past it hold the chunk's rows alone

@@ -79,3 +79,14 @@ def test_infinities_and_nan_in_q_at_a_scale_of_zero(e4m3):
         want, bound, _ = p.expected(scale=scale)
         assert np.isnan(want[hit]).all() and np.isnan(got[hit]).all()
         assert (np.abs(got - want) <= bound)[~hit].all()
+
+
+@pytest.mark.parametrize("scale,by", [(1e-30, 1e-30), (1e-20, 1e-25), (-1e-30, 1e-30), (1e-30, 0.01)])
+def test_scales_whose_product_32_bits_do_not_hold(scale, by):
+    """The caller's scale times the keys' is 0 in fp32: all that a row sees weighs alike, the rest nothing."""
+    p = Problem(44, [20, 9], [200, 64], H=4, G=2, D=64, e4m3=True)
+    p.scales[0] = torch.full((2,), by)
+    _say("scales", scale, by)
+    got = p.call(scale=scale).double().cpu().numpy()
+    want, bound, _ = p.expected(scale=scale)
+    assert (np.abs(got - want) <= bound).all()
