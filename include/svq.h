@@ -503,8 +503,10 @@ size_t svq_tree_attention_workspace_bytes(int64_t M, int64_t S, int32_t H, int32
  * keys and values are rows beside q, not in the cache: what is accepted is written to
  * the cache afterwards. A score of -inf has weight zero; a row that sees nothing, or
  * only such scores, is zero. Rows outside every sequence are left as they were. What a
- * row does not see, infinities and NaN too, does not change its result. With starts that
- * do not ascend nothing is written.
+ * row does not see, infinities and NaN too, does not change its result. What it sees does,
+ * whatever its weight: a value that is infinite or NaN leaves its column of the row infinite
+ * or NaN. (Which of the two follows IEEE sums where its weight is in fp32's range; where it is
+ * smaller, or 0, it may be either.) With starts that do not ascend nothing is written.
  * Scores, weights' sums and products are fp32; weights enter the second product as bf16;
  * out is rounded to bf16 (nearest even).
  *   q        bf16 [M][ld_q], the first H*D of each row: H heads of D elements

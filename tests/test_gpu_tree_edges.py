@@ -90,3 +90,54 @@ def test_scales_whose_product_32_bits_do_not_hold(scale, by):
     got = p.call(scale=scale).double().cpu().numpy()
     want, bound, _ = p.expected(scale=scale)
     assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("rows,length,H,D,tree", [([1], 1500, 2, 64, False), ([5], 20000, 4, 128, False), ([16, 40], 700, 4, 64, True),
+                                                  ([24], 2500, 6, 256, True), ([3, 2], 20, 2, 64, True)])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_infinite_and_undefined_values_whatever_their_weight(rows, length, H, D, tree, e4m3):
+    """A seen value that is infinite or NaN leaves its column of the row infinite or NaN, though its weight is
+    less than fp32 holds or 0, wherever it stands among masked tiles, whole ones and parts; other columns are as
+    if it were finite."""
+    p = Problem(45, rows, [length] * len(rows), H=H, G=2, D=D, e4m3=e4m3, tree=tree)
+    n = len(rows)
+    places = sorted({0, 1, length // 3, length // 2, length - 2, length - 1})
+    p.q[:] = p.q.abs() + 0.5
+    # the token that takes all the weight: the scores of others are hundreds of powers of two below
+    for peak in (places[1], places[-2], None):
+        keys = p.caches[0].clone()
+        for s in range(n):
+            if peak is not None:
+                keys[p.table[s, peak // p.page], peak % p.page] = 400.0 if e4m3 else 100.0
+            elif not e4m3:  # scores of -inf
+                for j in places:
+                    keys[p.table[s, j // p.page], j % p.page] = float("-inf")
+        keep, p.caches[0] = p.caches[0], keys
+        want, bound, _ = p.expected()
+        p.caches[0] = keep
+        odd = [i for i, j in enumerate(places) if j != peak]
+        fine = [i for i in range(D) if i not in odd]
+        for x in [float("nan")] if e4m3 else [float("inf"), float("-inf"), float("nan")]:
+            values = p.caches[1].clone()
+            for i in odd:
+                j = places[i]
+                for s in range(n):
+                    values[p.table[s, j // p.page], j % p.page, :, i] = x
+            _say("values of", x, "peak", peak, "at", places)
+            got = p.call(k_cache=keys.cuda(), v_cache=values.cuda()).double().cpu().numpy()
+            assert not np.isfinite(got[:, :, odd]).any()
+            assert (np.abs(got - want) <= bound)[:, :, fine].all()
+
+
+def test_a_row_that_sees_scores_of_minus_infinity_alone():
+    """Zero where the values are finite; a column with an infinite or undefined one is not."""
+    for rows, length in (([3], 70), ([5], 3000), ([1], 64)):
+        p = Problem(46, rows, [length], H=2, G=1, tree=False)
+        p.q[:] = p.q.abs() + 0.1
+        p.caches[0][:] = float("-inf")
+        p.k[:] = float("-inf")
+        p.caches[1][p.table[0, 1], 3, 0, 7] = float("inf")
+        got = p.call().float().cpu()
+        assert not torch.isfinite(got[:, :, 7]).any()
+        got[:, :, 7] = 0
+        assert (got == 0).all()
