@@ -566,7 +566,12 @@ __global__ __launch_bounds__((64 * WR * WK), 1) void attend_kernel(const Params)
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        // their weights, for all waves of the group
+        // Their weights, for all waves of the group: summed in fp32, rounded to bf16 (off by 2^-8 of each
+        // at most) for a second product at one matrix instruction's cost, since values are bf16. Results
+        // are then 0.0023 to 0.0024 of their norm off, of which the result's own rounding is 0.0017. As two
+        // bf16 parts, which keep 16 bits, they would be 0.0017 off, but double the second product: 5 rows over
+        // 65000 66.5 us for 64.4, 8-bit batch 152 for 139, window 45.2 for 41.7, 4 x 200 rows at D = 128 93 for
+        // 83, and blocks of 128 rows at D = 256 have no LDS for them.
         auto weigh = [&](float to2, bool masked) {
             const int l = fresh(lane), col = l & 15, quad = l >> 4;
 #pragma unroll

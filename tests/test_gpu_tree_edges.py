@@ -141,3 +141,29 @@ def test_a_row_that_sees_scores_of_minus_infinity_alone():
         assert not torch.isfinite(got[:, :, 7]).any()
         got[:, :, 7] = 0
         assert (got == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (5, 2)])
+def test_a_pool_of_no_pages_and_a_table_of_none(e4m3, window, sinks):
+    """Rows see their paths alone, whatever the lengths say; with a table there is nothing that it could name."""
+    p = Problem(47, [9, 70, 1], [50, 0, 3], H=4, G=2, D=64, e4m3=e4m3, window=window, sinks=sinks)
+    none = [c[:0] for c in p.caches]
+    _say("no pages", window, sinks)
+    named = p.call(k_cache=none[0].cuda(), v_cache=none[1].cuda())   # lengths count, for a window too
+    p.table[:] = -1
+    assert torch.equal(_bits(named), _bits(p.call()))
+    p.check("a table that names nothing", named, overall=False)
+    bare = p.call(k_cache=none[0].cuda(), v_cache=none[1].cuda(), page_table=p.table[:, :0])
+    p.lengths[:] = 0
+    p.check("no table", bare, overall=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,lengths", [([100, 300], [2000, 130]), ([64, 20], [4000, 90])])
+def test_missing_pages_before_wide_trees(rows, lengths, e4m3):
+    """Tiles with tokens that are not there, far before the chunk's rows."""
+    p = Problem(48, rows, lengths, H=2, G=1, D=64, e4m3=e4m3)
+    p.table[0, 3::7] = -1
+    p.table[1, 1] = len(p.caches[0])
+    p.check(f"missing pages, {rows}")
