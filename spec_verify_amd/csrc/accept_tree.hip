@@ -4,7 +4,7 @@
 // samples are read once, ahead of the walk, where the sequence has at most 64 * kKept.
 //
 // Latency: one trip to memory for starts, one for the rows, then registers alone. 1 tree of 8
-// rows 2.7 us, 32 of 64 rows 4.8, 2048 of 1 to 32 rows 6.0 (the call costs the host 11.7).
+// rows 2.9 us, 32 of 64 rows 4.3, 2048 of 1 to 32 rows 5.9 (the call costs the host 11.7).
 #include "svq_tree.h"
 
 namespace svq {

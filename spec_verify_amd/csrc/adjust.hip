@@ -7,10 +7,10 @@
 // and streams the row's logits past them; the next row's are loaded meanwhile.
 //
 // Bound by the logits' way in and out. Measured (V = 248320; replayed):
-//   1 row behind 1500 tokens              7.2 us  latency of one workgroup: history, row, stores
-//   128 rows of 32, histories of 8192    39.9 us  3.2 TB/s: each of the 16 ranges reads the history again,
+//   1 row behind 1500 tokens              6.0 us  latency of one workgroup: history, row, stores
+//   128 rows of 32, histories of 8192    38.7 us  3.4 TB/s: each of the 16 ranges reads the history again,
 //                                                 and has 4 rows to spread that over
-//   512 rows of 8, histories of 4096    113 us    4.5 TB/s, 94% of a copy
+//   512 rows of 8, histories of 4096    111 us    4.6 TB/s, 95% of a copy
 #include <algorithm>
 
 #include "svq_pack.h"

@@ -22,16 +22,17 @@
 // different lengths keep the chip equally busy. A block of rows that ends up in several
 // workgroups is joined by a second launch from its parts' maxima, sums and fp32 values.
 //
-// Measured (24 query heads on 4 key heads, D = 256; both launches, replayed):
-//   1 row over 1500 tokens                       16.4 us  latency: 11.7 (lengths 0.8, shares 0.5, q 1,
+// Measured (24 query heads on 4 key heads, D = 256; both launches, replayed at clocks that 0.3 s of the same
+// have settled: the first launches after a pause are slower, those of 32 x 64 rows by up to a fifth):
+//   1 row over 1500 tokens                       15.4 us  latency: 11.7 (lengths 0.8, shares 0.5, q 1,
 //                                                         first tiles 2.4, steps and sums) and the join 4
-//   5 rows over 65000                            66.4 us  the cache at 4.0 TB/s
-//   32 x 4 rows over 8192, 8-bit cache          147 us    the cache at 3.7 TB/s; decoding to bf16 and the
+//   5 rows over 65000                            63.8 us  the cache at 4.2 TB/s
+//   32 x 4 rows over 8192, 8-bit cache          137 us    the cache at 4.0 TB/s; decoding to bf16 and the
 //                                                         products' issue stand beside the loads
-//   32 x 64 rows over 4096                      365 us    565 TFLOP/s. No unit is full: matrix 28% of
+//   32 x 64 rows over 4096                      367 us    561 TFLOP/s. No unit is full: matrix 27% of
 //                                                         their cycles, LDS 35%, vector 38%; without its
 //                                                         loads 391 of then 399 us, without its products 329
-//   16 x 24 rows, window 2000, D = 128, 20 heads 43 us    34 in 8 steps a workgroup between prologue and
+//   16 x 24 rows, window 2000, D = 128, 20 heads 42 us    31 in 8 steps a workgroup between prologue and
 //                                                         parts, 10 of join
 #include <algorithm>
 #include <cfloat>
