@@ -544,8 +544,8 @@ typedef struct svq_adjustments {
     const int32_t *bias_tokens;    /* int32 [biases] */
     const float *bias_values;      /* fp32 [biases] */
     int64_t biases;
-    const int32_t *allowed;        /* int32 [masks][ld_allowed]: bit v % 32 of word v / 32 is 1 if
-                                      token v may follow */
+    const int32_t *allowed;        /* int32 [masks][ld_allowed], at least one mask: bit v % 32 of word
+                                      v / 32 is 1 if token v may follow */
     int64_t ld_allowed, masks;
     const int32_t *mask_rows;      /* int32 [M]: the mask of each row; outside [0, masks): none */
 } svq_adjustments;

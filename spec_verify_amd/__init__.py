@@ -875,9 +875,9 @@ def adjust_logits(logits, history, lengths, inputs, starts, parents=None, prompt
     starts and parents as for tree_attention. A token that occurs in the history or on a row's path is
     divided (if positive) or multiplied by repetition[s]; frequency[s] per occurrence after
     the prompt and presence[s] once are subtracted; bias = (starts int32 [S + 1], tokens int32,
-    values float32) adds values to the tokens of each sequence; allowed int32 [masks, words]
-    holds a bit per token and mask_rows int32 [M] each row's mask (outside [0, masks):
-    none), a clear bit makes -inf. out may be logits itself; logits and out may be column
+    values float32) adds values to the tokens of each sequence; allowed int32 [masks, words],
+    of at least one mask, holds a bit per token and mask_rows int32 [M] each row's mask (outside
+    [0, masks): none), a clear bit makes -inf. out may be logits itself; logits and out may be column
     slices of wider matrices. Rows outside every sequence are not written.
     """
     kd = _kinds()
